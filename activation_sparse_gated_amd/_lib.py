@@ -1,4 +1,4 @@
-"""ctypes view of the C ABI in include/ffn_sparse.h and include/ffn_gsi.h (no computation here)."""
+"""ctypes view of the C ABI in include/ffn_sparse.h, ffn_gsi.h and ffn_linear.h (no computation here)."""
 from __future__ import annotations
 
 import ctypes
@@ -9,7 +9,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libffn_sparse.so")
 
 FFN_OK, FFN_E_INVALID, FFN_E_UNSUPPORTED, FFN_E_WORKSPACE, FFN_E_HIP = 0, -1, -2, -3, -4
-DTYPES = {"f32": 0, "bf16": 1}
+FFN_F32, FFN_BF16 = 0, 1
+DTYPES = {"f32": FFN_F32, "bf16": FFN_BF16}
 ACTS = {"relu": 0, "silu": 1}
 SELS = {"bias": 0, "thresh": 1, "topk": 2}
 KERNEL_KINDS = {"gate": 0, "lowrank_v": 1, "topk": 2, "updown": 3, "reduce": 4, "fallback": 5, "dense": 6,
@@ -26,6 +27,12 @@ EXPORTS = [
     "ffn_gsi_check_config", "ffn_gsi_workspace_bytes", "ffn_gsi_init", "ffn_gsi_forward",
     "ffn_gsi_dense_forward", "ffn_gsi_image", "ffn_gsi_timing_enable", "ffn_gsi_timing_read",
     "ffn_gsi_destroy",
+]
+LINEAR_EXPORTS = [
+    "ffn_linear_abi_version", "ffn_rmsnorm_forward", "ffn_rmsnorm_backward_workspace_bytes",
+    "ffn_rmsnorm_backward", "ffn_fp8_quantize", "ffn_fp8_linear_workspace_bytes", "ffn_fp8_linear",
+    "ffn_grouped_forward_workspace_bytes", "ffn_grouped_forward", "ffn_grouped_backward_workspace_bytes",
+    "ffn_grouped_backward",
 ]
 GSI_KERNEL_KINDS = {"proj": 0, "resid": 1, "out": 2, "dense": 3}
 
@@ -109,6 +116,21 @@ def load() -> ctypes.CDLL:
         "ffn_gsi_timing_enable": (c_int32, [c_void_p, c_int32, c_int32]),
         "ffn_gsi_timing_read": (c_int32, [c_void_p, c_int32, P(c_int32), P(c_double)]),
         "ffn_gsi_destroy": (None, [c_void_p]),
+        "ffn_linear_abi_version": (c_int32, []),
+        "ffn_rmsnorm_forward": (c_int32, [c_void_p] * 3 + [c_int32] * 3 + [c_float] + [c_void_p] * 5),
+        "ffn_rmsnorm_backward_workspace_bytes": (c_size_t, [c_int32] * 2),
+        "ffn_rmsnorm_backward": (c_int32, [c_void_p] * 4 + [c_int32] * 3 + [c_float, c_void_p, c_void_p, c_int32,
+                                                                           c_void_p, c_size_t, c_void_p]),
+        "ffn_fp8_quantize": (c_int32, [c_void_p] + [c_int32] * 5 + [c_void_p] * 5),
+        "ffn_fp8_linear_workspace_bytes": (c_size_t, [c_int32] * 4),
+        "ffn_fp8_linear": (c_int32, [c_void_p] * 4 + [c_int32] * 4 + [c_void_p, c_int32, c_void_p, c_int32, c_int32,
+                                                                      c_void_p, c_size_t, c_void_p]),
+        "ffn_grouped_forward_workspace_bytes": (c_size_t, [c_int32] * 4),
+        "ffn_grouped_forward": (c_int32, [c_void_p] * 3 + [c_int32] * 4 + [c_void_p, c_int32, c_void_p, c_size_t,
+                                                                           c_void_p]),
+        "ffn_grouped_backward_workspace_bytes": (c_size_t, [c_int32] * 4),
+        "ffn_grouped_backward": (c_int32, [c_void_p] * 4 + [c_int32] * 4 + [c_void_p, c_void_p, c_int32, c_void_p,
+                                                                            c_size_t, c_void_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -1,0 +1,99 @@
+// Device helpers of the operators around the FFN: typed 8-element rows, bf16
+// and e4m3 rounding, the scale of an 8-bit block, the rows of an expert.
+#pragma once
+#include "common.cuh"
+#include "linear.cuh"
+
+namespace ffn {
+
+// Two fp32 values as bf16 bits, rounded to nearest even (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{a, b}), bf2));
+}
+__device__ __forceinline__ float round_bf16(float a) { return __uint_as_float(pack_bf16(a, 0.f) << 16); }
+
+// Eight consecutive elements of a bf16 or fp32 row.
+template <typename T>
+struct Row8;
+template <>
+struct Row8<uint16_t> {
+  uint4 v;
+  __device__ __forceinline__ void load(const void* p, size_t i) { v = ldg16(reinterpret_cast<const uint16_t*>(p) + i); }
+  __device__ __forceinline__ void zero() { v = uint4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void get(float (&f)[8]) const { unpack8(v, f); }
+  __device__ __forceinline__ static void round(float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = round_bf16(f[i]);
+  }
+  __device__ __forceinline__ static void store(void* p, size_t i, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) =
+        uint4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+  }
+};
+template <>
+struct Row8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p, size_t i) {
+    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
+    a = q[0];
+    b = q[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = float4{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  __device__ __forceinline__ static void round(float (&)[8]) {}
+  __device__ __forceinline__ static void store(void* p, size_t i, const float (&f)[8]) {
+    float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
+    q[0] = float4{f[0], f[1], f[2], f[3]};
+    q[1] = float4{f[4], f[5], f[6], f[7]};
+  }
+};
+
+// |v| as ordered bits: a NaN is the largest, so that a maximum keeps it.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t max8(const float (&f)[8], uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
+  return m;
+}
+// Maximum over each 16-lane row of the wave.
+__device__ __forceinline__ uint32_t row16_max(uint32_t m) {
+  m = max(m, (uint32_t)wave_xchg_i<1>((int)m));
+  m = max(m, (uint32_t)wave_xchg_i<2>((int)m));
+  m = max(m, (uint32_t)wave_xchg_i<4>((int)m));
+  m = max(m, (uint32_t)wave_xchg_i<8>((int)m));
+  return m;
+}
+// Scale of a block whose largest magnitude has these bits: max|x| / 448 as one
+// fp32 product, at least 2^-100 (a block of zeros, or of values so small that
+// the reciprocal of its scale would overflow). NaN and infinity pass through.
+__device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
+  const float s = __uint_as_float(amax_bits) * (1.0f / 448.0f);
+  return s < 0x1p-100f ? 0x1p-100f : s;
+}
+// Eight values times inv as e4m3 (round to nearest even; |v * inv| <= 448 (1 + 2^-22)
+// rounds to at most 448).
+__device__ __forceinline__ uint2 fp8_pack8(const float (&f)[8], float inv) {
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0] * inv, f[1] * inv, 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2] * inv, f[3] * inv, lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4] * inv, f[5] * inv, 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6] * inv, f[7] * inv, hi, true);
+  return uint2{(uint32_t)lo, (uint32_t)hi};
+}
+
+// Rows [lo, hi) of expert g, kept inside 0..m whatever the offsets hold.
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int g, int m, int& lo, int& hi) {
+  if (!offsets) {
+    lo = 0;
+    hi = m;
+    return;
+  }
+  lo = min(max(offsets[g], 0), m);
+  hi = max(min(max(offsets[g + 1], 0), m), lo);
+}
+
+}  // namespace ffn

@@ -1,0 +1,292 @@
+"""Python binding of the operators around the FFN (include/ffn_linear.h).
+
+Argument checks and marshalling only: PyTorch provides device memory and the
+current stream of the tensors' device; every step runs in the HIP kernels
+behind the C ABI. Function names follow the C entry points. Tensors are
+contiguous and on one GPU; what does not fit raises ValueError before anything
+is launched. Outputs that are not passed in are allocated.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+from ._lib import FFN_BF16, FFN_F32, check
+
+_DTYPES = {torch.bfloat16: FFN_BF16, torch.float32: FFN_F32}
+FP8 = torch.float8_e4m3fn
+BLOCK = 128
+
+
+@dataclass
+class Fp8Tensor:
+    """A matrix in 8-bit blocks, or one for each expert (layout in the C header):
+    q float8_e4m3fn [..., m, k]; scale fp32 [..., ceil(k/128), m] (block_rows 1)
+    or [..., ceil(m/128), ceil(k/128)] (block_rows 128). A value is q * scale."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    block_rows: int
+
+    def dequantize(self) -> torch.Tensor:
+        """The values in fp32 (elementary torch operations, for inspection)."""
+        m, k = self.q.shape[-2:]
+        s = self.scale.transpose(-1, -2) if self.block_rows == 1 else \
+            self.scale.repeat_interleave(BLOCK, -2)[..., :m, :]
+        return self.q.float() * s.repeat_interleave(BLOCK, -1)[..., :k]
+
+
+def _blocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def _scale_shape(shape, block_rows):
+    *lead, m, k = shape
+    return (*lead, _blocks(k), m) if block_rows == 1 else (*lead, _blocks(m), _blocks(k))
+
+
+def _fail(name, t, want):
+    got = type(t).__name__ if not isinstance(t, torch.Tensor) else \
+        f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}"
+    raise ValueError(f"{name}: expected a contiguous {want}, got {got}")
+
+
+def _check(name, t, dtype, shape, device):
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        _fail(name, t, f"{dtype} {tuple(shape)} on {device}")
+
+
+def _first(name, t, dtypes, ndims):
+    """The tensor that the others are measured by."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() in ndims and t.is_cuda and t.is_contiguous()):
+        _fail(name, t, f"GPU tensor of {' or '.join(map(str, ndims))} dimensions, {' or '.join(map(str, dtypes))}")
+    return t.device
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, device, stream, *args):
+    """The C call on the tensors' own device, on its current stream unless one is given."""
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    check(fn(*args, s.cuda_stream), fn.__name__)
+
+
+def _workspace(workspace, nbytes, device):
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    _check("workspace", workspace, torch.uint8, workspace.shape, device)
+    return workspace
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel()
+
+
+# ---------------------------------------------------------------- RMS norm
+def rmsnorm_forward(x, w, *, residual=None, eps=1e-6, fp8=False, r=None, y=None, stream=None):
+    """RMS norm of the rows of x + residual (ffn_rmsnorm_forward): (y, r).
+
+    x [m, d] bf16 or fp32; w [d]; residual [m, d] or None. r is the sum, which
+    the residual stream goes on with (x itself without a residual; it may be
+    passed as x or residual to be written in place). y is of x's type, or with
+    fp8 an Fp8Tensor of blocks of 1 x 128."""
+    dev = _first("x", x, (torch.bfloat16, torch.float32), (2,))
+    m, d = x.shape
+    _check("w", w, x.dtype, (d,), dev)
+    if residual is not None:
+        _check("residual", residual, x.dtype, x.shape, dev)
+        if r is None:
+            r = torch.empty_like(x)
+    if r is not None:
+        _check("r", r, x.dtype, x.shape, dev)
+    if fp8:
+        if y is None:
+            y = Fp8Tensor(torch.empty((m, d), dtype=FP8, device=dev),
+                          torch.empty((_blocks(d), m), dtype=torch.float32, device=dev), 1)
+        else:
+            _check_fp8("y", y, (m, d), 1, dev)
+        out, q, scale = None, y.q, y.scale
+    else:
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _check("y", y, x.dtype, x.shape, dev)
+        out, q, scale = y, None, None
+    _call(_lib.load().ffn_rmsnorm_forward, dev, stream, _ptr(x), _ptr(residual), _ptr(w), _DTYPES[x.dtype], m, d,
+          float(eps), _ptr(r), _ptr(out), _ptr(q), _ptr(scale))
+    return y, (x if r is None else r)
+
+
+def rmsnorm_backward(r, w, dy, *, dr=None, eps=1e-6, dx=None, dw=None, accumulate=False, workspace=None, stream=None):
+    """Gradients of the norm of the rows r (ffn_rmsnorm_backward): (dx, dw).
+
+    dx [m, d] of r's type is the gradient of x and of the residual, dr (the
+    gradient that reaches r besides) included; dw [d] is fp32, written, or added
+    to with accumulate."""
+    dev = _first("r", r, (torch.bfloat16, torch.float32), (2,))
+    m, d = r.shape
+    _check("w", w, r.dtype, (d,), dev)
+    _check("dy", dy, r.dtype, r.shape, dev)
+    if dr is not None:
+        _check("dr", dr, r.dtype, r.shape, dev)
+    if dx is None:
+        dx = torch.empty_like(r)
+    else:
+        _check("dx", dx, r.dtype, r.shape, dev)
+    dw = _accumulator("dw", dw, accumulate, (d,), dev)
+    lib = _lib.load()
+    workspace = _workspace(workspace, lib.ffn_rmsnorm_backward_workspace_bytes(m, d), dev)
+    _call(lib.ffn_rmsnorm_backward, dev, stream, _ptr(r), _ptr(w), _ptr(dy), _ptr(dr), _DTYPES[r.dtype], m, d,
+          float(eps), _ptr(dx), _ptr(dw), int(bool(accumulate)), _ptr(workspace), _nbytes(workspace))
+    return dx, dw
+
+
+def _accumulator(name, t, accumulate, shape, dev):
+    if t is None:
+        if accumulate:
+            raise ValueError(f"{name}: accumulate needs the tensor that is added to")
+        return torch.empty(shape, dtype=torch.float32, device=dev)
+    _check(name, t, torch.float32, shape, dev)
+    return t
+
+
+# ---------------------------------------------------------------- 8-bit blocks
+def _check_fp8(name, t, shape, block_rows, dev):
+    if not isinstance(t, Fp8Tensor) or t.block_rows != block_rows:
+        raise ValueError(f"{name}: expected an Fp8Tensor of blocks of {block_rows} x {BLOCK}")
+    _check(f"{name}.q", t.q, FP8, shape, dev)
+    _check(f"{name}.scale", t.scale, torch.float32, _scale_shape(shape, block_rows), dev)
+
+
+def fp8_quantize(x, *, block_rows=1, transposed=False, out=None, out_t=None, stream=None):
+    """x [m, k] (or [experts, m, k]), bf16 or fp32, in 8-bit blocks of block_rows
+    (1 or 128) x 128 (ffn_fp8_quantize): an Fp8Tensor, or with transposed a pair
+    of it and the blocks of the transposed matrices [k, m], their rows filled
+    with zeros to a multiple of 16."""
+    dev = _first("x", x, (torch.bfloat16, torch.float32), (2, 3))
+    if block_rows not in (1, BLOCK):
+        raise ValueError(f"block_rows: 1 or {BLOCK}, got {block_rows}")
+    *lead, m, k = x.shape
+    mt = (m + 15) // 16 * 16
+    shape_t = (*lead, k, mt)
+    if out is None:
+        out = Fp8Tensor(torch.empty(x.shape, dtype=FP8, device=dev),
+                        torch.empty(_scale_shape(x.shape, block_rows), dtype=torch.float32, device=dev), block_rows)
+    else:
+        _check_fp8("out", out, x.shape, block_rows, dev)
+    if transposed:
+        if out_t is None:
+            out_t = Fp8Tensor(torch.empty(shape_t, dtype=FP8, device=dev),
+                              torch.empty(_scale_shape(shape_t, block_rows), dtype=torch.float32, device=dev),
+                              block_rows)
+        else:
+            _check_fp8("out_t", out_t, shape_t, block_rows, dev)
+    elif out_t is not None:
+        raise ValueError("out_t: given without transposed")
+    groups = lead[0] if lead else 1
+    if groups:
+        _call(_lib.load().ffn_fp8_quantize, dev, stream, _ptr(x), _DTYPES[x.dtype], groups, m, k, block_rows,
+              _ptr(out.q), _ptr(out.scale), _ptr(out_t.q if transposed else None),
+              _ptr(out_t.scale if transposed else None))
+    return (out, out_t) if transposed else out
+
+
+def fp8_linear(x: Fp8Tensor, w: Fp8Tensor, *, offsets=None, y=None, out_dtype=torch.bfloat16, accumulate=False,
+               workspace=None, stream=None):
+    """y = x w^T of 8-bit blocks (ffn_fp8_linear), [m, n] in out_dtype (bf16 or fp32).
+
+    x: blocks of 1 x 128, [m, k]. w: [n, k], blocks of 128 x 128 or 1 x 128; with
+    offsets (int32 [experts + 1] on the GPU) [experts, n, k], blocks of 128 x 128:
+    rows offsets[e] .. offsets[e + 1] - 1 are expert e's. accumulate adds to an
+    fp32 y."""
+    if not isinstance(x, Fp8Tensor) or not isinstance(w, Fp8Tensor):
+        raise ValueError("x, w: expected Fp8Tensors")
+    dev = _first("x.q", x.q, (FP8,), (2,))
+    m, k = x.q.shape
+    _check_fp8("x", x, (m, k), 1, dev)
+    if w.block_rows not in (1, BLOCK) or (offsets is not None and w.block_rows == 1):
+        raise ValueError(f"w: blocks of {w.block_rows} x {BLOCK} are not taken here")
+    _first("w.q", w.q, (FP8,), (2,) if offsets is None else (3,))
+    *lead, n, _ = w.q.shape
+    _check_fp8("w", w, (*lead, n, k), w.block_rows, dev)
+    groups = lead[0] if lead else 1
+    y = _product_out(y, (m, n), out_dtype, dev, accumulate)
+    _check_offsets(offsets, groups, dev)
+    lib = _lib.load()
+    workspace = _workspace(workspace, lib.ffn_fp8_linear_workspace_bytes(m, n, k, groups), dev)
+    _call(lib.ffn_fp8_linear, dev, stream, _ptr(x.q), _ptr(x.scale), _ptr(w.q), _ptr(w.scale), w.block_rows, m, n, k,
+          _ptr(offsets), groups, _ptr(y), _DTYPES[y.dtype], int(bool(accumulate)), _ptr(workspace), _nbytes(workspace))
+    return y
+
+
+def _product_out(y, shape, out_dtype, dev, accumulate=False):
+    if y is None:
+        if accumulate:
+            raise ValueError("y: accumulate needs the tensor that is added to")
+        if out_dtype not in _DTYPES:
+            raise ValueError(f"out_dtype: bfloat16 or float32, got {out_dtype}")
+        return torch.empty(shape, dtype=out_dtype, device=dev)
+    if accumulate and y.dtype != torch.float32:
+        raise ValueError("y: accumulate needs fp32")
+    _check("y", y, y.dtype if y.dtype in _DTYPES else torch.bfloat16, shape, dev)
+    return y
+
+
+def _check_offsets(offsets, groups, dev):
+    if offsets is not None:
+        _check("offsets", offsets, torch.int32, (groups + 1,), dev)
+
+
+# ---------------------------------------------------------------- products by expert
+def grouped_forward(x, w, offsets, *, y=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """y[t] = W_e x[t] for the rows t of each expert e (ffn_grouped_forward).
+
+    x [m, k] bf16, sorted by expert; w [experts, n, k] bf16; offsets int32
+    [experts + 1] on the GPU: rows offsets[e] .. offsets[e + 1] - 1 are expert
+    e's. y [m, n] in out_dtype (bf16 or fp32); rows of no expert are left as
+    they were."""
+    dev = _first("x", x, (torch.bfloat16,), (2,))
+    _first("w", w, (torch.bfloat16,), (3,))
+    m, k = x.shape
+    groups, n, _ = w.shape
+    _check("w", w, torch.bfloat16, (groups, n, k), dev)
+    _check("offsets", offsets, torch.int32, (groups + 1,), dev)
+    y = _product_out(y, (m, n), out_dtype, dev)
+    lib = _lib.load()
+    workspace = _workspace(workspace, lib.ffn_grouped_forward_workspace_bytes(m, n, k, groups), dev)
+    _call(lib.ffn_grouped_forward, dev, stream, _ptr(x), _ptr(w), _ptr(offsets), groups, m, n, k, _ptr(y),
+          _DTYPES[y.dtype], _ptr(workspace), _nbytes(workspace))
+    return y
+
+
+def grouped_backward(x, w, dy, offsets, *, dx=None, dw=None, accumulate=False, workspace=None, stream=None):
+    """Gradients of grouped_forward (ffn_grouped_backward): (dx, dw).
+
+    dy [m, n] bf16; dx [m, k] bf16, rows of no expert left as they were; dw
+    [experts, n, k] fp32, written (zeros for an expert without rows) or added to
+    with accumulate."""
+    dev = _first("x", x, (torch.bfloat16,), (2,))
+    _first("w", w, (torch.bfloat16,), (3,))
+    m, k = x.shape
+    groups, n, _ = w.shape
+    _check("w", w, torch.bfloat16, (groups, n, k), dev)
+    _check("dy", dy, torch.bfloat16, (m, n), dev)
+    _check("offsets", offsets, torch.int32, (groups + 1,), dev)
+    if dx is None:
+        dx = torch.empty_like(x)
+    else:
+        _check("dx", dx, torch.bfloat16, x.shape, dev)
+    dw = _accumulator("dw", dw, accumulate, (groups, n, k), dev)
+    lib = _lib.load()
+    workspace = _workspace(workspace, lib.ffn_grouped_backward_workspace_bytes(m, n, k, groups), dev)
+    _call(lib.ffn_grouped_backward, dev, stream, _ptr(x), _ptr(w), _ptr(dy), _ptr(offsets), groups, m, n, k, _ptr(dx),
+          _ptr(dw), int(bool(accumulate)), _ptr(workspace), _nbytes(workspace))
+    return dx, dw
