@@ -1,10 +1,24 @@
 // Products of 8-bit blocks and products grouped by expert on gfx950.
 //
-// out[r][c] = sum_j B[r][j] A[c][j], one 128 x 128 tile a workgroup of four
-// waves, each a 64 x 64 quadrant on 16 x 16 MFMA tiles (operand lane l: row
-// l % 16, its contraction elements in group l / 16; accumulator lane l: column
-// 4 (l / 16) + v of the output, row l % 16). A step contracts 128 bytes of a
-// row: one 8-bit block, or 64 bf16 elements.
+// out[r][c] = sum_j B[r][j] A[c][j]: a workgroup of eight waves owns an RT x 256
+// tile of the output (RT rows) and walks the contraction in steps of 128 bytes
+// of a row: one 8-bit block, or 64 bf16 elements. Both operands' slices of the
+// next step travel from memory straight into the other of two LDS stages
+// (16-byte loads to LDS, no registers) while the matrix cores work on this
+// one; one barrier a step. Products run on 16 x 16 MFMA tiles (operand lane l:
+// row l % 16, contraction elements in group l / 16; accumulator lane l:
+// columns 4 (l / 16) + v of the output, row l % 16, so a lane stores four
+// neighbours).
+//
+// LDS layouts, both free of bank conflicts beyond what the instruction width
+// costs. An operand whose rows run along the contraction keeps 128-byte rows,
+// chunk c of 16 bytes at c ^ (row % 8): the 16 rows of a 16-byte operand read
+// fall into different banks. An operand read across its rows (W in dx, both in
+// dW: the contraction is the slower index) keeps the rows as they lie in
+// memory, 64 of them a step, and is transposed on the way to the registers by
+// ds_read_b64_tr_b16; chunk c lies at c ^ f(row), f spreading the 16 rows one
+// such read touches. Loads to LDS write 16 bytes a lane in lane order, so the
+// permutation is applied to the address that is read.
 //
 // How 8-bit products are summed. The e4m3 matrix instructions hold each sum of
 // 8 products (8 consecutive k of a row) to 13 bits below its largest product
@@ -14,31 +28,33 @@
 // rounding of a bf16 output, but not fp32. So an fp32 output (a weight's
 // gradient) is made on the bf16 instructions, at half their rate: every e4m3
 // value is a bf16 value, products of two are exact in fp32, and so are their
-// sums to fp32 roundings.
+// sums to fp32 roundings. A block's sum starts at zero, is scaled in fp32 and
+// added to the accumulator.
+#include <type_traits>
+
 #include "lin_util.cuh"
 
 namespace ffn {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int LT = 128;                          // tile edge
-constexpr int LIN_THREADS = 256;
+constexpr int LIN_THREADS = 512;
+constexpr int LIN_CT = 256;                      // columns of a tile
+constexpr int LIN_BYTES = 128;                   // contraction bytes of a step
 
-__device__ __forceinline__ int lin_slot(int row, int c) { return row * 8 + (c ^ (row & 7)); }
-
-// Tile of this workgroup: expert g, its rows [lo, hi), first output row r0.
-// Row tiles count expert by expert; false past the last one.
-__device__ __forceinline__ bool lin_tile(const LinDesc& d, int tile, int& g, int& lo, int& hi, int& r0) {
-  for (g = 0; g < d.groups; ++g) {
-    expert_rows(d.offsets, g, d.rows, lo, hi);
-    const int t = (hi - lo + LT - 1) / LT;
-    if (tile < t) {
-      r0 = lo + tile * LT;
-      return true;
-    }
-    tile -= t;
-  }
-  return false;
+// 16 (or 4) bytes a lane from global memory to LDS: the wave's lanes in order from `l` on.
+__device__ __forceinline__ void lds_load16(const char* g, void* l) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g, (__attribute__((address_space(3))) void*)l, 16, 0, 0);
+}
+__device__ __forceinline__ void lds_load4(const char* g, void* l) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g, (__attribute__((address_space(3))) void*)l, 4, 0, 0);
+}
+// Every load to LDS and every LDS read of this wave is done, then every wave's.
+__device__ __forceinline__ void lin_sync() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // Eight e4m3 values as bf16 (exact).
@@ -49,156 +65,358 @@ __device__ __forceinline__ bf16x8_t fp8_to_bf16(uint32_t lo, uint32_t hi) {
   return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-template <int KIND, bool EXACT>
+// One operand's slice of a step in LDS: R rows of the output's side.
+// ALONG: rows of 128 bytes along the contraction; otherwise 64 contraction
+// rows of R bf16 elements.
+template <int R, bool ALONG>
+struct LinTile {
+  static constexpr int BYTES = R * LIN_BYTES;
+  static constexpr int LOADS = BYTES / (LIN_THREADS * 16);     // 16-byte loads of a thread
+  static_assert(LOADS >= 1, "tile too small");
+  static constexpr int CPR = ALONG ? 8 : R / 8;                // chunks of an LDS row
+  __device__ __forceinline__ static int swz(int row) { return (ALONG ? row : ((row & 3) << 1) | (row & 8)) & (CPR < 16 ? CPR - 1 : 15); }
+  // load q = i * 512 + thread: LDS chunk q, that is row q / CPR, place q % CPR
+  __device__ __forceinline__ static int row_of(int q) { return q / CPR; }
+  __device__ __forceinline__ static int chunk_of(int q) { return (q % CPR) ^ swz(q / CPR); }
+};
+
+// Where a thread's loads of one operand come from: `base` (uniform) + off[i],
+// `base` moving on by `step` bytes.
+template <int R, bool ALONG, int ESZ>
+struct LinSrc {
+  using T = LinTile<R, ALONG>;
+  const char* base;
+  size_t step;
+  uint32_t off[T::LOADS];
+  // rows r0.. of at most rend rows of p, contraction from k0 on, ld elements apart.
+  // Rows past the end repeat the last one: their results are not stored.
+  __device__ __forceinline__ void init(const char* p, int ld, int r0, int rend, int k0, int tid) {
+    if constexpr (ALONG) {
+      base = p + ((size_t)r0 * ld + k0) * ESZ;
+      step = LIN_BYTES;
+#pragma unroll
+      for (int i = 0; i < T::LOADS; ++i) {
+        const int q = i * LIN_THREADS + tid;
+        off[i] = (uint32_t)min(T::row_of(q), rend - 1 - r0) * (uint32_t)(ld * ESZ) + T::chunk_of(q) * 16;
+      }
+    } else {
+      base = p + ((size_t)k0 * ld + r0) * ESZ;
+      step = (size_t)64 * ld * ESZ;
+#pragma unroll
+      for (int i = 0; i < T::LOADS; ++i) {
+        const int q = i * LIN_THREADS + tid;
+        off[i] = (uint32_t)T::row_of(q) * (uint32_t)(ld * ESZ) + min(T::chunk_of(q) * 8, rend - 8 - r0) * ESZ;
+      }
+    }
+  }
+  __device__ __forceinline__ void load(char* lds, int wave) {
+#pragma unroll
+    for (int i = 0; i < T::LOADS; ++i) lds_load16(base + off[i], lds + (i * LIN_THREADS + wave * 64) * 16);
+    base += step;
+  }
+  // The last, partial step: `left` contraction elements, zeros behind them.
+  __device__ __forceinline__ void load_part(char* lds, int left, int tid) {
+#pragma unroll
+    for (int i = 0; i < T::LOADS; ++i) {
+      const int q = i * LIN_THREADS + tid;
+      const bool ok = ALONG ? T::chunk_of(q) * (16 / ESZ) < left : T::row_of(q) < left;
+      *reinterpret_cast<uint4*>(lds + q * 16) = ok ? ldg16(base + off[i]) : uint4{0, 0, 0, 0};
+    }
+  }
+};
+
+// Tile of this workgroup: expert g, its rows [lo, hi), first output row r0.
+// Row tiles count expert by expert; false past the last one.
+template <int RT>
+__device__ __forceinline__ bool lin_tile(const LinDesc& d, int tile, int& g, int& lo, int& hi, int& r0) {
+  for (g = 0; g < d.groups; ++g) {
+    expert_rows(d.offsets, g, d.rows, lo, hi);
+    const int t = (hi - lo + RT - 1) / RT;
+    if (tile < t) {
+      r0 = lo + tile * RT;
+      return true;
+    }
+    tile -= t;
+  }
+  return false;
+}
+
+template <int KIND, int RT, bool EXACT, bool AROW>
 __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int ctiles, int rtiles) {
   constexpr bool FP8 = KIND == LIN_FP8;
-  constexpr bool ASTR = KIND == LIN_DX || KIND == LIN_DW, BSTR = KIND == LIN_DW;
-  constexpr int ESZ = FP8 ? 1 : 2, CE = 16 / ESZ, BK = 128 / ESZ;
-  __shared__ uint4 s_a[LT * 8], s_b[LT * 8];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wc = wave & 1, wr = wave >> 1;
-  const int ct = blockIdx.x % ctiles, rt = blockIdx.x / ctiles;
-  const int c0 = ct * LT;
+  constexpr bool AALONG = KIND == LIN_FP8 || KIND == LIN_FWD, BALONG = KIND != LIN_DW;
+  constexpr int ESZ = FP8 ? 1 : 2, BK = LIN_BYTES / ESZ;
+  constexpr int WR = RT >= 128 ? 2 : 1, WC = 8 / WR;           // waves along rows and columns
+  constexpr int BT = RT / WR / 16, AT = LIN_CT / WC / 16;      // 16 x 16 tiles of a wave
+  using TA = LinTile<LIN_CT, AALONG>;
+  using TB = LinTile<RT, BALONG>;
+  constexpr int SCALES = FP8 ? (RT + LIN_CT) * 4 : 0;
+  constexpr int STAGE = TA::BYTES + TB::BYTES + SCALES;
+  __shared__ __attribute__((aligned(16))) char smem[2][STAGE];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wc = wave % WC, wr = wave / WC;
+
+  // Workgroups go to the 8 XCDs in turn: each XCD takes a contiguous run of
+  // tiles, so that what its neighbours read is in its L2. Tiles run down
+  // column by column inside bands of 4 row tiles.
+  const int total = ctiles * rtiles, per = (total + 7) / 8;
+  const int lin = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (lin >= total) return;
+  constexpr int BAND = 4;
+  const int band = lin / (BAND * ctiles), inb = lin - band * BAND * ctiles;
+  const int bh = min(BAND, rtiles - band * BAND);
+  const int rt = band * BAND + inb % bh, c0 = inb / bh * LIN_CT;
   int g, lo, hi, r0, klo = 0, khi = d.K, rend;
-  if (KIND == LIN_DW) {
-    g = rt / rtiles;
-    r0 = (rt % rtiles) * LT;
+  if constexpr (KIND == LIN_DW) {
+    const int per_expert = (d.rows + RT - 1) / RT;
+    g = rt / per_expert;
+    r0 = rt % per_expert * RT;
     rend = d.rows;
     expert_rows(d.offsets, g, d.K, klo, khi);
     if (d.accumulate && klo == khi) return;
   } else {
-    if (!lin_tile(d, rt, g, lo, hi, r0)) return;
+    if (!lin_tile<RT>(d, rt, g, lo, hi, r0)) return;
     rend = hi;
   }
   const char* A = reinterpret_cast<const char*>(d.A) + (KIND == LIN_DW ? 0 : (size_t)g * d.a_group * ESZ);
-  const char* B = reinterpret_cast<const char*>(d.B);
-  const float* sa = d.sa;
+  LinSrc<LIN_CT, AALONG, ESZ> sa;
+  LinSrc<RT, BALONG, ESZ> sb;
+  sa.init(A, AALONG ? d.K : d.cols, c0, d.cols, klo, tid);
+  sb.init(reinterpret_cast<const char*>(d.B), BALONG ? d.K : d.rows, r0, rend, klo, tid);
+
+  // 8-bit blocks: the step's scales travel with it, one float a row of B, and of A if its blocks are single rows
   const int kblocks = (d.K + kFp8Block - 1) / kFp8Block;
-  if (FP8 && d.a_rows > 1) sa += (size_t)g * ((d.cols + 127) / 128) * kblocks;
+  const float *scb = nullptr, *sca = nullptr;
+  uint32_t scoff = 0;
+  if constexpr (FP8) {
+    const int w0 = tid;                                        // threads 0..RT-1 load B's, the next 256 A's
+    scb = d.sb + r0;
+    if constexpr (!AROW) {
+      sca = d.sa + (size_t)g * ((d.cols + 127) / 128) * kblocks + (size_t)min((c0 + wc * AT * 16) / 128, (d.cols - 1) / 128) * kblocks;
+      if (w0 < RT) scoff = min(w0, rend - 1 - r0) * 4;
+    } else {
+      sca = d.sa + c0;
+      scoff = (w0 < RT ? min(w0, rend - 1 - r0) : min(w0 - RT, d.cols - 1 - c0)) * 4;
+    }
+  }
+  auto load_scales = [&](char* st, int kb) {
+    if constexpr (FP8) {
+      char* s = st + TA::BYTES + TB::BYTES;
+      if (wave * 64 < RT) lds_load4(reinterpret_cast<const char*>(scb + (size_t)kb * d.rows) + scoff, s + wave * 256);
+      if constexpr (RT + LIN_CT > LIN_THREADS) static_assert(RT + LIN_CT <= LIN_THREADS, "one scale a thread");
+      if (AROW && wave * 64 >= RT && wave * 64 < RT + LIN_CT)
+        lds_load4(reinterpret_cast<const char*>(sca + (size_t)kb * d.cols) + scoff, s + wave * 256);
+    }
+  };
 
-  f32x4_t acc[4][4];
+  f32x4_t acc[AT][BT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < AT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < BT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // one step's operand into LDS: rows of the tile (128), 8 chunks of 16 bytes each
-  auto stage = [&](uint4* s, const char* p, bool strided, int ld, int t0, int tend, int k0) {
-    for (int q = tid; q < LT * 8; q += LIN_THREADS) {
-      uint4 v{0, 0, 0, 0};
-      if (!strided) {
-        const int r = q >> 3, c = q & 7, row = t0 + r, k = k0 + c * CE;
-        if (row < tend && k < khi) v = ldg16(p + ((size_t)row * ld + k) * ESZ);
-        s[lin_slot(r, c)] = v;
-      } else {
-        // contraction row k0 + q / 16, eight of the tile's rows
-        const int k = k0 + (q >> 4), r = (q & 15) * 8, row = t0 + r;
-        if (k < khi && row < tend) v = ldg16(p + ((size_t)k * ld + row) * ESZ);
-        uint16_t* o = reinterpret_cast<uint16_t*>(s);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const int l16 = lane & 15, q4 = lane >> 4;
+  const int fo = l16 * LIN_BYTES + (((2 * q4) ^ (l16 & 7)) << 4);   // 8-bit operand reads
+  const int bo = l16 * LIN_BYTES + ((q4 ^ (l16 & 7)) << 4);         // bf16 ones along the contraction, of row 0 of a tile
+  auto compute = [&](const char* st, int kb) {
+    const char* la = st;
+    const char* lb = st + TA::BYTES;
+    if constexpr (FP8) {
+      const float* ls = reinterpret_cast<const float*>(st + TA::BYTES + TB::BYTES);
+      // 32 bytes of a row: chunks 2 q4 and 2 q4 + 1, whose places differ in the lowest bit; the tile's rows are l16
+      // modulo 16, so the places are the same for every tile
+      auto frag = [&](const char* t, int tile) {
+        const char* p = t + tile * (16 * LIN_BYTES);
+        const uint4 a = *reinterpret_cast<const uint4*>(p + fo), b = *reinterpret_cast<const uint4*>(p + (fo ^ 16));
+        return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+      };
+      i32x8_t af[AT];
+      f32x4_t fa[AT];
+      const float s1 = AROW ? 0.f : sca[kb];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int kk = q >> 4;
-          o[lin_slot(r + e, kk >> 3) * 8 + (kk & 7)] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
+      for (int i = 0; i < AT; ++i) {
+        af[i] = frag(la, wc * AT + i);
+        if constexpr (AROW) fa[i] = *reinterpret_cast<const f32x4_t*>(ls + RT + (wc * AT + i) * 16 + 4 * q4);
+      }
+      bf16x8_t ax[EXACT ? AT : 1][4];
+      if constexpr (EXACT) {
+#pragma unroll
+        for (int i = 0; i < AT; ++i)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) ax[i][s] = fp8_to_bf16(af[i][2 * s], af[i][2 * s + 1]);
+      }
+      // B tile j + 1 is read, and tile j - 1's sums are scaled, while the matrix cores work on tile j; the fences keep
+      // the compiler from reading all tiles ahead, which spills
+      const float* lr = ls + wr * BT * 16 + l16;
+      i32x8_t bf = frag(lb, wr * BT);
+      float s = lr[0], sp = 0.f;
+      f32x4_t p[2][AT];
+#pragma unroll
+      for (int j = 0; j <= BT; ++j) {
+        i32x8_t bn;
+        float sn = 0.f;
+        if (j + 1 < BT) {
+          bn = frag(lb, wr * BT + j + 1);
+          sn = lr[(j + 1) * 16];
+        }
+        if (j < BT) {
+          bf16x8_t bx[4];
+          if constexpr (EXACT) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) bx[t] = fp8_to_bf16(bf[2 * t], bf[2 * t + 1]);
+          }
+#pragma unroll
+          for (int i = 0; i < AT; ++i) {
+            f32x4_t z{0.f, 0.f, 0.f, 0.f};
+            if constexpr (EXACT) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[i][t], bx[t], z, 0, 0, 0);
+            } else {
+              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf, z, 0, 0, 0, 0, 0, 0);
+            }
+            p[j & 1][i] = z;
+          }
+        }
+        if (j > 0) {
+          const float s2 = s1 * sp;
+#pragma unroll
+          for (int i = 0; i < AT; ++i)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              acc[i][j - 1][v] = fmaf(p[(j - 1) & 1][i][v], AROW ? fa[i][v] * sp : s2, acc[i][j - 1][v]);
+        }
+        sp = s;
+        s = sn;
+        bf = bn;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      // a row of the operand along the contraction, or across it through the transposing read: in each 16 lanes,
+      // lane 4 v + u points at row 8 q4 + 4 h + v, elements 4 u .. + 3, and lane j receives element j % 4 of lane
+      // 4 v + j / 4 as its value v
+      auto along = [&](const char* t, int row, int kk) {
+        return as_bf16x8(*reinterpret_cast<const uint4*>(t + row * LIN_BYTES + (bo ^ (kk * 64))));
+      };
+      auto across = [&](auto rl, const char* t, int col, int kk) {
+        constexpr int RL = decltype(rl)::value;
+        s16x4_t h[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int kr = kk * 32 + 8 * q4 + 4 * e + (l16 >> 2), c = col + 4 * (l16 & 3);
+          const int at = kr * RL * 2 + (((c >> 3) ^ LinTile<RL, false>::swz(kr)) << 4) + (c & 7) * 2;
+          h[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(t + at));
+        }
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(bf16x8_t, s16x8{h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]});
+      };
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        bf16x8_t af[AT];
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+          const int c = (wc * AT + i) * 16;
+          if constexpr (AALONG) af[i] = along(la, c, kk);
+          else af[i] = across(std::integral_constant<int, LIN_CT>{}, la, c, kk);
+        }
+#pragma unroll
+        for (int j = 0; j < BT; ++j) {
+          const int r = (wr * BT + j) * 16;
+          bf16x8_t bf;
+          if constexpr (BALONG) bf = along(lb, r, kk);
+          else bf = across(std::integral_constant<int, RT>{}, lb, r, kk);
+#pragma unroll
+          for (int i = 0; i < AT; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], bf, acc[i][j], 0, 0, 0);
         }
       }
     }
   };
-  const int lda = ASTR ? d.cols : d.K, ldb = BSTR ? d.rows : d.K;
-  for (int k0 = klo; k0 < khi; k0 += BK) {
-    stage(s_a, A, ASTR, lda, c0, d.cols, k0);
-    stage(s_b, B, BSTR, ldb, r0, rend, k0);
-    __syncthreads();
-    if constexpr (FP8) {
-      const int kb = k0 / kFp8Block;
-      i32x8_t af[4], bf[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int ra = wc * 64 + i * 16 + (lane & 15), rb = wr * 64 + i * 16 + (lane & 15), c = (lane >> 4) * 2;
-        const uint4 a0 = s_a[lin_slot(ra, c)], a1 = s_a[lin_slot(ra, c + 1)];
-        const uint4 b0 = s_b[lin_slot(rb, c)], b1 = s_b[lin_slot(rb, c + 1)];
-        af[i] = i32x8_t{(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
-        bf[i] = i32x8_t{(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = r0 + wr * 64 + j * 16 + (lane & 15);
-        const float sb = row < rend ? d.sb[(size_t)kb * d.rows + row] : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = c0 + wc * 64 + i * 16 + 4 * (lane >> 4);
-          f32x4_t p{0.f, 0.f, 0.f, 0.f};
-          if constexpr (EXACT) {
-#pragma unroll
-            for (int s = 0; s < 8; s += 2)
-              p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp8_to_bf16(af[i][s], af[i][s + 1]), fp8_to_bf16(bf[j][s], bf[j][s + 1]), p, 0, 0, 0);
-          } else {
-            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[j], p, 0, 0, 0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int cc = min(col + v, d.cols - 1);
-            const float s = d.a_rows == 1 ? sa[(size_t)kb * d.cols + cc] : sa[(size_t)(cc / 128) * kblocks + kb];
-            acc[i][j][v] = fmaf(p[v], s * sb, acc[i][j][v]);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        const int c = kk * 4 + (lane >> 4);
-        uint4 af[4], bf[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          af[i] = s_a[lin_slot(wc * 64 + i * 16 + (lane & 15), c)];
-          bf[i] = s_b[lin_slot(wr * 64 + i * 16 + (lane & 15), c)];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(af[i]), as_bf16x8(bf[j]), acc[i][j], 0, 0, 0);
-      }
-    }
-    __syncthreads();
+
+  const int steps = (khi - klo) / BK, left = (khi - klo) - steps * BK;
+  auto load = [&](int s) {
+    char* st = smem[s & 1];
+    sa.load(st, wave);
+    sb.load(st + TA::BYTES, wave);
+    load_scales(st, s);
+  };
+  if (steps > 0) load(0);
+  for (int s = 0; s < steps; ++s) {
+    lin_sync();                                  // step s is in LDS, and nobody reads the other stage any more
+    if (s + 1 < steps) load(s + 1);
+    compute(smem[s & 1], s);
   }
+  if (left > 0) {
+    char* st = smem[steps & 1];                  // its last readers are behind the last barrier
+    sa.load_part(st, left, tid);
+    sb.load_part(st + TA::BYTES, left, tid);
+    load_scales(st, steps);
+    lin_sync();
+    compute(st, steps);
+  }
+
   const size_t out0 = KIND == LIN_DW ? (size_t)g * d.rows * d.cols : 0;
+  const bool vec = (d.cols & 3) == 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int j = 0; j < BT; ++j) {
+    const int row = r0 + (wr * BT + j) * 16 + l16;
+    if (row >= rend) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = r0 + wr * 64 + j * 16 + (lane & 15), col = c0 + wc * 64 + i * 16 + 4 * (lane >> 4);
-      if (row >= rend) continue;
+    for (int i = 0; i < AT; ++i) {
+      const int col = c0 + (wc * AT + i) * 16 + 4 * q4;
+      if (col >= d.cols) continue;
       const size_t at = out0 + (size_t)row * d.cols + col;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (col + v >= d.cols) continue;
-        if (d.out_f32) {
-          float* o = reinterpret_cast<float*>(d.out) + at + v;
-          *o = d.accumulate ? *o + acc[i][j][v] : acc[i][j][v];
+      f32x4_t a = acc[i][j];
+      if (KIND == LIN_DW || d.out_f32) {
+        float* o = reinterpret_cast<float*>(d.out) + at;
+        if (vec) {
+          if (d.accumulate) a += *reinterpret_cast<const f32x4_t*>(o);
+          *reinterpret_cast<f32x4_t*>(o) = a;
         } else {
-          reinterpret_cast<uint16_t*>(d.out)[at + v] = (uint16_t)pack_bf16(acc[i][j][v], 0.f);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (col + v < d.cols) o[v] = d.accumulate ? o[v] + a[v] : a[v];
+        }
+      } else {
+        uint16_t* o = reinterpret_cast<uint16_t*>(d.out) + at;
+        const uint2 h{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+        if (vec) {
+          *reinterpret_cast<uint2*>(o) = h;
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (col + v < d.cols) o[v] = (uint16_t)((v < 2 ? h.x : h.y) >> (16 * (v & 1)));
         }
       }
     }
+  }
 }
 
-template <int KIND, bool EXACT = false>
+template <int KIND, int RT, bool EXACT, bool AROW>
 static hipError_t go_linear(const LinDesc& d, hipStream_t s) {
-  const int ct = (d.cols + LT - 1) / LT;
+  const int ct = (d.cols + LIN_CT - 1) / LIN_CT;
   // row tiles of every expert at most: whole ones, and one ragged one each
-  const int rt = KIND == LIN_DW ? (d.rows + LT - 1) / LT : d.rows / LT + d.groups;
-  const size_t wgs = (size_t)ct * rt * (KIND == LIN_DW ? d.groups : 1);
-  if (wgs > 0x7FFFFFFFu) return hipErrorInvalidValue;
-  ffn_launch((k_linear<KIND, EXACT>), dim3((unsigned)wgs), dim3(LIN_THREADS), 0, s, d, ct, rt);
+  const long long rt = KIND == LIN_DW ? (long long)(d.rows + RT - 1) / RT * d.groups : d.rows / RT + d.groups;
+  const long long wgs = (ct * rt + 7) / 8 * 8;
+  if (wgs > 0x7FFFFFF0ll) return hipErrorInvalidValue;
+  ffn_launch((k_linear<KIND, RT, EXACT, AROW>), dim3((unsigned)wgs), dim3(LIN_THREADS), 0, s, d, ct, (int)rt);
   return hipGetLastError();
+}
+template <int KIND, bool EXACT = false, bool AROW = false>
+static hipError_t pick_linear(const LinDesc& d, hipStream_t s) {
+  const int rows = KIND == LIN_DW ? d.rows : d.rows / d.groups;
+  if (rows <= 64) return go_linear<KIND, 64, EXACT, AROW>(d, s);
+  if (rows <= 128) return go_linear<KIND, 128, EXACT, AROW>(d, s);
+  if constexpr (EXACT) return go_linear<KIND, 128, EXACT, AROW>(d, s);
+  else return go_linear<KIND, 256, EXACT, AROW>(d, s);
 }
 hipError_t launch_linear(const LinDesc& d, hipStream_t s) {
   switch (d.kind) {
-    case LIN_FP8: return d.out_f32 ? go_linear<LIN_FP8, true>(d, s) : go_linear<LIN_FP8>(d, s);
-    case LIN_FWD: return go_linear<LIN_FWD>(d, s);
-    case LIN_DX: return go_linear<LIN_DX>(d, s);
-    case LIN_DW: return go_linear<LIN_DW>(d, s);
+    case LIN_FP8:
+      if (d.a_rows == 1) return d.out_f32 ? pick_linear<LIN_FP8, true, true>(d, s) : pick_linear<LIN_FP8, false, true>(d, s);
+      return d.out_f32 ? pick_linear<LIN_FP8, true>(d, s) : pick_linear<LIN_FP8>(d, s);
+    case LIN_FWD: return pick_linear<LIN_FWD>(d, s);
+    case LIN_DX: return pick_linear<LIN_DX>(d, s);
+    case LIN_DW: return pick_linear<LIN_DW>(d, s);
   }
   return hipErrorInvalidValue;
 }

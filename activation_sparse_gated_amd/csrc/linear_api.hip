@@ -21,6 +21,7 @@ ffn_status done(hipError_t e) { return e == hipSuccess ? FFN_OK : FFN_E_HIP; }
 hipStream_t st(void* stream) { return reinterpret_cast<hipStream_t>(stream); }
 
 constexpr int kMaxRowTiles = 1 << 30;
+constexpr int kMaxWidth = 1 << 22;   // 256 rows of it stay within 32-bit byte offsets
 
 bool norm_shape_ok(int32_t dtype, int32_t m, int32_t d, float eps) {
   return dtype_ok(dtype) && m >= 0 && d >= 8 && d % 8 == 0 && d <= 16384 && std::isfinite(eps) && eps >= 0.f;
@@ -28,6 +29,7 @@ bool norm_shape_ok(int32_t dtype, int32_t m, int32_t d, float eps) {
 // Tiles of the largest grid any kernel makes for this product, in workgroups.
 bool product_shape_ok(int32_t m, int32_t n, int32_t k, int32_t groups) {
   if (m < 0 || n < 1 || k < 1 || groups < 1 || groups > FFN_LINEAR_MAX_GROUPS) return false;
+  if (n > kMaxWidth || k > kMaxWidth) return false;
   const long long rt = m / 16 + groups, ct = n / 16 + 1, kt = k / 16 + 1;
   return rt * ct < kMaxRowTiles && ct * kt * groups < kMaxRowTiles && rt * kt < kMaxRowTiles;
 }
