@@ -43,12 +43,19 @@ constexpr int LIN_THREADS = 512;
 constexpr int LIN_CT = 256;                      // columns of a tile
 constexpr int LIN_BYTES = 128;                   // contraction bytes of a step
 
-// 16 (or 4) bytes a lane from global memory to LDS: the wave's lanes in order from `l` on.
-__device__ __forceinline__ void lds_load16(const char* g, void* l) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g, (__attribute__((address_space(3))) void*)l, 16, 0, 0);
+// 16 (or 4) bytes a lane from base + off to LDS: the wave's lanes in order from
+// address `l` on. In assembly, because the compiler takes a load to LDS for a
+// possible writer of whatever LDS is read next and waits for it there, which
+// would end the overlap; lin_sync() is the wait. Such a load has no register
+// to write, and the compiler's own waits for other loads only become stricter.
+__device__ __forceinline__ uint32_t lds_address(const char* l) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)l;
 }
-__device__ __forceinline__ void lds_load4(const char* g, void* l) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g, (__attribute__((address_space(3))) void*)l, 4, 0, 0);
+__device__ __forceinline__ void lds_load16(const char* base, uint32_t off, uint32_t l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(l), "v"(off), "s"(base) : "m0");
+}
+__device__ __forceinline__ void lds_load4(const char* base, uint32_t off, uint32_t l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(l), "v"(off), "s"(base) : "m0");
 }
 // Every load to LDS and every LDS read of this wave is done, then every wave's.
 __device__ __forceinline__ void lin_sync() {
@@ -74,53 +81,59 @@ struct LinTile {
   static constexpr int LOADS = BYTES / (LIN_THREADS * 16);     // 16-byte loads of a thread
   static_assert(LOADS >= 1, "tile too small");
   static constexpr int CPR = ALONG ? 8 : R / 8;                // chunks of an LDS row
-  __device__ __forceinline__ static int swz(int row) { return (ALONG ? row : ((row & 3) << 1) | (row & 8)) & (CPR < 16 ? CPR - 1 : 15); }
+  __host__ __device__ __forceinline__ static constexpr int swz(int row) { return (ALONG ? row : ((row & 3) << 1) | (row & 8)) & (CPR < 16 ? CPR - 1 : 15); }
   // load q = i * 512 + thread: LDS chunk q, that is row q / CPR, place q % CPR
   __device__ __forceinline__ static int row_of(int q) { return q / CPR; }
   __device__ __forceinline__ static int chunk_of(int q) { return (q % CPR) ^ swz(q / CPR); }
 };
 
-// Where a thread's loads of one operand come from: `base` (uniform) + off[i],
-// `base` moving on by `step` bytes.
+// Where a thread's loads of one operand come from: `base` (uniform, moving on
+// by `step` bytes a step) + min(first + i * stride, last). All loads of a
+// thread lie at the same place of their LDS rows (512 threads are whole groups
+// of rows with the same permutation), so two registers describe them.
 template <int R, bool ALONG, int ESZ>
 struct LinSrc {
   using T = LinTile<R, ALONG>;
+  static constexpr int ROWS = LIN_THREADS / T::CPR;            // LDS rows of one load of the workgroup
+  static_assert(T::LOADS == 1 || T::swz(ROWS) == 0, "loads at one place of their rows");
   const char* base;
   size_t step;
-  uint32_t off[T::LOADS];
+  uint32_t first, last, stride;
   // rows r0.. of at most rend rows of p, contraction from k0 on, ld elements apart.
   // Rows past the end repeat the last one: their results are not stored.
   __device__ __forceinline__ void init(const char* p, int ld, int r0, int rend, int k0, int tid) {
+    const uint32_t pitch = (uint32_t)ld * ESZ;
     if constexpr (ALONG) {
       base = p + ((size_t)r0 * ld + k0) * ESZ;
       step = LIN_BYTES;
-#pragma unroll
-      for (int i = 0; i < T::LOADS; ++i) {
-        const int q = i * LIN_THREADS + tid;
-        off[i] = (uint32_t)min(T::row_of(q), rend - 1 - r0) * (uint32_t)(ld * ESZ) + T::chunk_of(q) * 16;
-      }
+      first = T::row_of(tid) * pitch + T::chunk_of(tid) * 16;
+      last = (uint32_t)(rend - 1 - r0) * pitch + T::chunk_of(tid) * 16;
     } else {
       base = p + ((size_t)k0 * ld + r0) * ESZ;
-      step = (size_t)64 * ld * ESZ;
-#pragma unroll
-      for (int i = 0; i < T::LOADS; ++i) {
-        const int q = i * LIN_THREADS + tid;
-        off[i] = (uint32_t)T::row_of(q) * (uint32_t)(ld * ESZ) + min(T::chunk_of(q) * 8, rend - 8 - r0) * ESZ;
-      }
+      step = (size_t)64 * pitch;
+      first = T::row_of(tid) * pitch + min(T::chunk_of(tid) * 8, rend - 8 - r0) * ESZ;
+      last = 0xFFFFFFFFu;
     }
+    stride = ROWS * pitch;
   }
   __device__ __forceinline__ void load(char* lds, int wave) {
+    const uint32_t at = lds_address(lds) + wave * 64 * 16;
+    uint32_t o = first;
+    asm volatile("" : "+v"(o));                  // the offsets are made here, not kept (as 64-bit pairs) over the loop
 #pragma unroll
-    for (int i = 0; i < T::LOADS; ++i) lds_load16(base + off[i], lds + (i * LIN_THREADS + wave * 64) * 16);
+    for (int i = 0; i < T::LOADS; ++i)
+      lds_load16(base, ALONG ? min(o + i * stride, last) : o + i * stride, at + i * LIN_THREADS * 16);
     base += step;
   }
   // The last, partial step: `left` contraction elements, zeros behind them.
   __device__ __forceinline__ void load_part(char* lds, int left, int tid) {
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < T::LOADS; ++i) {
       const int q = i * LIN_THREADS + tid;
       const bool ok = ALONG ? T::chunk_of(q) * (16 / ESZ) < left : T::row_of(q) < left;
-      *reinterpret_cast<uint4*>(lds + q * 16) = ok ? ldg16(base + off[i]) : uint4{0, 0, 0, 0};
+      uint4 v{0, 0, 0, 0};
+      if (ok) v = ldg16(base + (ALONG ? min(first + i * stride, last) : first + i * stride));
+      *reinterpret_cast<uint4*>(lds + q * 16) = v;
     }
   }
 };
@@ -185,28 +198,32 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
   sa.init(A, AALONG ? d.K : d.cols, c0, d.cols, klo, tid);
   sb.init(reinterpret_cast<const char*>(d.B), BALONG ? d.K : d.rows, r0, rend, klo, tid);
 
-  // 8-bit blocks: the step's scales travel with it, one float a row of B, and of A if its blocks are single rows
+  // 8-bit blocks: the step's scales travel with it, one float a row of B (threads 0 .. RT - 1) and a column of the
+  // tile (the next 256 threads; with blocks of 128 rows of A, columns of a block all get its scale)
+  static_assert(RT + LIN_CT <= LIN_THREADS, "one scale a thread");
   const int kblocks = (d.K + kFp8Block - 1) / kFp8Block;
-  const float *scb = nullptr, *sca = nullptr;
+  const char *scb = nullptr, *sca = nullptr;
+  size_t sca_step = 0;
   uint32_t scoff = 0;
   if constexpr (FP8) {
-    const int w0 = tid;                                        // threads 0..RT-1 load B's, the next 256 A's
-    scb = d.sb + r0;
-    if constexpr (!AROW) {
-      sca = d.sa + (size_t)g * ((d.cols + 127) / 128) * kblocks + (size_t)min((c0 + wc * AT * 16) / 128, (d.cols - 1) / 128) * kblocks;
-      if (w0 < RT) scoff = min(w0, rend - 1 - r0) * 4;
+    scb = reinterpret_cast<const char*>(d.sb + r0);
+    const int c = tid - RT;
+    if constexpr (AROW) {
+      sca = reinterpret_cast<const char*>(d.sa + c0);
+      sca_step = (size_t)d.cols * 4;
+      scoff = (uint32_t)min(c, d.cols - 1 - c0) * 4;
     } else {
-      sca = d.sa + c0;
-      scoff = (w0 < RT ? min(w0, rend - 1 - r0) : min(w0 - RT, d.cols - 1 - c0)) * 4;
+      sca = reinterpret_cast<const char*>(d.sa + ((size_t)g * ((d.cols + kFp8Block - 1) / kFp8Block) + c0 / kFp8Block) * kblocks);
+      sca_step = 4;
+      scoff = (uint32_t)(min(c, d.cols - 1 - c0) / kFp8Block * kblocks) * 4;
     }
+    if (c < 0) scoff = (uint32_t)min(tid, rend - 1 - r0) * 4;
   }
-  auto load_scales = [&](char* st, int kb) {
+  auto load_scales = [&](const char* st, int kb) {
     if constexpr (FP8) {
-      char* s = st + TA::BYTES + TB::BYTES;
-      if (wave * 64 < RT) lds_load4(reinterpret_cast<const char*>(scb + (size_t)kb * d.rows) + scoff, s + wave * 256);
-      if constexpr (RT + LIN_CT > LIN_THREADS) static_assert(RT + LIN_CT <= LIN_THREADS, "one scale a thread");
-      if (AROW && wave * 64 >= RT && wave * 64 < RT + LIN_CT)
-        lds_load4(reinterpret_cast<const char*>(sca + (size_t)kb * d.cols) + scoff, s + wave * 256);
+      const uint32_t at = lds_address(st) + TA::BYTES + TB::BYTES + wave * 256;
+      if (wave * 64 < RT) lds_load4(scb + (size_t)kb * d.rows * 4, scoff, at);
+      else if (wave * 64 < RT + LIN_CT) lds_load4(sca + (size_t)kb * sca_step, scoff, at);
     }
   };
 
@@ -217,141 +234,147 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
     for (int j = 0; j < BT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   const int l16 = lane & 15, q4 = lane >> 4;
-  const int fo = l16 * LIN_BYTES + (((2 * q4) ^ (l16 & 7)) << 4);   // 8-bit operand reads
-  const int bo = l16 * LIN_BYTES + ((q4 ^ (l16 & 7)) << 4);         // bf16 ones along the contraction, of row 0 of a tile
-  auto compute = [&](const char* st, int kb) {
-    const char* la = st;
-    const char* lb = st + TA::BYTES;
+  // operand reads of a 16-row tile. Along the contraction: bf16 chunk 4 kk + q4, or the 8-bit chunks 2 q4 and 2 q4 + 1,
+  // whose places differ in the lowest bit; the tile's rows are l16 modulo 16, so the places are those of row l16.
+  const int fo = l16 * LIN_BYTES + (((FP8 ? 2 * q4 : q4) ^ (l16 & 7)) << 4);
+  // Across it (bf16), through the transposing read: in each 16 lanes, lane 4 v + u points at row 8 q4 + 4 h + v,
+  // elements 4 u .. + 3, and lane j receives element j % 4 of lane 4 v + j / 4 as its value v.
+  using Frag = std::conditional_t<FP8, i32x8_t, bf16x8_t>;
+  auto along = [&](const char* t, int tile, int kk) -> Frag {
+    const char* p = t + tile * (16 * LIN_BYTES);
     if constexpr (FP8) {
-      const float* ls = reinterpret_cast<const float*>(st + TA::BYTES + TB::BYTES);
-      // 32 bytes of a row: chunks 2 q4 and 2 q4 + 1, whose places differ in the lowest bit; the tile's rows are l16
-      // modulo 16, so the places are the same for every tile
-      auto frag = [&](const char* t, int tile) {
-        const char* p = t + tile * (16 * LIN_BYTES);
-        const uint4 a = *reinterpret_cast<const uint4*>(p + fo), b = *reinterpret_cast<const uint4*>(p + (fo ^ 16));
-        return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-      };
-      i32x8_t af[AT];
-      f32x4_t fa[AT];
-      const float s1 = AROW ? 0.f : sca[kb];
+      const uint4 a = *reinterpret_cast<const uint4*>(p + fo), b = *reinterpret_cast<const uint4*>(p + (fo ^ 16));
+      return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+    } else {
+      return as_bf16x8(*reinterpret_cast<const uint4*>(p + (fo ^ (kk * 64))));
+    }
+  };
+  auto across = [&](auto rl, const char* t, int tile, int kk) -> bf16x8_t {
+    constexpr int RL = decltype(rl)::value;
+    s16x4_t h[2];
 #pragma unroll
-      for (int i = 0; i < AT; ++i) {
-        af[i] = frag(la, wc * AT + i);
-        if constexpr (AROW) fa[i] = *reinterpret_cast<const f32x4_t*>(ls + RT + (wc * AT + i) * 16 + 4 * q4);
-      }
-      bf16x8_t ax[EXACT ? AT : 1][4];
+    for (int e = 0; e < 2; ++e) {
+      const int kr = kk * 32 + 8 * q4 + 4 * e + (l16 >> 2), c = tile * 16 + 4 * (l16 & 3);
+      const int at = kr * RL * 2 + (((c >> 3) ^ LinTile<RL, false>::swz(kr)) << 4) + (c & 7) * 2;
+      h[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(t + at));
+    }
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(bf16x8_t, s16x8{h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]});
+  };
+  auto read_a = [&](const char* st, int i, int kk) -> Frag {
+    if constexpr (AALONG) return along(st, wc * AT + i, kk);
+    else return across(std::integral_constant<int, LIN_CT>{}, st, wc * AT + i, kk);
+  };
+  auto read_b = [&](const char* st, int j, int kk) -> Frag {
+    if constexpr (BALONG) return along(st + TA::BYTES, wr * BT + j, kk);
+    else return across(std::integral_constant<int, RT>{}, st + TA::BYTES, wr * BT + j, kk);
+  };
+
+  // The steps. A step is KK * BT turns of AT matrix instructions (of AT * 4 for an exact sum); the operand of turn
+  // t + AHEAD is read during turn t, A's next slice in the last turn that uses this one, so that the reads of a step
+  // are all behind it AHEAD turns before its end. There the workgroup meets: the next step has arrived, nobody reads
+  // this step's stage any more, and the loads of the step after the next go into it.
+  constexpr int KK = FP8 ? 1 : 2, TURNS = KK * BT, AHEAD = FP8 ? 1 : 3, RING = AHEAD + 1;
+  static_assert(TURNS % RING == 0 && TURNS > AHEAD, "turns of a step");
+  const int full = (khi - klo) / BK, left = (khi - klo) - full * BK, steps = full + (left > 0);
+  auto load = [&](int s) {
+    char* st = smem[s & 1];
+    if (s < full) {
+      sa.load(st, wave);
+      sb.load(st + TA::BYTES, wave);
+    } else {
+      sa.load_part(st, left, tid);
+      sb.load_part(st + TA::BYTES, left, tid);
+    }
+    load_scales(st, s);
+  };
+  Frag af[AT], bf[RING];
+  bf16x8_t ax[EXACT ? AT : 1][4];
+  f32x4_t fa[AROW ? AT : 1], z[2];
+  float fs[4], s1 = 0.f;                         // a turn's scale is used one turn later too
+  static_assert(TURNS % 4 == 0, "turns of a step");
+  auto scale_of = [&](const char* st) { return reinterpret_cast<const float*>(st + TA::BYTES + TB::BYTES); };
+  auto fetch_b = [&](const char* st, int t) {
+    bf[t % RING] = read_b(st, t % BT, t / BT);
+    if constexpr (FP8) fs[t % 4] = scale_of(st)[(wr * BT + t % BT) * 16 + l16];
+  };
+  auto fetch_scales = [&](const char* st) {
+    if constexpr (AROW) {
+#pragma unroll
+      for (int i = 0; i < AT; ++i) fa[i] = *reinterpret_cast<const f32x4_t*>(scale_of(st) + RT + (wc * AT + i) * 16 + 4 * q4);
+    } else if constexpr (FP8) {
+      s1 = scale_of(st)[RT + wc * AT * 16];
+    }
+  };
+  // the block's sum of matrix instruction n (turn n / AT, column tile n % AT) joins the accumulator
+  auto join = [&](int n) {
+    const float s = AROW ? fs[n / AT % 4] : s1 * fs[n / AT % 4];
+    f32x4_t& o = acc[n % AT][n / AT % BT];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) o[v] = fmaf(z[n & 1][v], AROW ? fa[AROW ? n % AT : 0][v] * s : s, o[v]);
+    asm volatile("" : "+v"(o));                  // here, not where the compiler would gather them, with every z kept till then
+  };
+  if (steps > 0) {
+    load(0);
+    lin_sync();
+    if (steps > 1) load(1);
+#pragma unroll
+    for (int i = 0; i < AT; ++i) af[i] = read_a(smem[0], i, 0);
+#pragma unroll
+    for (int t = 0; t < AHEAD; ++t) fetch_b(smem[0], t);
+    fetch_scales(smem[0]);
+  }
+  for (int s = 0; s < steps; ++s) {
+    const char* st = smem[s & 1];
+    const char* nx = smem[(s & 1) ^ 1];
+    if constexpr (FP8) {
       if constexpr (EXACT) {
 #pragma unroll
         for (int i = 0; i < AT; ++i)
 #pragma unroll
-          for (int s = 0; s < 4; ++s) ax[i][s] = fp8_to_bf16(af[i][2 * s], af[i][2 * s + 1]);
-      }
-      // B tile j + 1 is read, and tile j - 1's sums are scaled, while the matrix cores work on tile j; the fences keep
-      // the compiler from reading all tiles ahead, which spills
-      const float* lr = ls + wr * BT * 16 + l16;
-      i32x8_t bf = frag(lb, wr * BT);
-      float s = lr[0], sp = 0.f;
-      f32x4_t p[2][AT];
-#pragma unroll
-      for (int j = 0; j <= BT; ++j) {
-        i32x8_t bn;
-        float sn = 0.f;
-        if (j + 1 < BT) {
-          bn = frag(lb, wr * BT + j + 1);
-          sn = lr[(j + 1) * 16];
-        }
-        if (j < BT) {
-          bf16x8_t bx[4];
-          if constexpr (EXACT) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) bx[t] = fp8_to_bf16(bf[2 * t], bf[2 * t + 1]);
-          }
-#pragma unroll
-          for (int i = 0; i < AT; ++i) {
-            f32x4_t z{0.f, 0.f, 0.f, 0.f};
-            if constexpr (EXACT) {
-#pragma unroll
-              for (int t = 0; t < 4; ++t) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[i][t], bx[t], z, 0, 0, 0);
-            } else {
-              z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf, z, 0, 0, 0, 0, 0, 0);
-            }
-            p[j & 1][i] = z;
-          }
-        }
-        if (j > 0) {
-          const float s2 = s1 * sp;
-#pragma unroll
-          for (int i = 0; i < AT; ++i)
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              acc[i][j - 1][v] = fmaf(p[(j - 1) & 1][i][v], AROW ? fa[i][v] * sp : s2, acc[i][j - 1][v]);
-        }
-        sp = s;
-        s = sn;
-        bf = bn;
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    } else {
-      // a row of the operand along the contraction, or across it through the transposing read: in each 16 lanes,
-      // lane 4 v + u points at row 8 q4 + 4 h + v, elements 4 u .. + 3, and lane j receives element j % 4 of lane
-      // 4 v + j / 4 as its value v
-      auto along = [&](const char* t, int row, int kk) {
-        return as_bf16x8(*reinterpret_cast<const uint4*>(t + row * LIN_BYTES + (bo ^ (kk * 64))));
-      };
-      auto across = [&](auto rl, const char* t, int col, int kk) {
-        constexpr int RL = decltype(rl)::value;
-        s16x4_t h[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int kr = kk * 32 + 8 * q4 + 4 * e + (l16 >> 2), c = col + 4 * (l16 & 3);
-          const int at = kr * RL * 2 + (((c >> 3) ^ LinTile<RL, false>::swz(kr)) << 4) + (c & 7) * 2;
-          h[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(t + at));
-        }
-        typedef short s16x8 __attribute__((ext_vector_type(8)));
-        return __builtin_bit_cast(bf16x8_t, s16x8{h[0][0], h[0][1], h[0][2], h[0][3], h[1][0], h[1][1], h[1][2], h[1][3]});
-      };
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        bf16x8_t af[AT];
-#pragma unroll
-        for (int i = 0; i < AT; ++i) {
-          const int c = (wc * AT + i) * 16;
-          if constexpr (AALONG) af[i] = along(la, c, kk);
-          else af[i] = across(std::integral_constant<int, LIN_CT>{}, la, c, kk);
-        }
-#pragma unroll
-        for (int j = 0; j < BT; ++j) {
-          const int r = (wr * BT + j) * 16;
-          bf16x8_t bf;
-          if constexpr (BALONG) bf = along(lb, r, kk);
-          else bf = across(std::integral_constant<int, RT>{}, lb, r, kk);
-#pragma unroll
-          for (int i = 0; i < AT; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], bf, acc[i][j], 0, 0, 0);
-        }
+          for (int e = 0; e < 4; ++e) ax[i][e] = fp8_to_bf16(af[i][2 * e], af[i][2 * e + 1]);
       }
     }
-  };
-
-  const int steps = (khi - klo) / BK, left = (khi - klo) - steps * BK;
-  auto load = [&](int s) {
-    char* st = smem[s & 1];
-    sa.load(st, wave);
-    sb.load(st + TA::BYTES, wave);
-    load_scales(st, s);
-  };
-  if (steps > 0) load(0);
-  for (int s = 0; s < steps; ++s) {
-    lin_sync();                                  // step s is in LDS, and nobody reads the other stage any more
-    if (s + 1 < steps) load(s + 1);
-    compute(smem[s & 1], s);
-  }
-  if (left > 0) {
-    char* st = smem[steps & 1];                  // its last readers are behind the last barrier
-    sa.load_part(st, left, tid);
-    sb.load_part(st + TA::BYTES, left, tid);
-    load_scales(st, steps);
-    lin_sync();
-    compute(st, steps);
+#pragma unroll
+    for (int t = 0; t < TURNS; ++t) {
+      const int j = t % BT;
+      if (t == TURNS - AHEAD && s + 1 < steps) {
+        lin_sync();
+        if (s + 2 < steps) load(s + 2);
+      }
+      // past the last step this reads a stage that nobody writes, for nothing
+      if (t + AHEAD < TURNS) fetch_b(st, t + AHEAD);
+      else fetch_b(nx, t + AHEAD - TURNS);
+      bf16x8_t bx[4];
+      if constexpr (EXACT) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bx[e] = fp8_to_bf16(bf[t % RING][2 * e], bf[t % RING][2 * e + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        if constexpr (FP8) {
+          const int n = t * AT + i;
+          f32x4_t p{0.f, 0.f, 0.f, 0.f};
+          if constexpr (EXACT) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[i][e], bx[e], p, 0, 0, 0);
+          } else {
+            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[t % RING], p, 0, 0, 0, 0, 0, 0);
+          }
+          z[n & 1] = p;
+          if (n > 0) join(n - 1);
+        } else {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], bf[t % RING], acc[i][j], 0, 0, 0);
+        }
+        if (FP8 || j == BT - 1) __builtin_amdgcn_sched_barrier(0);
+        if (j == BT - 1) af[i] = t + 1 < TURNS ? read_a(st, i, t / BT + 1) : read_a(nx, i, 0);
+      }
+      if (FP8 && t == TURNS - 1) {
+        join(TURNS * AT - 1);
+        fetch_scales(nx);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
   const size_t out0 = KIND == LIN_DW ? (size_t)g * d.rows * d.cols : 0;
