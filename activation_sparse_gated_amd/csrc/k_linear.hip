@@ -116,14 +116,11 @@ struct LinSrc {
     }
     stride = ROWS * pitch;
   }
-  __device__ __forceinline__ void load(char* lds, int wave) {
-    const uint32_t at = lds_address(lds) + wave * 64 * 16;
-    uint32_t o = first;
-    asm volatile("" : "+v"(o));                  // the offsets are made here, not kept (as 64-bit pairs) over the loop
-#pragma unroll
-    for (int i = 0; i < T::LOADS; ++i)
-      lds_load16(base, ALONG ? min(o + i * stride, last) : o + i * stride, at + i * LIN_THREADS * 16);
-    base += step;
+  // load i of the step that `base` points at; `at`: the wave's place in the operand's LDS tile
+  __device__ __forceinline__ void load(int i, uint32_t at) const {
+    uint32_t o = first + i * stride;
+    asm volatile("" : "+v"(o));                  // made here, not kept (as a 64-bit pair) over the loop
+    lds_load16(base, ALONG ? min(o, last) : o, at + i * LIN_THREADS * 16);
   }
   // The last, partial step: `left` contraction elements, zeros behind them.
   __device__ __forceinline__ void load_part(char* lds, int left, int tid) {
@@ -170,16 +167,19 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wc = wave % WC, wr = wave / WC;
 
-  // Workgroups go to the 8 XCDs in turn: each XCD takes a contiguous run of
-  // tiles, so that what its neighbours read is in its L2. Tiles run down
-  // column by column inside bands of 4 row tiles.
+  // Workgroups go to the 8 XCDs in turn: each XCD takes a contiguous run of tiles. Tiles come in patches of 4 row tiles
+  // by 8 column tiles, about what an XCD works on at a time, so that a step's slices are read by 4 or 8 of its
+  // workgroups and come from its L2 but once; patches run down all rows before the next 8 columns, so that the
+  // weights are read about once in all.
   const int total = ctiles * rtiles, per = (total + 7) / 8;
   const int lin = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
   if (lin >= total) return;
-  constexpr int BAND = 4;
-  const int band = lin / (BAND * ctiles), inb = lin - band * BAND * ctiles;
-  const int bh = min(BAND, rtiles - band * BAND);
-  const int rt = band * BAND + inb % bh, c0 = inb / bh * LIN_CT;
+  constexpr int PR = 4, PC = 8;
+  const int strip = lin / (PC * rtiles), ins = lin - strip * PC * rtiles;
+  const int sw = min(PC, ctiles - strip * PC);
+  const int patch = ins / (PR * sw), inp = ins - patch * PR * sw;
+  const int ph = min(PR, rtiles - patch * PR);
+  const int rt = patch * PR + inp % ph, c0 = (strip * PC + inp / ph) * LIN_CT;
   int g, lo, hi, r0, klo = 0, khi = d.K, rend;
   if constexpr (KIND == LIN_DW) {
     const int per_expert = (d.rows + RT - 1) / RT;
@@ -277,20 +277,31 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
   constexpr int KK = FP8 ? 1 : 2, TURNS = KK * BT, AHEAD = FP8 ? 1 : 3, RING = AHEAD + 1;
   static_assert(TURNS % RING == 0 && TURNS > AHEAD, "turns of a step");
   const int full = (khi - klo) / BK, left = (khi - klo) - full * BK, steps = full + (left > 0);
-  auto load = [&](int s) {
+  // A step's loads go out a few a turn over half a step, from the meeting on: the address unit takes 16 cycles for each,
+  // and a wave that finds its queue full stands still, matrix instructions and all.
+  constexpr int LOADS = TA::LOADS + TB::LOADS, PER = (LOADS + TURNS / 2 - 1) / (TURNS / 2);
+  auto load = [&](int s, int turn) {             // s: the step; turn: turns since the meeting
     char* st = smem[s & 1];
     if (s < full) {
-      sa.load(st, wave);
-      sb.load(st + TA::BYTES, wave);
-    } else {
+      const uint32_t at = lds_address(st) + wave * 1024;
+#pragma unroll
+      for (int i = turn * PER; i < (turn + 1) * PER && i < LOADS; ++i) {
+        if (i < TA::LOADS) sa.load(i, at);
+        else sb.load(i - TA::LOADS, at + TA::BYTES);
+      }
+    } else if (turn == 0) {
       sa.load_part(st, left, tid);
       sb.load_part(st + TA::BYTES, left, tid);
     }
-    load_scales(st, s);
+    if (turn == 0) load_scales(st, s);
+  };
+  auto next_step = [&] {
+    sa.base += sa.step;
+    sb.base += sb.step;
   };
   Frag af[AT], bf[RING];
   bf16x8_t ax[EXACT ? AT : 1][4];
-  f32x4_t fa[AROW ? AT : 1], z[2];
+  f32x4_t fa[AROW ? AT : 1], z[4];
   float fs[4], s1 = 0.f;                         // a turn's scale is used one turn later too
   static_assert(TURNS % 4 == 0, "turns of a step");
   auto scale_of = [&](const char* st) { return reinterpret_cast<const float*>(st + TA::BYTES + TB::BYTES); };
@@ -311,13 +322,18 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
     const float s = AROW ? fs[n / AT % 4] : s1 * fs[n / AT % 4];
     f32x4_t& o = acc[n % AT][n / AT % BT];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) o[v] = fmaf(z[n & 1][v], AROW ? fa[AROW ? n % AT : 0][v] * s : s, o[v]);
+    for (int v = 0; v < 4; ++v) o[v] = fmaf(z[n & 3][v], AROW ? fa[AROW ? n % AT : 0][v] * s : s, o[v]);
     asm volatile("" : "+v"(o));                  // here, not where the compiler would gather them, with every z kept till then
   };
   if (steps > 0) {
-    load(0);
+#pragma unroll
+    for (int t = 0; t < TURNS; ++t) load(0, t);
+    next_step();
     lin_sync();
-    if (steps > 1) load(1);
+    if (steps > 1) {
+#pragma unroll
+      for (int t = 0; t < AHEAD; ++t) load(1, t);
+    }
 #pragma unroll
     for (int i = 0; i < AT; ++i) af[i] = read_a(smem[0], i, 0);
 #pragma unroll
@@ -338,9 +354,14 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
 #pragma unroll
     for (int t = 0; t < TURNS; ++t) {
       const int j = t % BT;
-      if (t == TURNS - AHEAD && s + 1 < steps) {
-        lin_sync();
-        if (s + 2 < steps) load(s + 2);
+      if (t < TURNS - AHEAD) {
+        if (t + AHEAD < (LOADS + PER - 1) / PER && s + 1 < steps) load(s + 1, t + AHEAD);
+      } else {
+        if (t == TURNS - AHEAD && s + 1 < steps) {
+          lin_sync();
+          next_step();
+        }
+        if (s + 2 < steps) load(s + 2, t - (TURNS - AHEAD));
       }
       // past the last step this reads a stage that nobody writes, for nothing
       if (t + AHEAD < TURNS) fetch_b(st, t + AHEAD);
@@ -361,8 +382,8 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
           } else {
             p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[t % RING], p, 0, 0, 0, 0, 0, 0);
           }
-          z[n & 1] = p;
-          if (n > 0) join(n - 1);
+          z[n & 3] = p;
+          if (n > 2) join(n - 3);
         } else {
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], bf[t % RING], acc[i][j], 0, 0, 0);
         }
@@ -370,6 +391,8 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
         if (j == BT - 1) af[i] = t + 1 < TURNS ? read_a(st, i, t / BT + 1) : read_a(nx, i, 0);
       }
       if (FP8 && t == TURNS - 1) {
+        join(TURNS * AT - 3);
+        join(TURNS * AT - 2);
         join(TURNS * AT - 1);
         fetch_scales(nx);
       }
