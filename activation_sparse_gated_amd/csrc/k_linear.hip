@@ -36,7 +36,6 @@
 
 namespace ffn {
 
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int LIN_THREADS = 512;
@@ -62,14 +61,6 @@ __device__ __forceinline__ void lin_sync() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-}
-
-// Eight e4m3 values as bf16 (exact).
-__device__ __forceinline__ bf16x8_t fp8_to_bf16(uint32_t lo, uint32_t hi) {
-  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-  const bf2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-  const bf2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
-  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // One operand's slice of a step in LDS: R rows of the output's side.
@@ -135,22 +126,6 @@ struct LinSrc {
   }
 };
 
-// Tile of this workgroup: expert g, its rows [lo, hi), first output row r0.
-// Row tiles count expert by expert; false past the last one.
-template <int RT>
-__device__ __forceinline__ bool lin_tile(const LinDesc& d, int tile, int& g, int& lo, int& hi, int& r0) {
-  for (g = 0; g < d.groups; ++g) {
-    expert_rows(d.offsets, g, d.rows, lo, hi);
-    const int t = (hi - lo + RT - 1) / RT;
-    if (tile < t) {
-      r0 = lo + tile * RT;
-      return true;
-    }
-    tile -= t;
-  }
-  return false;
-}
-
 template <int KIND, int RT, bool EXACT, bool AROW>
 __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int ctiles, int rtiles) {
   constexpr bool FP8 = KIND == LIN_FP8;
@@ -180,7 +155,7 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
   const int patch = ins / (PR * sw), inp = ins - patch * PR * sw;
   const int ph = min(PR, rtiles - patch * PR);
   const int rt = patch * PR + inp % ph, c0 = (strip * PC + inp / ph) * LIN_CT;
-  int g, lo, hi, r0, klo = 0, khi = d.K, rend;
+  int g, r0, rend, klo = 0, khi = d.K;
   if constexpr (KIND == LIN_DW) {
     const int per_expert = (d.rows + RT - 1) / RT;
     g = rt / per_expert;
@@ -189,8 +164,7 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
     expert_rows(d.offsets, g, d.K, klo, khi);
     if (d.accumulate && klo == khi) return;
   } else {
-    if (!lin_tile<RT>(d, rt, g, lo, hi, r0)) return;
-    rend = hi;
+    if (!lin_tile<RT>(d, rt, g, r0, rend)) return;
   }
   const char* A = reinterpret_cast<const char*>(d.A) + (KIND == LIN_DW ? 0 : (size_t)g * d.a_group * ESZ);
   LinSrc<LIN_CT, AALONG, ESZ> sa;
@@ -244,7 +218,7 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
     const char* p = t + tile * (16 * LIN_BYTES);
     if constexpr (FP8) {
       const uint4 a = *reinterpret_cast<const uint4*>(p + fo), b = *reinterpret_cast<const uint4*>(p + (fo ^ 16));
-      return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+      return as_i32x8(a, b);
     } else {
       return as_bf16x8(*reinterpret_cast<const uint4*>(p + (fo ^ (kk * 64))));
     }
@@ -400,8 +374,7 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
     }
   }
 
-  const size_t out0 = KIND == LIN_DW ? (size_t)g * d.rows * d.cols : 0;
-  const bool vec = (d.cols & 3) == 0;
+  const int orow = KIND == LIN_DW ? g * d.rows : 0;
 #pragma unroll
   for (int j = 0; j < BT; ++j) {
     const int row = r0 + (wr * BT + j) * 16 + l16;
@@ -409,30 +382,7 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
 #pragma unroll
     for (int i = 0; i < AT; ++i) {
       const int col = c0 + (wc * AT + i) * 16 + 4 * q4;
-      if (col >= d.cols) continue;
-      const size_t at = out0 + (size_t)row * d.cols + col;
-      f32x4_t a = acc[i][j];
-      if (KIND == LIN_DW || d.out_f32) {
-        float* o = reinterpret_cast<float*>(d.out) + at;
-        if (vec) {
-          if (d.accumulate) a += *reinterpret_cast<const f32x4_t*>(o);
-          *reinterpret_cast<f32x4_t*>(o) = a;
-        } else {
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (col + v < d.cols) o[v] = d.accumulate ? o[v] + a[v] : a[v];
-        }
-      } else {
-        uint16_t* o = reinterpret_cast<uint16_t*>(d.out) + at;
-        const uint2 h{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
-        if (vec) {
-          *reinterpret_cast<uint2*>(o) = h;
-        } else {
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (col + v < d.cols) o[v] = (uint16_t)((v < 2 ? h.x : h.y) >> (16 * (v & 1)));
-        }
-      }
+      if (col < d.cols) lin_store(d, 0, orow + row, col, acc[i][j]);
     }
   }
 }
@@ -448,23 +398,49 @@ static hipError_t go_linear(const LinDesc& d, hipStream_t s) {
   return hipGetLastError();
 }
 template <int KIND, bool EXACT = false, bool AROW = false>
-static hipError_t pick_linear(const LinDesc& d, hipStream_t s) {
-  const int rows = KIND == LIN_DW ? d.rows : d.rows / d.groups;
-  if (rows <= 64) return go_linear<KIND, 64, EXACT, AROW>(d, s);
-  if (rows <= 128) return go_linear<KIND, 128, EXACT, AROW>(d, s);
-  if constexpr (EXACT) return go_linear<KIND, 128, EXACT, AROW>(d, s);
-  else return go_linear<KIND, 256, EXACT, AROW>(d, s);
+static hipError_t pick_linear(const LinDesc& d, const LinPlan& p, hipStream_t s) {
+  if (p.rt == 64) return go_linear<KIND, 64, EXACT, AROW>(d, s);
+  if (EXACT || p.rt == 128) return go_linear<KIND, 128, EXACT, AROW>(d, s);
+  if constexpr (!EXACT) return go_linear<KIND, 256, EXACT, AROW>(d, s);
 }
-hipError_t launch_linear(const LinDesc& d, hipStream_t s) {
+hipError_t launch_linear_tiled(const LinDesc& d, const LinPlan& p, hipStream_t s) {
   switch (d.kind) {
     case LIN_FP8:
-      if (d.a_rows == 1) return d.out_f32 ? pick_linear<LIN_FP8, true, true>(d, s) : pick_linear<LIN_FP8, false, true>(d, s);
-      return d.out_f32 ? pick_linear<LIN_FP8, true>(d, s) : pick_linear<LIN_FP8>(d, s);
-    case LIN_FWD: return pick_linear<LIN_FWD>(d, s);
-    case LIN_DX: return pick_linear<LIN_DX>(d, s);
-    case LIN_DW: return pick_linear<LIN_DW>(d, s);
+      if (d.a_rows == 1) return d.out_f32 ? pick_linear<LIN_FP8, true, true>(d, p, s) : pick_linear<LIN_FP8, false, true>(d, p, s);
+      return d.out_f32 ? pick_linear<LIN_FP8, true>(d, p, s) : pick_linear<LIN_FP8>(d, p, s);
+    case LIN_FWD: return pick_linear<LIN_FWD>(d, p, s);
+    case LIN_DX: return pick_linear<LIN_DX>(d, p, s);
+    case LIN_DW: return pick_linear<LIN_DW>(d, p, s);
   }
   return hipErrorInvalidValue;
+}
+
+LinPlan lin_plan(int kind, int rows, int cols, int K, int groups) {
+  LinPlan p{};
+  p.ks = 1;
+  const int per = kind == LIN_DW ? rows : (rows + groups - 1) / groups;   // rows of an expert, if they were even
+  if ((kind == LIN_FP8 || kind == LIN_FWD) && per <= 64) {
+    p.skinny = 1;
+    p.mb = per <= 16 ? 1 : per <= 32 ? 2 : 4;
+    const int cw = p.mb == 1 ? 16 : 32, nb = (K * (kind == LIN_FP8 ? 1 : 2) + 127) / 128;
+    const int rt = (per + 16 * p.mb - 1) / (16 * p.mb) * groups;
+    const long long wgs = (long long)(cols + cw - 1) / cw * rt;
+    p.nw = p.mb == 1 && wgs < 512 && nb >= 32 ? 16 : 8;
+    // slices, where the workgroups leave CUs empty: at least two turns of the waves each
+    while (wgs * p.ks < 256 && p.ks < 16 && nb / (p.ks * 2) >= 2 * p.nw) p.ks *= 2;
+    return p;
+  }
+  p.rt = per <= 64 ? 64 : per <= 128 ? 128 : 256;
+  return p;
+}
+size_t lin_workspace(const LinPlan& p, int rows, int cols) { return p.ks > 1 ? (size_t)p.ks * rows * cols * 4 : 0; }
+
+hipError_t launch_linear(LinDesc d, float* workspace, size_t workspace_bytes, hipStream_t s) {
+  LinPlan p = lin_plan(d.kind, d.rows, d.cols, d.K, d.groups);
+  if (p.ks > 1 && (!workspace || workspace_bytes < lin_workspace(p, d.rows, d.cols))) p.ks = 1;
+  d.ks = p.ks;
+  d.part = workspace;
+  return p.skinny ? launch_linear_skinny(d, p, s) : launch_linear_tiled(d, p, s);
 }
 
 }  // namespace ffn

@@ -96,4 +96,63 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int g, int m
   hi = max(min(max(offsets[g + 1], 0), m), lo);
 }
 
+// Tile `tile` of RT rows: expert g, first output row r0, end of its rows.
+// Tiles count expert by expert; false past the last one.
+template <int RT>
+__device__ __forceinline__ bool lin_tile(const LinDesc& d, int tile, int& g, int& r0, int& rend) {
+  for (g = 0; g < d.groups; ++g) {
+    int lo;
+    expert_rows(d.offsets, g, d.rows, lo, rend);
+    const int t = (rend - lo + RT - 1) / RT;
+    if (tile < t) {
+      r0 = lo + tile * RT;
+      return true;
+    }
+    tile -= t;
+  }
+  return false;
+}
+
+// Four neighbouring outputs (row, col ..): the slab of slice z, or the output,
+// added to what it holds if the product accumulates. Columns past the end are
+// left out; whole 16-byte (8-byte) stores where rows allow.
+__device__ __forceinline__ void lin_store(const LinDesc& d, int z, int row, int col, f32x4_t a) {
+  const bool vec = (d.cols & 3) == 0;
+  if (d.ks > 1 || d.out_f32) {
+    const bool add = d.ks == 1 && d.accumulate;
+    float* o = (d.ks > 1 ? d.part + (size_t)z * d.rows * d.cols : reinterpret_cast<float*>(d.out)) + (size_t)row * d.cols + col;
+    if (vec) {
+      if (add) a += *reinterpret_cast<const f32x4_t*>(o);
+      *reinterpret_cast<f32x4_t*>(o) = a;
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (col + v < d.cols) o[v] = add ? o[v] + a[v] : a[v];
+    }
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(d.out) + (size_t)row * d.cols + col;
+    const uint2 h{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+    if (vec) {
+      *reinterpret_cast<uint2*>(o) = h;
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (col + v < d.cols) o[v] = (uint16_t)((v < 2 ? h.x : h.y) >> (16 * (v & 1)));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- matrix operands
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ i32x8_t as_i32x8(const uint4 a, const uint4 b) {
+  return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+// Eight e4m3 values as bf16 (exact).
+__device__ __forceinline__ bf16x8_t fp8_to_bf16(uint32_t lo, uint32_t hi) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  const bf2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const bf2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 }  // namespace ffn

@@ -53,7 +53,21 @@ struct LinDesc {
   int out_f32, accumulate;
   const float *sa, *sb;          // LIN_FP8: scales of A and B
   int a_rows;                    // LIN_FP8: rows of a block of A, 1 or 128
+  int ks;                        // slices of the contraction; > 1: fp32 slabs part[ks][rows][cols]
+  float* part;
 };
-hipError_t launch_linear(const LinDesc& d, hipStream_t s);
+// How a product is run (lin_plan, a rule on sizes alone).
+struct LinPlan {
+  int skinny;                    // k_linear_skinny, else k_linear
+  int mb, nw;                    // skinny: 16-row blocks of a row tile, waves
+  int rt;                        // k_linear: rows of a tile
+  int ks;                        // slices of the contraction
+};
+LinPlan lin_plan(int kind, int rows, int cols, int K, int groups);
+size_t lin_workspace(const LinPlan& p, int rows, int cols);
+hipError_t launch_linear(LinDesc d, float* workspace, size_t workspace_bytes, hipStream_t s);
+hipError_t launch_linear_tiled(const LinDesc& d, const LinPlan& p, hipStream_t s);
+hipError_t launch_linear_skinny(const LinDesc& d, const LinPlan& p, hipStream_t s);
+hipError_t launch_linear_sum(const LinDesc& d, hipStream_t s);
 
 }  // namespace ffn

@@ -119,7 +119,9 @@ ffn_status ffn_fp8_quantize(const void* x, int32_t dtype, int32_t groups, int32_
   return done(launch_fp8_quant(d, st(stream)));
 }
 
-size_t ffn_fp8_linear_workspace_bytes(int32_t, int32_t, int32_t, int32_t) { return 0; }
+size_t ffn_fp8_linear_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t groups) {
+  return product_shape_ok(m, n, k, groups) && m > 0 ? lin_workspace(lin_plan(LIN_FP8, m, n, k, groups), m, n) : 0;
+}
 
 ffn_status ffn_fp8_linear(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
                           int32_t w_block_rows, int32_t m, int32_t n, int32_t k, const int32_t* offsets, int32_t groups,
@@ -149,10 +151,12 @@ ffn_status ffn_fp8_linear(const uint8_t* x, const float* x_scale, const uint8_t*
   d.sa = w_scale;
   d.sb = x_scale;
   d.a_rows = w_block_rows;
-  return done(launch_linear(d, st(stream)));
+  return done(launch_linear(d, static_cast<float*>(workspace), workspace_bytes, st(stream)));
 }
 
-size_t ffn_grouped_forward_workspace_bytes(int32_t, int32_t, int32_t, int32_t) { return 0; }
+size_t ffn_grouped_forward_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t groups) {
+  return product_shape_ok(m, n, k, groups) && m > 0 ? lin_workspace(lin_plan(LIN_FWD, m, n, k, groups), m, n) : 0;
+}
 
 ffn_status ffn_grouped_forward(const void* x, const void* w, const int32_t* offsets, int32_t groups, int32_t m, int32_t n,
                                int32_t k, void* y, int32_t y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
@@ -171,10 +175,12 @@ ffn_status ffn_grouped_forward(const void* x, const void* w, const int32_t* offs
   d.groups = groups;
   d.out = y;
   d.out_f32 = y_dtype == FFN_F32;
-  return done(launch_linear(d, st(stream)));
+  return done(launch_linear(d, static_cast<float*>(workspace), workspace_bytes, st(stream)));
 }
 
-size_t ffn_grouped_backward_workspace_bytes(int32_t, int32_t, int32_t, int32_t) { return 0; }
+size_t ffn_grouped_backward_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t groups) {
+  return product_shape_ok(m, n, k, groups) && m > 0 ? lin_workspace(lin_plan(LIN_DX, m, k, n, groups), m, k) : 0;
+}
 
 ffn_status ffn_grouped_backward(const void* x, const void* w, const void* dy, const int32_t* offsets, int32_t groups,
                                 int32_t m, int32_t n, int32_t k, void* dx, float* dw, int32_t accumulate, void* workspace,
@@ -199,7 +205,7 @@ ffn_status ffn_grouped_backward(const void* x, const void* w, const void* dy, co
     d.K = n;
     d.a_group = (long long)n * k;
     d.out = dx;
-    const hipError_t e = launch_linear(d, st(stream));
+    const hipError_t e = launch_linear(d, static_cast<float*>(workspace), workspace_bytes, st(stream));
     if (e != hipSuccess) return FFN_E_HIP;
   }
   if (dw) {
@@ -213,7 +219,7 @@ ffn_status ffn_grouped_backward(const void* x, const void* w, const void* dy, co
     d.out = dw;
     d.out_f32 = 1;
     d.accumulate = accumulate;
-    return done(launch_linear(d, st(stream)));
+    return done(launch_linear(d, static_cast<float*>(workspace), workspace_bytes, st(stream)));
   }
   return FFN_OK;
 }
