@@ -1,7 +1,7 @@
 // Products of 8-bit blocks and products grouped by expert on gfx950.
 //
-// out[r][c] = sum_j B[r][j] A[c][j]: a workgroup of eight waves owns an RT x 256
-// tile of the output (RT rows) and walks the contraction in steps of 128 bytes
+// out[r][c] = sum_j B[r][j] A[c][j]: a workgroup of eight waves owns an RT x CT
+// tile of the output (RT rows, CT columns) and walks the contraction in steps of 128 bytes
 // of a row: one 8-bit block, or 64 bf16 elements. Both operands' slices of the
 // next step travel from memory straight into the other of two LDS stages
 // (16-byte loads to LDS, no registers) while the matrix cores work on this
@@ -30,6 +30,7 @@
 // value is a bf16 value, products of two are exact in fp32, and so are their
 // sums to fp32 roundings. A block's sum starts at zero, is scaled in fp32 and
 // added to the accumulator.
+#include <algorithm>
 #include <type_traits>
 
 #include "lin_util.cuh"
@@ -39,7 +40,7 @@ namespace ffn {
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int LIN_THREADS = 512;
-constexpr int LIN_CT = 256;                      // columns of a tile
+constexpr int kCUs = 256;                        // MI355X
 constexpr int LIN_BYTES = 128;                   // contraction bytes of a step
 
 // 16 (or 4) bytes a lane from base + off to LDS: the wave's lanes in order from
@@ -126,87 +127,155 @@ struct LinSrc {
   }
 };
 
-template <int KIND, int RT, bool EXACT, bool AROW>
-__global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int ctiles, int rtiles) {
+template <int KIND, int RT, int CT, bool EXACT, bool AROW>
+__global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_linear(const LinDesc d) {
   constexpr bool FP8 = KIND == LIN_FP8;
   constexpr bool AALONG = KIND == LIN_FP8 || KIND == LIN_FWD, BALONG = KIND != LIN_DW;
   constexpr int ESZ = FP8 ? 1 : 2, BK = LIN_BYTES / ESZ;
   constexpr int WR = RT >= 128 ? 2 : 1, WC = 8 / WR;           // waves along rows and columns
-  constexpr int BT = RT / WR / 16, AT = LIN_CT / WC / 16;      // 16 x 16 tiles of a wave
-  using TA = LinTile<LIN_CT, AALONG>;
+  constexpr int BT = RT / WR / 16, AT = CT / WC / 16;          // 16 x 16 tiles of a wave
+  using TA = LinTile<CT, AALONG>;
   using TB = LinTile<RT, BALONG>;
-  constexpr int SCALES = FP8 ? (RT + LIN_CT) * 4 : 0;
+  constexpr int SCALES = FP8 ? (RT + CT) * 4 : 0;
   constexpr int STAGE = TA::BYTES + TB::BYTES + SCALES;
   __shared__ __attribute__((aligned(16))) char smem[2][STAGE];
+  __shared__ int s_lo[kLinMaxGroups], s_hi[kLinMaxGroups], s_first[kLinMaxGroups];   // rows and first row tile of an expert
+  __shared__ int s_scan[LIN_THREADS / 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wc = wave % WC, wr = wave / WC;
 
-  // Workgroups go to the 8 XCDs in turn: each XCD takes a contiguous run of tiles. Tiles come in patches of 4 row tiles
-  // by 8 column tiles, about what an XCD works on at a time, so that a step's slices are read by 4 or 8 of its
-  // workgroups and come from its L2 but once; patches run down all rows before the next 8 columns, so that the
-  // weights are read about once in all.
-  const int total = ctiles * rtiles, per = (total + 7) / 8;
-  const int lin = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (lin >= total) return;
-  constexpr int PR = 4, PC = 8;
-  const int strip = lin / (PC * rtiles), ins = lin - strip * PC * rtiles;
-  const int sw = min(PC, ctiles - strip * PC);
-  const int patch = ins / (PR * sw), inp = ins - patch * PR * sw;
-  const int ph = min(PR, rtiles - patch * PR);
-  const int rt = patch * PR + inp % ph, c0 = (strip * PC + inp / ph) * LIN_CT;
-  int g, r0, rend, klo = 0, khi = d.K;
-  if constexpr (KIND == LIN_DW) {
-    const int per_expert = (d.rows + RT - 1) / RT;
-    g = rt / per_expert;
-    r0 = rt % per_expert * RT;
-    rend = d.rows;
-    expert_rows(d.offsets, g, d.K, klo, khi);
-    if (d.accumulate && klo == khi) return;
-  } else {
-    if (!lin_tile<RT>(d, rt, g, r0, rend)) return;
+  // ---------------------------------------------------------------- the tiles of this workgroup
+  int rtiles;
+  {
+    int lo = 0, hi = 0;
+    if (tid < d.groups) expert_rows(d.offsets, tid, KIND == LIN_DW ? d.K : d.rows, lo, hi);
+    const int mine = tid >= d.groups ? 0 : ((KIND == LIN_DW ? d.rows : hi - lo) + RT - 1) / RT;
+    const int first = block_excl_scan<LIN_THREADS>(mine, s_scan, &rtiles);
+    rtiles = __builtin_amdgcn_readfirstlane(rtiles);
+    if (tid < kLinMaxGroups) {
+      s_lo[tid] = lo;
+      s_hi[tid] = hi;
+      s_first[tid] = tid < d.groups ? first : 0x7FFFFFFF;
+    }
+    __syncthreads();
   }
-  const char* A = reinterpret_cast<const char*>(d.A) + (KIND == LIN_DW ? 0 : (size_t)g * d.a_group * ESZ);
-  LinSrc<LIN_CT, AALONG, ESZ> sa;
-  LinSrc<RT, BALONG, ESZ> sb;
-  sa.init(A, AALONG ? d.K : d.cols, c0, d.cols, klo, tid);
-  sb.init(reinterpret_cast<const char*>(d.B), BALONG ? d.K : d.rows, r0, rend, klo, tid);
+  const int ctiles = (d.cols + CT - 1) / CT, tiles = ctiles * rtiles;
+  // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of tiles, its workgroups one after the other.
+  // Tiles come in patches of 4 row tiles by 8 column tiles, about what an XCD works on at a time, so that a step's
+  // slices are read by 4 or 8 of its workgroups and come from its L2 but once; patches run down all rows before the
+  // next 8 columns, so that the weights are read about once in all. Slices of the contraction come last.
+  const int total = tiles * d.ks, per = (total + 7) / 8, stride = gridDim.x >> 3;
+  const int run0 = (blockIdx.x & 7) * per, end = min(run0 + per, total), begin = run0 + (blockIdx.x >> 3);
+  struct Tile {
+    int g, r0, rend, c0, z, klo, full, left, steps;
+  };
+  auto tile_at = [&](int at) {
+    constexpr int PR = 4, PC = 8;
+    Tile x;
+    x.z = at / tiles;
+    const int lin = at - x.z * tiles;
+    const int strip = lin / (PC * rtiles), ins = lin - strip * PC * rtiles;
+    const int sw = min(PC, ctiles - strip * PC);
+    const int patch = ins / (PR * sw), inp = ins - patch * PR * sw;
+    const int ph = min(PR, rtiles - patch * PR);
+    const int rt = patch * PR + inp % ph;
+    x.c0 = (strip * PC + inp / ph) * CT;
+    int n = 0;                                   // the last expert that starts at or before row tile rt
+#pragma unroll
+    for (int i = 0; i < kLinMaxGroups / 64; ++i) n += __popcll(ballot64(s_first[i * 64 + lane] <= rt));
+    x.g = n - 1;
+    const int lo = __builtin_amdgcn_readfirstlane(s_lo[x.g]), hi = __builtin_amdgcn_readfirstlane(s_hi[x.g]);
+    const int in = rt - __builtin_amdgcn_readfirstlane(s_first[x.g]);
+    x.r0 = (KIND == LIN_DW ? 0 : lo) + in * RT;
+    x.rend = KIND == LIN_DW ? d.rows : hi;
+    x.klo = KIND == LIN_DW ? lo : 0;
+    const int k = KIND == LIN_DW ? hi - lo : d.K, all = k / BK;
+    // a slice: whole steps, the last one with what is left
+    const int s0 = (int)((long long)all * x.z / d.ks);
+    x.full = (int)((long long)all * (x.z + 1) / d.ks) - s0;
+    x.klo += s0 * BK;
+    x.left = x.z + 1 == d.ks ? k - all * BK : 0;
+    x.steps = x.full + (x.left > 0);
+    return x;
+  };
 
+  // ---------------------------------------------------------------- loads
+  // The cursor: the step whose loads go out, up to two steps ahead of the products and so, at the end of a tile, in
+  // the next one: its first slices arrive while this tile is finished and stored.
+  LinSrc<CT, AALONG, ESZ> sa;
+  LinSrc<RT, BALONG, ESZ> sb;
+  int cat = begin - stride, cstep = 0, cfull = 0, cleft = 0, ckb = 0;
+  bool more = true;
   // 8-bit blocks: the step's scales travel with it, one float a row of B (threads 0 .. RT - 1) and a column of the
-  // tile (the next 256 threads; with blocks of 128 rows of A, columns of a block all get its scale)
-  static_assert(RT + LIN_CT <= LIN_THREADS, "one scale a thread");
+  // tile (the next CT threads; with blocks of 128 rows of A, columns of a block all get its scale)
+  static_assert(RT + CT <= LIN_THREADS, "one scale a thread");
   const int kblocks = (d.K + kFp8Block - 1) / kFp8Block;
   const char *scb = nullptr, *sca = nullptr;
-  size_t sca_step = 0;
+  const size_t sca_step = AROW ? (size_t)d.cols * 4 : 4;
   uint32_t scoff = 0;
-  if constexpr (FP8) {
-    scb = reinterpret_cast<const char*>(d.sb + r0);
-    const int c = tid - RT;
-    if constexpr (AROW) {
-      sca = reinterpret_cast<const char*>(d.sa + c0);
-      sca_step = (size_t)d.cols * 4;
-      scoff = (uint32_t)min(c, d.cols - 1 - c0) * 4;
-    } else {
-      sca = reinterpret_cast<const char*>(d.sa + ((size_t)g * ((d.cols + kFp8Block - 1) / kFp8Block) + c0 / kFp8Block) * kblocks);
-      sca_step = 4;
-      scoff = (uint32_t)(min(c, d.cols - 1 - c0) / kFp8Block * kblocks) * 4;
-    }
-    if (c < 0) scoff = (uint32_t)min(tid, rend - 1 - r0) * 4;
-  }
-  auto load_scales = [&](const char* st, int kb) {
+  auto advance = [&] {
+    sa.base += sa.step;
+    sb.base += sb.step;
+    if (++cstep < cfull + (cleft > 0)) return;
+    Tile x;
+    do {
+      cat += stride;
+      more = cat < end;
+      if (!more) return;
+      x = tile_at(cat);
+    } while (x.steps == 0);
+    cstep = 0;
+    cfull = x.full;
+    cleft = x.left;
+    const char* A = reinterpret_cast<const char*>(d.A) + (KIND == LIN_DW ? 0 : (size_t)x.g * d.a_group * ESZ);
+    sa.init(A, AALONG ? d.K : d.cols, x.c0, d.cols, x.klo, tid);
+    sb.init(reinterpret_cast<const char*>(d.B), BALONG ? d.K : d.rows, x.r0, x.rend, x.klo, tid);
     if constexpr (FP8) {
-      const uint32_t at = lds_address(st) + TA::BYTES + TB::BYTES + wave * 256;
-      if (wave * 64 < RT) lds_load4(scb + (size_t)kb * d.rows * 4, scoff, at);
-      else if (wave * 64 < RT + LIN_CT) lds_load4(sca + (size_t)kb * sca_step, scoff, at);
+      ckb = x.klo / BK;
+      scb = reinterpret_cast<const char*>(d.sb + x.r0);
+      const int c = min(tid - RT, d.cols - 1 - x.c0);
+      if constexpr (AROW) {
+        sca = reinterpret_cast<const char*>(d.sa + x.c0);
+        scoff = (uint32_t)c * 4;
+      } else {
+        sca = reinterpret_cast<const char*>(d.sa + ((size_t)x.g * ((d.cols + kFp8Block - 1) / kFp8Block) + x.c0 / kFp8Block) * kblocks);
+        scoff = (uint32_t)(c / kFp8Block * kblocks) * 4;
+      }
+      if (tid < RT) scoff = (uint32_t)min(tid, x.rend - 1 - x.r0) * 4;
     }
   };
 
-  f32x4_t acc[AT][BT];
+  // The steps. A step is KK * BT turns of AT matrix instructions (of AT * 4 for an exact sum); the operand of turn
+  // t + AHEAD is read during turn t, A's next slice in the last turn that uses this one, so that the reads of a step
+  // are all behind it AHEAD turns before its end. There the workgroup meets: the next step has arrived, nobody reads
+  // this step's stage any more, and the loads of the step after the next go into it. They go out a few a turn over
+  // half a step: the address unit takes 16 cycles for each, and a wave that finds its queue full stands still, matrix
+  // instructions and all.
+  constexpr int KK = FP8 ? 1 : 2, TURNS = KK * BT, AHEAD = FP8 ? 1 : 3, RING = AHEAD + 1;
+  static_assert(TURNS % RING == 0 && TURNS > AHEAD && TURNS % 4 == 0, "turns of a step");
+  constexpr int LOADS = TA::LOADS + TB::LOADS, PER = (LOADS + TURNS / 2 - 1) / (TURNS / 2), LTURNS = (LOADS + PER - 1) / PER;
+  auto load = [&](char* st, int turn) {          // turn: turns since the meeting
+    if (cstep < cfull) {
+      const uint32_t at = lds_address(st) + wave * 1024;
 #pragma unroll
-  for (int i = 0; i < AT; ++i)
-#pragma unroll
-    for (int j = 0; j < BT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int i = turn * PER; i < (turn + 1) * PER && i < LOADS; ++i) {
+        if (i < TA::LOADS) sa.load(i, at);
+        else sb.load(i - TA::LOADS, at + TA::BYTES);
+      }
+    } else if (turn == 0) {
+      sa.load_part(st, cleft, tid);
+      sb.load_part(st + TA::BYTES, cleft, tid);
+    }
+    if (FP8 && turn == 0) {
+      const uint32_t at = lds_address(st) + TA::BYTES + TB::BYTES + wave * 256;
+      const size_t kb = ckb + cstep;
+      if (wave * 64 < RT) lds_load4(scb + kb * d.rows * 4, scoff, at);
+      else if (wave * 64 < RT + CT) lds_load4(sca + kb * sca_step, scoff, at);
+    }
+  };
 
+  // ---------------------------------------------------------------- operands and sums
   const int l16 = lane & 15, q4 = lane >> 4;
   // operand reads of a 16-row tile. Along the contraction: bf16 chunk 4 kk + q4, or the 8-bit chunks 2 q4 and 2 q4 + 1,
   // whose places differ in the lowest bit; the tile's rows are l16 modulo 16, so the places are those of row l16.
@@ -237,47 +306,20 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
   };
   auto read_a = [&](const char* st, int i, int kk) -> Frag {
     if constexpr (AALONG) return along(st, wc * AT + i, kk);
-    else return across(std::integral_constant<int, LIN_CT>{}, st, wc * AT + i, kk);
+    else return across(std::integral_constant<int, CT>{}, st, wc * AT + i, kk);
   };
   auto read_b = [&](const char* st, int j, int kk) -> Frag {
     if constexpr (BALONG) return along(st + TA::BYTES, wr * BT + j, kk);
     else return across(std::integral_constant<int, RT>{}, st + TA::BYTES, wr * BT + j, kk);
   };
-
-  // The steps. A step is KK * BT turns of AT matrix instructions (of AT * 4 for an exact sum); the operand of turn
-  // t + AHEAD is read during turn t, A's next slice in the last turn that uses this one, so that the reads of a step
-  // are all behind it AHEAD turns before its end. There the workgroup meets: the next step has arrived, nobody reads
-  // this step's stage any more, and the loads of the step after the next go into it.
-  constexpr int KK = FP8 ? 1 : 2, TURNS = KK * BT, AHEAD = FP8 ? 1 : 3, RING = AHEAD + 1;
-  static_assert(TURNS % RING == 0 && TURNS > AHEAD, "turns of a step");
-  const int full = (khi - klo) / BK, left = (khi - klo) - full * BK, steps = full + (left > 0);
-  // A step's loads go out a few a turn over half a step, from the meeting on: the address unit takes 16 cycles for each,
-  // and a wave that finds its queue full stands still, matrix instructions and all.
-  constexpr int LOADS = TA::LOADS + TB::LOADS, PER = (LOADS + TURNS / 2 - 1) / (TURNS / 2);
-  auto load = [&](int s, int turn) {             // s: the step; turn: turns since the meeting
-    char* st = smem[s & 1];
-    if (s < full) {
-      const uint32_t at = lds_address(st) + wave * 1024;
-#pragma unroll
-      for (int i = turn * PER; i < (turn + 1) * PER && i < LOADS; ++i) {
-        if (i < TA::LOADS) sa.load(i, at);
-        else sb.load(i - TA::LOADS, at + TA::BYTES);
-      }
-    } else if (turn == 0) {
-      sa.load_part(st, left, tid);
-      sb.load_part(st + TA::BYTES, left, tid);
-    }
-    if (turn == 0) load_scales(st, s);
-  };
-  auto next_step = [&] {
-    sa.base += sa.step;
-    sb.base += sb.step;
-  };
+  // the block's sum of matrix instruction n (turn n / AT, column tile n % AT) joins the accumulator, three instructions
+  // later: its result takes that long (an exact sum's four are one behind)
+  constexpr int LATER = EXACT ? 1 : 3;
+  static_assert(TURNS * AT > LATER, "instructions of a step");
   Frag af[AT], bf[RING];
   bf16x8_t ax[EXACT ? AT : 1][4];
-  f32x4_t fa[AROW ? AT : 1], z[4];
+  f32x4_t acc[AT][BT], fa[AROW ? AT : 1], z[LATER + 1];
   float fs[4], s1 = 0.f;                         // a turn's scale is used one turn later too
-  static_assert(TURNS % 4 == 0, "turns of a step");
   auto scale_of = [&](const char* st) { return reinterpret_cast<const float*>(st + TA::BYTES + TB::BYTES); };
   auto fetch_b = [&](const char* st, int t) {
     bf[t % RING] = read_b(st, t % BT, t / BT);
@@ -291,22 +333,27 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
       s1 = scale_of(st)[RT + wc * AT * 16];
     }
   };
-  // the block's sum of matrix instruction n (turn n / AT, column tile n % AT) joins the accumulator
   auto join = [&](int n) {
     const float s = AROW ? fs[n / AT % 4] : s1 * fs[n / AT % 4];
     f32x4_t& o = acc[n % AT][n / AT % BT];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) o[v] = fmaf(z[n & 3][v], AROW ? fa[AROW ? n % AT : 0][v] * s : s, o[v]);
+    for (int v = 0; v < 4; ++v) o[v] = fmaf(z[n % (LATER + 1)][v], AROW ? fa[AROW ? n % AT : 0][v] * s : s, o[v]);
     asm volatile("" : "+v"(o));                  // here, not where the compiler would gather them, with every z kept till then
   };
-  if (steps > 0) {
+
+  // ---------------------------------------------------------------- the walk
+  cstep = -1;
+  sa.step = sb.step = 0;
+  sa.base = sb.base = nullptr;
+  advance();
+  if (more) {
 #pragma unroll
-    for (int t = 0; t < TURNS; ++t) load(0, t);
-    next_step();
+    for (int t = 0; t < LTURNS; ++t) load(smem[0], t);
     lin_sync();
-    if (steps > 1) {
+    advance();
+    if (more) {
 #pragma unroll
-      for (int t = 0; t < AHEAD; ++t) load(1, t);
+      for (int t = 0; t < AHEAD && t < LTURNS; ++t) load(smem[1], t);
     }
 #pragma unroll
     for (int i = 0; i < AT; ++i) af[i] = read_a(smem[0], i, 0);
@@ -314,94 +361,104 @@ __global__ __launch_bounds__(LIN_THREADS) void k_linear(const LinDesc d, int cti
     for (int t = 0; t < AHEAD; ++t) fetch_b(smem[0], t);
     fetch_scales(smem[0]);
   }
-  for (int s = 0; s < steps; ++s) {
-    const char* st = smem[s & 1];
-    const char* nx = smem[(s & 1) ^ 1];
-    if constexpr (FP8) {
+  int par = 0;
+  for (int at = begin; at < end; at += stride) {
+    const Tile x = tile_at(at);
+#pragma unroll
+    for (int i = 0; i < AT; ++i)
+#pragma unroll
+      for (int j = 0; j < BT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < x.steps; ++s, par ^= 1) {
+      char* st = smem[par];
+      char* nx = smem[par ^ 1];
       if constexpr (EXACT) {
 #pragma unroll
         for (int i = 0; i < AT; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) ax[i][e] = fp8_to_bf16(af[i][2 * e], af[i][2 * e + 1]);
       }
-    }
 #pragma unroll
-    for (int t = 0; t < TURNS; ++t) {
-      const int j = t % BT;
-      if (t < TURNS - AHEAD) {
-        if (t + AHEAD < (LOADS + PER - 1) / PER && s + 1 < steps) load(s + 1, t + AHEAD);
-      } else {
-        if (t == TURNS - AHEAD && s + 1 < steps) {
-          lin_sync();
-          next_step();
+      for (int t = 0; t < TURNS; ++t) {
+        const int j = t % BT;
+        if (t < TURNS - AHEAD) {
+          if (t + AHEAD < LTURNS && more) load(nx, t + AHEAD);
+        } else {
+          if (t == TURNS - AHEAD && more) {
+            lin_sync();
+            advance();
+          }
+          if (t - (TURNS - AHEAD) < LTURNS && more) load(st, t - (TURNS - AHEAD));
         }
-        if (s + 2 < steps) load(s + 2, t - (TURNS - AHEAD));
-      }
-      // past the last step this reads a stage that nobody writes, for nothing
-      if (t + AHEAD < TURNS) fetch_b(st, t + AHEAD);
-      else fetch_b(nx, t + AHEAD - TURNS);
-      bf16x8_t bx[4];
-      if constexpr (EXACT) {
+        // past the last step of all this reads a stage that nobody writes, for nothing
+        if (t + AHEAD < TURNS) fetch_b(st, t + AHEAD);
+        else fetch_b(nx, t + AHEAD - TURNS);
+        bf16x8_t bx[4];
+        if constexpr (EXACT) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) bx[e] = fp8_to_bf16(bf[t % RING][2 * e], bf[t % RING][2 * e + 1]);
+          for (int e = 0; e < 4; ++e) bx[e] = fp8_to_bf16(bf[t % RING][2 * e], bf[t % RING][2 * e + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+          if constexpr (FP8) {
+            const int n = t * AT + i;
+            f32x4_t p{0.f, 0.f, 0.f, 0.f};
+            if constexpr (EXACT) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[i][e], bx[e], p, 0, 0, 0);
+            } else {
+              p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[t % RING], p, 0, 0, 0, 0, 0, 0);
+            }
+            z[n % (LATER + 1)] = p;
+            if (n >= LATER) join(n - LATER);
+          } else {
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], bf[t % RING], acc[i][j], 0, 0, 0);
+          }
+          if (FP8 || j == BT - 1) __builtin_amdgcn_sched_barrier(0);
+          if (j == BT - 1) af[i] = t + 1 < TURNS ? read_a(st, i, t / BT + 1) : read_a(nx, i, 0);
+        }
+        if (FP8 && t == TURNS - 1) {
+#pragma unroll
+          for (int n = TURNS * AT - LATER; n < TURNS * AT; ++n) join(n);
+          fetch_scales(nx);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
+    }
+    if (KIND == LIN_DW && x.steps == 0 && d.accumulate) continue;
+    const int orow = KIND == LIN_DW ? x.g * d.rows : 0;
+#pragma unroll
+    for (int j = 0; j < BT; ++j) {
+      const int row = x.r0 + (wr * BT + j) * 16 + l16;
+      if (row >= x.rend) continue;
 #pragma unroll
       for (int i = 0; i < AT; ++i) {
-        if constexpr (FP8) {
-          const int n = t * AT + i;
-          f32x4_t p{0.f, 0.f, 0.f, 0.f};
-          if constexpr (EXACT) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[i][e], bx[e], p, 0, 0, 0);
-          } else {
-            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[t % RING], p, 0, 0, 0, 0, 0, 0);
-          }
-          z[n & 3] = p;
-          if (n > 2) join(n - 3);
-        } else {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], bf[t % RING], acc[i][j], 0, 0, 0);
-        }
-        if (FP8 || j == BT - 1) __builtin_amdgcn_sched_barrier(0);
-        if (j == BT - 1) af[i] = t + 1 < TURNS ? read_a(st, i, t / BT + 1) : read_a(nx, i, 0);
+        const int col = x.c0 + (wc * AT + i) * 16 + 4 * q4;
+        if (col < d.cols) lin_store(d, x.z, orow + row, col, acc[i][j]);
       }
-      if (FP8 && t == TURNS - 1) {
-        join(TURNS * AT - 3);
-        join(TURNS * AT - 2);
-        join(TURNS * AT - 1);
-        fetch_scales(nx);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-
-  const int orow = KIND == LIN_DW ? g * d.rows : 0;
-#pragma unroll
-  for (int j = 0; j < BT; ++j) {
-    const int row = r0 + (wr * BT + j) * 16 + l16;
-    if (row >= rend) continue;
-#pragma unroll
-    for (int i = 0; i < AT; ++i) {
-      const int col = c0 + (wc * AT + i) * 16 + 4 * q4;
-      if (col < d.cols) lin_store(d, 0, orow + row, col, acc[i][j]);
     }
   }
 }
 
-template <int KIND, int RT, bool EXACT, bool AROW>
+template <int KIND, int RT, int CT, bool EXACT, bool AROW>
 static hipError_t go_linear(const LinDesc& d, hipStream_t s) {
-  const int ct = (d.cols + LIN_CT - 1) / LIN_CT;
-  // row tiles of every expert at most: whole ones, and one ragged one each
+  // as many workgroups as run at once (what their LDS allows), or as there are tiles at most: whole ones, and one
+  // ragged one for each expert
+  constexpr int OCC = RT * CT >= 128 * 256 ? 1 : RT * CT >= 128 * 128 ? 2 : 3;
+  const long long ct = (d.cols + CT - 1) / CT;
   const long long rt = KIND == LIN_DW ? (long long)(d.rows + RT - 1) / RT * d.groups : d.rows / RT + d.groups;
-  const long long wgs = (ct * rt + 7) / 8 * 8;
-  if (wgs > 0x7FFFFFF0ll) return hipErrorInvalidValue;
-  ffn_launch((k_linear<KIND, RT, EXACT, AROW>), dim3((unsigned)wgs), dim3(LIN_THREADS), 0, s, d, ct, (int)rt);
-  return hipGetLastError();
+  const long long wgs = std::min<long long>(ct * rt * d.ks, kCUs * OCC);
+  if (ct * rt * d.ks > 0x3FFFFFFF) return hipErrorInvalidValue;
+  ffn_launch((k_linear<KIND, RT, CT, EXACT, AROW>), dim3((unsigned)(wgs + 7) / 8 * 8), dim3(LIN_THREADS), 0, s, d);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || d.ks == 1) return e;
+  return launch_linear_sum(d, s);
 }
 template <int KIND, bool EXACT = false, bool AROW = false>
 static hipError_t pick_linear(const LinDesc& d, const LinPlan& p, hipStream_t s) {
-  if (p.rt == 64) return go_linear<KIND, 64, EXACT, AROW>(d, s);
-  if (EXACT || p.rt == 128) return go_linear<KIND, 128, EXACT, AROW>(d, s);
-  if constexpr (!EXACT) return go_linear<KIND, 256, EXACT, AROW>(d, s);
+  if (p.rt == 64) return go_linear<KIND, 64, 128, EXACT, AROW>(d, s);
+  if (p.rt == 128 && p.ct == 128) return go_linear<KIND, 128, 128, EXACT, AROW>(d, s);
+  if constexpr (EXACT) return go_linear<KIND, 128, 256, EXACT, AROW>(d, s);
+  else return p.rt == 128 ? go_linear<KIND, 128, 256, EXACT, AROW>(d, s) : go_linear<KIND, 256, 256, EXACT, AROW>(d, s);
 }
 hipError_t launch_linear_tiled(const LinDesc& d, const LinPlan& p, hipStream_t s) {
   switch (d.kind) {
@@ -431,6 +488,7 @@ LinPlan lin_plan(int kind, int rows, int cols, int K, int groups) {
     return p;
   }
   p.rt = per <= 64 ? 64 : per <= 128 ? 128 : 256;
+  p.ct = p.rt == 64 ? 128 : 256;
   return p;
 }
 size_t lin_workspace(const LinPlan& p, int rows, int cols) { return p.ks > 1 ? (size_t)p.ks * rows * cols * 4 : 0; }

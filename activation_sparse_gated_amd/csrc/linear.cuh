@@ -60,7 +60,7 @@ struct LinDesc {
 struct LinPlan {
   int skinny;                    // k_linear_skinny, else k_linear
   int mb, nw;                    // skinny: 16-row blocks of a row tile, waves
-  int rt;                        // k_linear: rows of a tile
+  int rt, ct;                    // k_linear: rows and columns of a tile
   int ks;                        // slices of the contraction
 };
 LinPlan lin_plan(int kind, int rows, int cols, int K, int groups);
