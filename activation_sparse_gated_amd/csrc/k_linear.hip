@@ -54,6 +54,9 @@ __device__ __forceinline__ uint32_t lds_address(const char* l) {
 __device__ __forceinline__ void lds_load16(const char* base, uint32_t off, uint32_t l) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(l), "v"(off), "s"(base) : "m0");
 }
+__device__ __forceinline__ void lds_load16(const char* p, uint32_t l) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(l), "v"(p) : "m0");
+}
 __device__ __forceinline__ void lds_load4(const char* base, uint32_t off, uint32_t l) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(l), "v"(off), "s"(base) : "m0");
 }
@@ -63,6 +66,8 @@ __device__ __forceinline__ void lin_sync() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+
+__device__ const uint4 lin_zero = {0, 0, 0, 0};  // what lies behind the contraction's end
 
 // One operand's slice of a step in LDS: R rows of the output's side.
 // ALONG: rows of 128 bytes along the contraction; otherwise 64 contraction
@@ -114,16 +119,12 @@ struct LinSrc {
     asm volatile("" : "+v"(o));                  // made here, not kept (as a 64-bit pair) over the loop
     lds_load16(base, ALONG ? min(o, last) : o, at + i * LIN_THREADS * 16);
   }
-  // The last, partial step: `left` contraction elements, zeros behind them.
-  __device__ __forceinline__ void load_part(char* lds, int left, int tid) {
-#pragma unroll 1
-    for (int i = 0; i < T::LOADS; ++i) {
-      const int q = i * LIN_THREADS + tid;
-      const bool ok = ALONG ? T::chunk_of(q) * (16 / ESZ) < left : T::row_of(q) < left;
-      uint4 v{0, 0, 0, 0};
-      if (ok) v = ldg16(base + (ALONG ? min(first + i * stride, last) : first + i * stride));
-      *reinterpret_cast<uint4*>(lds + q * 16) = v;
-    }
+  // load i of the last, partial step: `left` contraction elements, zeros behind them
+  __device__ __forceinline__ void load_part(int i, uint32_t at, int left, int tid) const {
+    const int q = i * LIN_THREADS + tid;
+    const bool in = ALONG ? T::chunk_of(q) * (16 / ESZ) < left : T::row_of(q) < left;
+    const uint32_t o = first + i * stride;
+    lds_load16(in ? base + (ALONG ? min(o, last) : o) : reinterpret_cast<const char*>(&lin_zero), at + i * LIN_THREADS * 16);
   }
 };
 
@@ -162,16 +163,16 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
   }
   const int ctiles = (d.cols + CT - 1) / CT, tiles = ctiles * rtiles;
   // Workgroups go to the 8 XCDs in turn; each XCD takes a contiguous run of tiles, its workgroups one after the other.
-  // Tiles come in patches of 4 row tiles by 8 column tiles, about what an XCD works on at a time, so that a step's
-  // slices are read by 4 or 8 of its workgroups and come from its L2 but once; patches run down all rows before the
-  // next 8 columns, so that the weights are read about once in all. Slices of the contraction come last.
+  // Tiles come in patches of 8 row tiles by 4 column tiles, about what an XCD works on at a time, so that a step's
+  // slices are read by 8 or 4 of its workgroups and come from its L2 but once; patches run down all rows before the
+  // next 4 columns, so that the weights are read about once in all. Slices of the contraction come last.
   const int total = tiles * d.ks, per = (total + 7) / 8, stride = gridDim.x >> 3;
   const int run0 = (blockIdx.x & 7) * per, end = min(run0 + per, total), begin = run0 + (blockIdx.x >> 3);
   struct Tile {
     int g, r0, rend, c0, z, klo, full, left, steps;
   };
   auto tile_at = [&](int at) {
-    constexpr int PR = 4, PC = 8;
+    constexpr int PR = 8, PC = 4;
     Tile x;
     x.z = at / tiles;
     const int lin = at - x.z * tiles;
@@ -256,22 +257,23 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
   static_assert(TURNS % RING == 0 && TURNS > AHEAD && TURNS % 4 == 0, "turns of a step");
   constexpr int LOADS = TA::LOADS + TB::LOADS, PER = (LOADS + TURNS / 2 - 1) / (TURNS / 2), LTURNS = (LOADS + PER - 1) / PER;
   auto load = [&](char* st, int turn) {          // turn: turns since the meeting
-    if (cstep < cfull) {
-      const uint32_t at = lds_address(st) + wave * 1024;
+    const uint32_t at = lds_address(st) + wave * 1024;
+    const bool whole = cstep < cfull;
 #pragma unroll
-      for (int i = turn * PER; i < (turn + 1) * PER && i < LOADS; ++i) {
-        if (i < TA::LOADS) sa.load(i, at);
-        else sb.load(i - TA::LOADS, at + TA::BYTES);
+    for (int i = turn * PER; i < (turn + 1) * PER && i < LOADS; ++i) {
+      if (i < TA::LOADS) {
+        if (whole) sa.load(i, at);
+        else sa.load_part(i, at, cleft, tid);
+      } else {
+        if (whole) sb.load(i - TA::LOADS, at + TA::BYTES);
+        else sb.load_part(i - TA::LOADS, at + TA::BYTES, cleft, tid);
       }
-    } else if (turn == 0) {
-      sa.load_part(st, cleft, tid);
-      sb.load_part(st + TA::BYTES, cleft, tid);
     }
     if (FP8 && turn == 0) {
-      const uint32_t at = lds_address(st) + TA::BYTES + TB::BYTES + wave * 256;
+      const uint32_t sat = lds_address(st) + TA::BYTES + TB::BYTES + wave * 256;
       const size_t kb = ckb + cstep;
-      if (wave * 64 < RT) lds_load4(scb + kb * d.rows * 4, scoff, at);
-      else if (wave * 64 < RT + CT) lds_load4(sca + kb * sca_step, scoff, at);
+      if (wave * 64 < RT) lds_load4(scb + kb * d.rows * 4, scoff, sat);
+      else if (wave * 64 < RT + CT) lds_load4(sca + kb * sca_step, scoff, sat);
     }
   };
 
@@ -426,6 +428,14 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
     }
     if (KIND == LIN_DW && x.steps == 0 && d.accumulate) continue;
     const int orow = KIND == LIN_DW ? x.g * d.rows : 0;
+    if (x.r0 + RT <= x.rend && x.c0 + CT <= d.cols && (d.cols & 3) == 0 && !(d.accumulate && d.ks == 1)) {
+#pragma unroll
+      for (int j = 0; j < BT; ++j)
+#pragma unroll
+        for (int i = 0; i < AT; ++i)
+          lin_store4<KIND == LIN_DW>(d, x.z, orow + x.r0 + (wr * BT + j) * 16 + l16, x.c0 + (wc * AT + i) * 16 + 4 * q4, acc[i][j]);
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < BT; ++j) {
       const int row = x.r0 + (wr * BT + j) * 16 + l16;

@@ -113,32 +113,31 @@ __device__ __forceinline__ bool lin_tile(const LinDesc& d, int tile, int& g, int
   return false;
 }
 
-// Four neighbouring outputs (row, col ..): the slab of slice z, or the output,
-// added to what it holds if the product accumulates. Columns past the end are
-// left out; whole 16-byte (8-byte) stores where rows allow.
+// Four neighbouring outputs (row, col ..) in one store of 16 (bf16: 8) bytes:
+// to the slab of slice z, or to the output. d.cols is a multiple of 4.
+template <bool F32 = false>                      // fp32, one slice
+__device__ __forceinline__ void lin_store4(const LinDesc& d, int z, int row, int col, f32x4_t a) {
+  const size_t at = (size_t)row * d.cols + col;
+  if (!F32 && d.ks > 1) *reinterpret_cast<f32x4_t*>(d.part + (size_t)z * d.rows * d.cols + at) = a;
+  else if (F32 || d.out_f32) *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(d.out) + at) = a;
+  else *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(d.out) + at) = uint2{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+}
+// The same, added to what the output holds if the product accumulates; columns
+// past the end are left out.
 __device__ __forceinline__ void lin_store(const LinDesc& d, int z, int row, int col, f32x4_t a) {
-  const bool vec = (d.cols & 3) == 0;
-  if (d.ks > 1 || d.out_f32) {
-    const bool add = d.ks == 1 && d.accumulate;
-    float* o = (d.ks > 1 ? d.part + (size_t)z * d.rows * d.cols : reinterpret_cast<float*>(d.out)) + (size_t)row * d.cols + col;
-    if (vec) {
-      if (add) a += *reinterpret_cast<const f32x4_t*>(o);
-      *reinterpret_cast<f32x4_t*>(o) = a;
-    } else {
+  const bool add = d.ks == 1 && d.accumulate;
+  const size_t at = (size_t)row * d.cols + col;
+  float* f = (d.ks > 1 ? d.part + (size_t)z * d.rows * d.cols : reinterpret_cast<float*>(d.out)) + at;
+  if ((d.cols & 3) == 0) {
+    if (add) a += *reinterpret_cast<const f32x4_t*>(f);
+    lin_store4(d, z, row, col, a);
+    return;
+  }
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (col + v < d.cols) o[v] = add ? o[v] + a[v] : a[v];
-    }
-  } else {
-    uint16_t* o = reinterpret_cast<uint16_t*>(d.out) + (size_t)row * d.cols + col;
-    const uint2 h{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
-    if (vec) {
-      *reinterpret_cast<uint2*>(o) = h;
-    } else {
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (col + v < d.cols) o[v] = (uint16_t)((v < 2 ? h.x : h.y) >> (16 * (v & 1)));
-    }
+  for (int v = 0; v < 4; ++v) {
+    if (col + v >= d.cols) break;
+    if (d.ks > 1 || d.out_f32) f[v] = add ? f[v] + a[v] : a[v];
+    else reinterpret_cast<uint16_t*>(d.out)[at + v] = (uint16_t)pack_bf16(a[v], 0.f);
   }
 }
 
