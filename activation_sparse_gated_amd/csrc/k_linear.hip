@@ -316,12 +316,13 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
   };
   // the block's sum of matrix instruction n (turn n / AT, column tile n % AT) joins the accumulator, three instructions
   // later: its result takes that long (an exact sum's four are one behind)
-  constexpr int LATER = EXACT ? 1 : 3;
-  static_assert(TURNS * AT > LATER, "instructions of a step");
+  constexpr int LATER = EXACT ? 1 : AT == 1 ? 2 : 3;
+  // a turn's scale is replaced three turns later, before that turn's joins
+  static_assert(TURNS * AT > LATER && (LATER + AT - 1) / AT <= 2, "instructions of a step");
   Frag af[AT], bf[RING];
   bf16x8_t ax[EXACT ? AT : 1][4];
   f32x4_t acc[AT][BT], fa[AROW ? AT : 1], z[LATER + 1];
-  float fs[4], s1 = 0.f;                         // a turn's scale is used one turn later too
+  float fs[4], s1 = 0.f;
   auto scale_of = [&](const char* st) { return reinterpret_cast<const float*>(st + TA::BYTES + TB::BYTES); };
   auto fetch_b = [&](const char* st, int t) {
     bf[t % RING] = read_b(st, t % BT, t / BT);
@@ -482,14 +483,35 @@ hipError_t launch_linear_tiled(const LinDesc& d, const LinPlan& p, hipStream_t s
   return hipErrorInvalidValue;
 }
 
-LinPlan lin_plan(int kind, int rows, int cols, int K, int groups) {
+// Which kernel, tile and slices, by the time that each would take, in
+// microseconds: what a CU spends on a step of a tile (measured over whole
+// rounds of large products, 8-bit / exact 8-bit / bf16), what a workgroup that
+// has its CU for itself needs for one at least (latency), what a tile costs
+// besides, and the slabs of a sliced product, written and read at 4 TB/s, with
+// their kernel. How the rows are spread over the experts only the device
+// knows: half a tile of each expert is taken to be empty, at least. A product too small for the chip ends up in small tiles and
+// slices (200 x 4096 x 14336: 256-row tiles 155 us, 128 x 128 in 4 slices 30),
+// a large one in large tiles (4096 x 4096 x 8192: 124 us, 128 x 128 168).
+LinPlan lin_plan(int kind, int exact, int rows, int cols, int K, int groups) {
+  struct Option {
+    int rt, ct, occ;
+    float step[3], tile;
+  };
+  static const Option options[] = {{256, 256, 1, {1.70f, 1e9f, 1.61f}, 7.f},
+                                   {128, 256, 1, {1.07f, 1.98f, 0.98f}, 5.f},
+                                   {128, 128, 2, {0.60f, 1.09f, 0.52f}, 2.5f},
+                                   {64, 128, 3, {0.46f, 0.69f, 0.33f}, 1.7f}};
+  constexpr float kLone = 0.6f, kSlabRate = 4e6f, kSlabLaunch = 5.f;   // us, bytes per us, us
   LinPlan p{};
   p.ks = 1;
-  const int per = kind == LIN_DW ? rows : (rows + groups - 1) / groups;   // rows of an expert, if they were even
-  if ((kind == LIN_FP8 || kind == LIN_FWD) && per <= 64) {
+  const int per = kind == LIN_DW ? rows : (rows + groups - 1) / groups, bytes = kind == LIN_FP8 ? 1 : 2;
+  // Few rows: k_linear_skinny up to 16; up to 32 while the weights are few enough for latency to count (24 rows of five
+  // experts: 21 MB 13.5 us, 64 x 128 tiles 14.2; 587 MB 167 us, tiles 127)
+  const double weights = (double)groups * cols * K * bytes;
+  if ((kind == LIN_FP8 || kind == LIN_FWD) && (per <= 16 || (per <= 32 && weights <= 48e6))) {
     p.skinny = 1;
-    p.mb = per <= 16 ? 1 : per <= 32 ? 2 : 4;
-    const int cw = p.mb == 1 ? 16 : 32, nb = (K * (kind == LIN_FP8 ? 1 : 2) + 127) / 128;
+    p.mb = per <= 16 ? 1 : 2;
+    const int cw = p.mb == 1 || exact ? 16 : 32, nb = (K * bytes + 127) / 128;
     const int rt = (per + 16 * p.mb - 1) / (16 * p.mb) * groups;
     const long long wgs = (long long)(cols + cw - 1) / cw * rt;
     p.nw = p.mb == 1 && wgs < 512 && nb >= 32 ? 16 : 8;
@@ -497,15 +519,32 @@ LinPlan lin_plan(int kind, int rows, int cols, int K, int groups) {
     while (wgs * p.ks < 256 && p.ks < 16 && nb / (p.ks * 2) >= 2 * p.nw) p.ks *= 2;
     return p;
   }
-  p.rt = per <= 64 ? 64 : per <= 128 ? 128 : 256;
-  p.ct = p.rt == 64 ? 128 : 256;
+  const int steps = ((kind == LIN_DW ? (K + groups - 1) / groups : K) * bytes + LIN_BYTES - 1) / LIN_BYTES;
+  float best = 1e30f;
+  for (const Option& o : options) {
+    long long rt = (long long)((per + o.rt - 1) / o.rt) * groups;
+    if (kind != LIN_DW && groups > 1) rt = std::max<long long>(rt, (rows + o.rt - 1) / o.rt + groups / 2);
+    const long long tiles = rt * ((cols + o.ct - 1) / o.ct);
+    for (int ks = 1; ks <= (kind == LIN_DW ? 1 : 16) && (ks == 1 || steps / ks >= 4); ks *= 2) {
+      const long long each = (tiles * ks + kCUs - 1) / kCUs;                     // tiles of a CU
+      const float step = std::max(o.step[kind == LIN_FP8 ? exact : 2] * each, kLone);
+      float t = step * ((steps + ks - 1) / ks) + o.tile * each;
+      if (ks > 1) t += kSlabLaunch + 2.f * 4.f * ks * rows * (float)cols / kSlabRate;
+      if (t < best) {
+        best = t;
+        p.rt = o.rt;
+        p.ct = o.ct;
+        p.ks = ks;
+      }
+    }
+  }
   return p;
 }
 size_t lin_workspace(const LinPlan& p, int rows, int cols) { return p.ks > 1 ? (size_t)p.ks * rows * cols * 4 : 0; }
 
 hipError_t launch_linear(LinDesc d, float* workspace, size_t workspace_bytes, hipStream_t s) {
-  LinPlan p = lin_plan(d.kind, d.rows, d.cols, d.K, d.groups);
-  if (p.ks > 1 && (!workspace || workspace_bytes < lin_workspace(p, d.rows, d.cols))) p.ks = 1;
+  LinPlan p = lin_plan(d.kind, d.kind == LIN_FP8 && d.out_f32, d.rows, d.cols, d.K, d.groups);
+  if (p.ks > 1 && (!workspace || workspace_bytes < lin_workspace(p, d.rows, d.cols))) p.ks = 1;   // whole sums then
   d.ks = p.ks;
   d.part = workspace;
   return p.skinny ? launch_linear_skinny(d, p, s) : launch_linear_tiled(d, p, s);

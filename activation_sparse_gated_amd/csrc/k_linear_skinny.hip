@@ -194,8 +194,7 @@ static hipError_t pick_skinny(const LinDesc& d, const LinPlan& p, hipStream_t s)
     if (p.nw == 16) return go_skinny<KIND, EXACT, AROW, 1, 1, 16, AROW ? 2 : 4>(d, s);
     return go_skinny<KIND, EXACT, AROW, 1, 1, 8, 4>(d, s);
   }
-  if (p.mb == 2) return go_skinny<KIND, EXACT, AROW, 2, BIG ? 1 : 2, 8, 2>(d, s);
-  return go_skinny<KIND, EXACT, AROW, 4, BIG ? 1 : 2, 8, 2>(d, s);
+  return go_skinny<KIND, EXACT, AROW, 2, BIG ? 1 : 2, 8, 2>(d, s);
 }
 hipError_t launch_linear_skinny(const LinDesc& d, const LinPlan& p, hipStream_t s) {
   if (d.kind == LIN_FWD) return pick_skinny<LIN_FWD, false, false>(d, p, s);

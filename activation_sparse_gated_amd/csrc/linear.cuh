@@ -63,7 +63,7 @@ struct LinPlan {
   int rt, ct;                    // k_linear: rows and columns of a tile
   int ks;                        // slices of the contraction
 };
-LinPlan lin_plan(int kind, int rows, int cols, int K, int groups);
+LinPlan lin_plan(int kind, int exact, int rows, int cols, int K, int groups);
 size_t lin_workspace(const LinPlan& p, int rows, int cols);
 hipError_t launch_linear(LinDesc d, float* workspace, size_t workspace_bytes, hipStream_t s);
 hipError_t launch_linear_tiled(const LinDesc& d, const LinPlan& p, hipStream_t s);

@@ -2,6 +2,7 @@
 // checks and launches. The calls keep no state.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/ffn_linear.h"
@@ -120,7 +121,9 @@ ffn_status ffn_fp8_quantize(const void* x, int32_t dtype, int32_t groups, int32_
 }
 
 size_t ffn_fp8_linear_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t groups) {
-  return product_shape_ok(m, n, k, groups) && m > 0 ? lin_workspace(lin_plan(LIN_FP8, m, n, k, groups), m, n) : 0;
+  if (!product_shape_ok(m, n, k, groups) || m == 0) return 0;
+  return std::max(lin_workspace(lin_plan(LIN_FP8, 0, m, n, k, groups), m, n),
+                  lin_workspace(lin_plan(LIN_FP8, 1, m, n, k, groups), m, n));
 }
 
 ffn_status ffn_fp8_linear(const uint8_t* x, const float* x_scale, const uint8_t* w, const float* w_scale,
@@ -155,7 +158,7 @@ ffn_status ffn_fp8_linear(const uint8_t* x, const float* x_scale, const uint8_t*
 }
 
 size_t ffn_grouped_forward_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t groups) {
-  return product_shape_ok(m, n, k, groups) && m > 0 ? lin_workspace(lin_plan(LIN_FWD, m, n, k, groups), m, n) : 0;
+  return product_shape_ok(m, n, k, groups) && m > 0 ? lin_workspace(lin_plan(LIN_FWD, 0, m, n, k, groups), m, n) : 0;
 }
 
 ffn_status ffn_grouped_forward(const void* x, const void* w, const int32_t* offsets, int32_t groups, int32_t m, int32_t n,
@@ -179,7 +182,7 @@ ffn_status ffn_grouped_forward(const void* x, const void* w, const int32_t* offs
 }
 
 size_t ffn_grouped_backward_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t groups) {
-  return product_shape_ok(m, n, k, groups) && m > 0 ? lin_workspace(lin_plan(LIN_DX, m, k, n, groups), m, k) : 0;
+  return product_shape_ok(m, n, k, groups) && m > 0 ? lin_workspace(lin_plan(LIN_DX, 0, m, k, n, groups), m, k) : 0;
 }
 
 ffn_status ffn_grouped_backward(const void* x, const void* w, const void* dy, const int32_t* offsets, int32_t groups,

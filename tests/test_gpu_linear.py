@@ -256,7 +256,9 @@ def product_slack(x, w, out):
 
 FP8_SHAPES = [(1, 64, 128), (1, 1, 16), (1, 4096, 2048), (2, 77, 144), (5, 130, 1008), (16, 257, 512), (17, 256, 4096),
               (33, 64, 272), (64, 300, 1024), (65, 512, 640), (100, 128, 896), (128, 128, 128), (129, 129, 400),
-              (250, 520, 768), (300, 1030, 384), (513, 264, 256), (700, 260, 2064)]
+              (250, 520, 768), (300, 1030, 384), (513, 264, 256), (700, 260, 2064),
+              # the contraction in slices, with a ragged end, for every size of tile
+              (3, 40, 8208), (24, 96, 8208), (40, 130, 8208), (200, 256, 8192), (300, 100, 6160)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
@@ -283,7 +285,8 @@ def test_fp8_linear(asg, m, n, k, rows, out):
 EXPERTS = [
     ([0, 3, 3, 10], 10, 96, 256), ([0, 0, 1], 1, 64, 144), ([2, 5, 9], 12, 77, 400), ([0, 40, 41, 41, 170], 170, 264, 512),
     ([0, 16, 48, 112, 120], 120, 128, 1024), ([5, 5, 5], 9, 64, 128), ([0, 300, 301, 700], 710, 300, 384),
-    ([0, 1, 2, 3, 4, 5, 6, 7, 8], 8, 512, 2048), ([0, 129, 129, 130], 130, 520, 272)]
+    ([0, 1, 2, 3, 4, 5, 6, 7, 8], 8, 512, 2048), ([0, 129, 129, 130], 130, 520, 272), ([0, 30, 70], 80, 72, 8208),
+    ([0, 200, 200, 500], 500, 136, 6160)]
 WIDE = [sorted(int(v) for v in rng(6).integers(0, 512, 257)), 512, 48, 144]
 
 
@@ -325,6 +328,7 @@ GROUPED = [
     ([0, 3, 3, 10], 10, 96, 256), ([0, 0, 1], 1, 64, 136), ([2, 5, 9], 12, 72, 400), ([0, 40, 41, 41, 170], 170, 264, 512),
     ([0, 16, 48, 112, 120], 120, 128, 1024), ([5, 5, 5], 9, 64, 128), ([0, 300, 301, 700], 710, 304, 384), ([0, 1], 1, 8, 8),
     ([0, 1, 2, 3, 4, 5, 6, 7, 8], 8, 512, 2048), ([0, 129, 129, 130], 130, 520, 264), ([0, 260, 520], 520, 512, 512),
+    ([0, 5, 20], 24, 72, 8200), ([0, 30, 70], 80, 72, 4104), ([0, 200, 200, 500], 500, 4104, 136), ([3, 4, 400], 401, 2056, 72),
     (WIDE[0], 512, 48, 144)]
 
 
