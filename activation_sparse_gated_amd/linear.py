@@ -5,10 +5,15 @@ current stream of the tensors' device; every step runs in the HIP kernels
 behind the C ABI. Function names follow the C entry points. Tensors are
 contiguous and on one GPU; what does not fit raises ValueError before anything
 is launched. Outputs that are not passed in are allocated.
+
+Every function takes `stream`, a torch.cuda.Stream of the tensors' device: the
+call is then made as inside `with torch.cuda.stream(stream)`, its outputs and
+scratch memory allocated there. Inputs made on other streams have to be ready
+and to stay (torch.Tensor.record_stream), as for any torch operation.
 """
 from __future__ import annotations
 
-import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -70,13 +75,29 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(fn, device, stream, *args):
-    """The C call on the tensors' own device, on its current stream unless one is given."""
-    if torch.cuda.current_device() != device.index:
+def _call(fn, device, *args):
+    """The C call on the tensors' own device, on its current stream."""
+    index = device.index
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
-            return _call(fn, device, stream, *args)
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    check(fn(*args, s.cuda_stream), fn.__name__)
+            return _call(fn, device, *args)
+    # the handle of torch.cuda.current_stream(device), without the object around it (2 us a call)
+    check(fn(*args, torch._C._cuda_getCurrentRawStream(index)), fn.__name__)
+
+
+def _on_stream(fn):
+    """Adds the `stream` argument (module docstring)."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        first = args[0] if args else next(iter(kw.values()))
+        device = getattr(first.q if isinstance(first, Fp8Tensor) else first, "device", None)
+        if device != stream.device:
+            raise ValueError(f"stream: of {stream.device}, the tensors are on {device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _workspace(workspace, nbytes, device):
@@ -91,7 +112,8 @@ def _nbytes(t):
 
 
 # ---------------------------------------------------------------- RMS norm
-def rmsnorm_forward(x, w, *, residual=None, eps=1e-6, fp8=False, r=None, y=None, stream=None):
+@_on_stream
+def rmsnorm_forward(x, w, *, residual=None, eps=1e-6, fp8=False, r=None, y=None):
     """RMS norm of the rows of x + residual (ffn_rmsnorm_forward): (y, r).
 
     x [m, d] bf16 or fp32; w [d]; residual [m, d] or None. r is the sum, which
@@ -120,12 +142,13 @@ def rmsnorm_forward(x, w, *, residual=None, eps=1e-6, fp8=False, r=None, y=None,
         else:
             _check("y", y, x.dtype, x.shape, dev)
         out, q, scale = y, None, None
-    _call(_lib.load().ffn_rmsnorm_forward, dev, stream, _ptr(x), _ptr(residual), _ptr(w), _DTYPES[x.dtype], m, d,
+    _call(_lib.load().ffn_rmsnorm_forward, dev, _ptr(x), _ptr(residual), _ptr(w), _DTYPES[x.dtype], m, d,
           float(eps), _ptr(r), _ptr(out), _ptr(q), _ptr(scale))
     return y, (x if r is None else r)
 
 
-def rmsnorm_backward(r, w, dy, *, dr=None, eps=1e-6, dx=None, dw=None, accumulate=False, workspace=None, stream=None):
+@_on_stream
+def rmsnorm_backward(r, w, dy, *, dr=None, eps=1e-6, dx=None, dw=None, accumulate=False, workspace=None):
     """Gradients of the norm of the rows r (ffn_rmsnorm_backward): (dx, dw).
 
     dx [m, d] of r's type is the gradient of x and of the residual, dr (the
@@ -144,7 +167,7 @@ def rmsnorm_backward(r, w, dy, *, dr=None, eps=1e-6, dx=None, dw=None, accumulat
     dw = _accumulator("dw", dw, accumulate, (d,), dev)
     lib = _lib.load()
     workspace = _workspace(workspace, lib.ffn_rmsnorm_backward_workspace_bytes(m, d), dev)
-    _call(lib.ffn_rmsnorm_backward, dev, stream, _ptr(r), _ptr(w), _ptr(dy), _ptr(dr), _DTYPES[r.dtype], m, d,
+    _call(lib.ffn_rmsnorm_backward, dev, _ptr(r), _ptr(w), _ptr(dy), _ptr(dr), _DTYPES[r.dtype], m, d,
           float(eps), _ptr(dx), _ptr(dw), int(bool(accumulate)), _ptr(workspace), _nbytes(workspace))
     return dx, dw
 
@@ -166,7 +189,8 @@ def _check_fp8(name, t, shape, block_rows, dev):
     _check(f"{name}.scale", t.scale, torch.float32, _scale_shape(shape, block_rows), dev)
 
 
-def fp8_quantize(x, *, block_rows=1, transposed=False, out=None, out_t=None, stream=None):
+@_on_stream
+def fp8_quantize(x, *, block_rows=1, transposed=False, out=None, out_t=None):
     """x [m, k] (or [experts, m, k]), bf16 or fp32, in 8-bit blocks of block_rows
     (1 or 128) x 128 (ffn_fp8_quantize): an Fp8Tensor, or with transposed a pair
     of it and the blocks of the transposed matrices [k, m], their rows filled
@@ -175,8 +199,7 @@ def fp8_quantize(x, *, block_rows=1, transposed=False, out=None, out_t=None, str
     if block_rows not in (1, BLOCK):
         raise ValueError(f"block_rows: 1 or {BLOCK}, got {block_rows}")
     *lead, m, k = x.shape
-    mt = (m + 15) // 16 * 16
-    shape_t = (*lead, k, mt)
+    shape_t = (*lead, k, (m + 15) // 16 * 16)
     if out is None:
         out = Fp8Tensor(torch.empty(x.shape, dtype=FP8, device=dev),
                         torch.empty(_scale_shape(x.shape, block_rows), dtype=torch.float32, device=dev), block_rows)
@@ -193,14 +216,15 @@ def fp8_quantize(x, *, block_rows=1, transposed=False, out=None, out_t=None, str
         raise ValueError("out_t: given without transposed")
     groups = lead[0] if lead else 1
     if groups:
-        _call(_lib.load().ffn_fp8_quantize, dev, stream, _ptr(x), _DTYPES[x.dtype], groups, m, k, block_rows,
+        _call(_lib.load().ffn_fp8_quantize, dev, _ptr(x), _DTYPES[x.dtype], groups, m, k, block_rows,
               _ptr(out.q), _ptr(out.scale), _ptr(out_t.q if transposed else None),
               _ptr(out_t.scale if transposed else None))
     return (out, out_t) if transposed else out
 
 
+@_on_stream
 def fp8_linear(x: Fp8Tensor, w: Fp8Tensor, *, offsets=None, y=None, out_dtype=torch.bfloat16, accumulate=False,
-               workspace=None, stream=None):
+               workspace=None):
     """y = x w^T of 8-bit blocks (ffn_fp8_linear), [m, n] in out_dtype (bf16 or fp32).
 
     x: blocks of 1 x 128, [m, k]. w: [n, k], blocks of 128 x 128 or 1 x 128; with
@@ -209,21 +233,30 @@ def fp8_linear(x: Fp8Tensor, w: Fp8Tensor, *, offsets=None, y=None, out_dtype=to
     fp32 y."""
     if not isinstance(x, Fp8Tensor) or not isinstance(w, Fp8Tensor):
         raise ValueError("x, w: expected Fp8Tensors")
-    dev = _first("x.q", x.q, (FP8,), (2,))
-    m, k = x.q.shape
-    _check_fp8("x", x, (m, k), 1, dev)
-    if w.block_rows not in (1, BLOCK) or (offsets is not None and w.block_rows == 1):
-        raise ValueError(f"w: blocks of {w.block_rows} x {BLOCK} are not taken here")
-    _first("w.q", w.q, (FP8,), (2,) if offsets is None else (3,))
-    *lead, n, _ = w.q.shape
-    _check_fp8("w", w, (*lead, n, k), w.block_rows, dev)
-    groups = lead[0] if lead else 1
+    rows = w.block_rows
+    if x.block_rows != 1 or (rows != BLOCK and (rows != 1 or offsets is not None)):
+        raise ValueError(f"x, w: blocks of {x.block_rows} x {BLOCK} and {rows} x {BLOCK} are not taken here")
+    xq, wq = x.q, w.q
+    dev = _first("x.q", xq, (FP8,), (2,))
+    m, k = xq.shape
+    kb = (k + 127) // 128
+    _check("x.scale", x.scale, torch.float32, (kb, m), dev)
+    if offsets is None:
+        _first("w.q", wq, (FP8,), (2,))
+        groups, n = 1, wq.shape[0]
+        _check("w.q", wq, FP8, (n, k), dev)
+        _check("w.scale", w.scale, torch.float32, (kb, n) if rows == 1 else ((n + 127) // 128, kb), dev)
+    else:
+        _first("w.q", wq, (FP8,), (3,))
+        groups, n, _ = wq.shape
+        _check("w.q", wq, FP8, (groups, n, k), dev)
+        _check("w.scale", w.scale, torch.float32, (groups, (n + 127) // 128, kb), dev)
+        _check("offsets", offsets, torch.int32, (groups + 1,), dev)
     y = _product_out(y, (m, n), out_dtype, dev, accumulate)
-    _check_offsets(offsets, groups, dev)
     lib = _lib.load()
     workspace = _workspace(workspace, lib.ffn_fp8_linear_workspace_bytes(m, n, k, groups), dev)
-    _call(lib.ffn_fp8_linear, dev, stream, _ptr(x.q), _ptr(x.scale), _ptr(w.q), _ptr(w.scale), w.block_rows, m, n, k,
-          _ptr(offsets), groups, _ptr(y), _DTYPES[y.dtype], int(bool(accumulate)), _ptr(workspace), _nbytes(workspace))
+    _call(lib.ffn_fp8_linear, dev, xq.data_ptr(), x.scale.data_ptr(), wq.data_ptr(), w.scale.data_ptr(), rows, m, n,
+          k, _ptr(offsets), groups, _ptr(y), _DTYPES[y.dtype], int(bool(accumulate)), _ptr(workspace), _nbytes(workspace))
     return y
 
 
@@ -240,13 +273,9 @@ def _product_out(y, shape, out_dtype, dev, accumulate=False):
     return y
 
 
-def _check_offsets(offsets, groups, dev):
-    if offsets is not None:
-        _check("offsets", offsets, torch.int32, (groups + 1,), dev)
-
-
 # ---------------------------------------------------------------- products by expert
-def grouped_forward(x, w, offsets, *, y=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+@_on_stream
+def grouped_forward(x, w, offsets, *, y=None, out_dtype=torch.bfloat16, workspace=None):
     """y[t] = W_e x[t] for the rows t of each expert e (ffn_grouped_forward).
 
     x [m, k] bf16, sorted by expert; w [experts, n, k] bf16; offsets int32
@@ -262,12 +291,13 @@ def grouped_forward(x, w, offsets, *, y=None, out_dtype=torch.bfloat16, workspac
     y = _product_out(y, (m, n), out_dtype, dev)
     lib = _lib.load()
     workspace = _workspace(workspace, lib.ffn_grouped_forward_workspace_bytes(m, n, k, groups), dev)
-    _call(lib.ffn_grouped_forward, dev, stream, _ptr(x), _ptr(w), _ptr(offsets), groups, m, n, k, _ptr(y),
+    _call(lib.ffn_grouped_forward, dev, _ptr(x), _ptr(w), _ptr(offsets), groups, m, n, k, _ptr(y),
           _DTYPES[y.dtype], _ptr(workspace), _nbytes(workspace))
     return y
 
 
-def grouped_backward(x, w, dy, offsets, *, dx=None, dw=None, accumulate=False, workspace=None, stream=None):
+@_on_stream
+def grouped_backward(x, w, dy, offsets, *, dx=None, dw=None, accumulate=False, workspace=None):
     """Gradients of grouped_forward (ffn_grouped_backward): (dx, dw).
 
     dy [m, n] bf16; dx [m, k] bf16, rows of no expert left as they were; dw
@@ -287,6 +317,6 @@ def grouped_backward(x, w, dy, offsets, *, dx=None, dw=None, accumulate=False, w
     dw = _accumulator("dw", dw, accumulate, (groups, n, k), dev)
     lib = _lib.load()
     workspace = _workspace(workspace, lib.ffn_grouped_backward_workspace_bytes(m, n, k, groups), dev)
-    _call(lib.ffn_grouped_backward, dev, stream, _ptr(x), _ptr(w), _ptr(dy), _ptr(offsets), groups, m, n, k, _ptr(dx),
+    _call(lib.ffn_grouped_backward, dev, _ptr(x), _ptr(w), _ptr(dy), _ptr(offsets), groups, m, n, k, _ptr(dx),
           _ptr(dw), int(bool(accumulate)), _ptr(workspace), _nbytes(workspace))
     return dx, dw
