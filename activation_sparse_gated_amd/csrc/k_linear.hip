@@ -256,9 +256,9 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
   constexpr int KK = FP8 ? 1 : 2, TURNS = KK * BT, AHEAD = FP8 ? 1 : 3, RING = AHEAD + 1;
   static_assert(TURNS % RING == 0 && TURNS > AHEAD && TURNS % 4 == 0, "turns of a step");
   constexpr int LOADS = TA::LOADS + TB::LOADS, PER = (LOADS + TURNS / 2 - 1) / (TURNS / 2), LTURNS = (LOADS + PER - 1) / PER;
-  auto load = [&](char* st, int turn) {          // turn: turns since the meeting
+  auto load = [&](char* st, int turn, bool known) {   // turn: turns since the meeting; known: a whole step
     const uint32_t at = lds_address(st) + wave * 1024;
-    const bool whole = cstep < cfull;
+    const bool whole = known || cstep < cfull;
 #pragma unroll
     for (int i = turn * PER; i < (turn + 1) * PER && i < LOADS; ++i) {
       if (i < TA::LOADS) {
@@ -351,12 +351,12 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
   advance();
   if (more) {
 #pragma unroll
-    for (int t = 0; t < LTURNS; ++t) load(smem[0], t);
+    for (int t = 0; t < LTURNS; ++t) load(smem[0], t, false);
     lin_sync();
     advance();
     if (more) {
 #pragma unroll
-      for (int t = 0; t < AHEAD && t < LTURNS; ++t) load(smem[1], t);
+      for (int t = 0; t < AHEAD && t < LTURNS; ++t) load(smem[1], t, false);
     }
 #pragma unroll
     for (int i = 0; i < AT; ++i) af[i] = read_a(smem[0], i, 0);
@@ -365,66 +365,86 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
     fetch_scales(smem[0]);
   }
   int par = 0;
+  // One step. INSIDE: the cursor's step is not the tile's last and the next is whole, so that nothing is to be decided;
+  // a branch in every turn costs a sixth of the time.
+  auto step = [&](auto inside) {
+    constexpr bool INSIDE = decltype(inside)::value;
+    char* st = smem[par];
+    char* nx = smem[par ^ 1];
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ax[i][e] = fp8_to_bf16(af[i][2 * e], af[i][2 * e + 1]);
+    }
+#pragma unroll
+    for (int t = 0; t < TURNS; ++t) {
+      const int j = t % BT;
+      if (t < TURNS - AHEAD) {
+        if (t + AHEAD < LTURNS && (INSIDE || more)) load(nx, t + AHEAD, INSIDE);
+      } else {
+        if (t == TURNS - AHEAD && (INSIDE || more)) {
+          lin_sync();
+          if constexpr (INSIDE) {
+            sa.base += sa.step;
+            sb.base += sb.step;
+            ++cstep;
+          } else {
+            advance();
+          }
+        }
+        if (t - (TURNS - AHEAD) < LTURNS && (INSIDE || more)) load(st, t - (TURNS - AHEAD), INSIDE);
+      }
+      // past the last step of all this reads a stage that nobody writes, for nothing
+      if (t + AHEAD < TURNS) fetch_b(st, t + AHEAD);
+      else fetch_b(nx, t + AHEAD - TURNS);
+      bf16x8_t bx[4];
+      if constexpr (EXACT) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bx[e] = fp8_to_bf16(bf[t % RING][2 * e], bf[t % RING][2 * e + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        if constexpr (FP8) {
+          const int n = t * AT + i;
+          f32x4_t p{0.f, 0.f, 0.f, 0.f};
+          if constexpr (EXACT) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[i][e], bx[e], p, 0, 0, 0);
+          } else {
+            p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[t % RING], p, 0, 0, 0, 0, 0, 0);
+          }
+          z[n % (LATER + 1)] = p;
+          if (n >= LATER) join(n - LATER);
+        } else {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], bf[t % RING], acc[i][j], 0, 0, 0);
+        }
+        if (FP8 || j == BT - 1) __builtin_amdgcn_sched_barrier(0);
+        if (j == BT - 1) af[i] = t + 1 < TURNS ? read_a(st, i, t / BT + 1) : read_a(nx, i, 0);
+      }
+      if (FP8 && t == TURNS - 1) {
+#pragma unroll
+        for (int n = TURNS * AT - LATER; n < TURNS * AT; ++n) join(n);
+        fetch_scales(nx);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    par ^= 1;
+  };
   for (int at = begin; at < end; at += stride) {
     const Tile x = tile_at(at);
 #pragma unroll
     for (int i = 0; i < AT; ++i)
 #pragma unroll
       for (int j = 0; j < BT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < x.steps; ++s, par ^= 1) {
-      char* st = smem[par];
-      char* nx = smem[par ^ 1];
-      if constexpr (EXACT) {
-#pragma unroll
-        for (int i = 0; i < AT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ax[i][e] = fp8_to_bf16(af[i][2 * e], af[i][2 * e + 1]);
-      }
-#pragma unroll
-      for (int t = 0; t < TURNS; ++t) {
-        const int j = t % BT;
-        if (t < TURNS - AHEAD) {
-          if (t + AHEAD < LTURNS && more) load(nx, t + AHEAD);
-        } else {
-          if (t == TURNS - AHEAD && more) {
-            lin_sync();
-            advance();
-          }
-          if (t - (TURNS - AHEAD) < LTURNS && more) load(st, t - (TURNS - AHEAD));
-        }
-        // past the last step of all this reads a stage that nobody writes, for nothing
-        if (t + AHEAD < TURNS) fetch_b(st, t + AHEAD);
-        else fetch_b(nx, t + AHEAD - TURNS);
-        bf16x8_t bx[4];
-        if constexpr (EXACT) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) bx[e] = fp8_to_bf16(bf[t % RING][2 * e], bf[t % RING][2 * e + 1]);
-        }
-#pragma unroll
-        for (int i = 0; i < AT; ++i) {
-          if constexpr (FP8) {
-            const int n = t * AT + i;
-            f32x4_t p{0.f, 0.f, 0.f, 0.f};
-            if constexpr (EXACT) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ax[i][e], bx[e], p, 0, 0, 0);
-            } else {
-              p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i], bf[t % RING], p, 0, 0, 0, 0, 0, 0);
-            }
-            z[n % (LATER + 1)] = p;
-            if (n >= LATER) join(n - LATER);
-          } else {
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], bf[t % RING], acc[i][j], 0, 0, 0);
-          }
-          if (FP8 || j == BT - 1) __builtin_amdgcn_sched_barrier(0);
-          if (j == BT - 1) af[i] = t + 1 < TURNS ? read_a(st, i, t / BT + 1) : read_a(nx, i, 0);
-        }
-        if (FP8 && t == TURNS - 1) {
-#pragma unroll
-          for (int n = TURNS * AT - LATER; n < TURNS * AT; ++n) join(n);
-          fetch_scales(nx);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+    for (int s = 0; s < x.steps;) {
+      // steps until the cursor's tile has one whole step left beyond the one under way
+      const int fast = more ? min(cfull - 1 - cstep, x.steps - s) : 0;
+      for (int i = 0; i < fast; ++i) step(std::true_type{});
+      s += max(fast, 0);
+      if (s < x.steps) {
+        step(std::false_type{});
+        ++s;
       }
     }
     if (KIND == LIN_DW && x.steps == 0 && d.accumulate) continue;
