@@ -140,7 +140,7 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
   constexpr int SCALES = FP8 ? (RT + CT) * 4 : 0;
   constexpr int STAGE = TA::BYTES + TB::BYTES + SCALES;
   __shared__ __attribute__((aligned(16))) char smem[2][STAGE];
-  __shared__ int s_lo[kLinMaxGroups], s_hi[kLinMaxGroups], s_first[kLinMaxGroups];   // rows and first row tile of an expert
+  __shared__ int s_start[kLinMaxGroups + 1], s_first[kLinMaxGroups];   // first row (or end) and first row tile of an expert
   __shared__ int s_scan[LIN_THREADS / 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -149,16 +149,23 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
   // ---------------------------------------------------------------- the tiles of this workgroup
   int rtiles;
   {
-    int lo = 0, hi = 0;
-    if (tid < d.groups) expert_rows(d.offsets, tid, KIND == LIN_DW ? d.K : d.rows, lo, hi);
-    const int mine = tid >= d.groups ? 0 : ((KIND == LIN_DW ? d.rows : hi - lo) + RT - 1) / RT;
+    // starts: never before an earlier one, by a running maximum over the waves' lanes and then the waves
+    int v = tid <= d.groups ? expert_start(d.offsets, tid, KIND == LIN_DW ? d.K : d.rows) : 0;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+      const int w = __shfl_up(v, o, 64);
+      if (lane >= o) v = max(v, w);
+    }
+    if (lane == 63) s_scan[wave] = v;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) v = max(v, s_scan[w]);
+    if (tid <= kLinMaxGroups) s_start[tid] = v;
+    __syncthreads();
+    const int rows = tid < d.groups ? s_start[tid + 1] - s_start[tid] : 0;
+    const int mine = tid >= d.groups ? 0 : ((KIND == LIN_DW ? d.rows : rows) + RT - 1) / RT;
     const int first = block_excl_scan<LIN_THREADS>(mine, s_scan, &rtiles);
     rtiles = __builtin_amdgcn_readfirstlane(rtiles);
-    if (tid < kLinMaxGroups) {
-      s_lo[tid] = lo;
-      s_hi[tid] = hi;
-      s_first[tid] = tid < d.groups ? first : 0x7FFFFFFF;
-    }
+    if (tid < kLinMaxGroups) s_first[tid] = tid < d.groups ? first : 0x7FFFFFFF;
     __syncthreads();
   }
   const int ctiles = (d.cols + CT - 1) / CT, tiles = ctiles * rtiles;
@@ -186,7 +193,7 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
 #pragma unroll
     for (int i = 0; i < kLinMaxGroups / 64; ++i) n += __popcll(ballot64(s_first[i * 64 + lane] <= rt));
     x.g = n - 1;
-    const int lo = __builtin_amdgcn_readfirstlane(s_lo[x.g]), hi = __builtin_amdgcn_readfirstlane(s_hi[x.g]);
+    const int lo = __builtin_amdgcn_readfirstlane(s_start[x.g]), hi = __builtin_amdgcn_readfirstlane(s_start[x.g + 1]);
     const int in = rt - __builtin_amdgcn_readfirstlane(s_first[x.g]);
     x.r0 = (KIND == LIN_DW ? 0 : lo) + in * RT;
     x.rend = KIND == LIN_DW ? d.rows : hi;
@@ -511,16 +518,16 @@ hipError_t launch_linear_tiled(const LinDesc& d, const LinPlan& p, hipStream_t s
 // their kernel. How the rows are spread over the experts only the device
 // knows: half a tile of each expert is taken to be empty, at least. A product too small for the chip ends up in small tiles and
 // slices (200 x 4096 x 14336: 256-row tiles 155 us, 128 x 128 in 4 slices 30),
-// a large one in large tiles (4096 x 4096 x 8192: 124 us, 128 x 128 168).
+// a large one in large tiles (4096 x 4096 x 8192: 120 us, 128 x 128 160).
 LinPlan lin_plan(int kind, int exact, int rows, int cols, int K, int groups) {
   struct Option {
     int rt, ct, occ;
     float step[3], tile;
   };
-  static const Option options[] = {{256, 256, 1, {1.70f, 1e9f, 1.61f}, 7.f},
-                                   {128, 256, 1, {1.07f, 1.98f, 0.98f}, 5.f},
-                                   {128, 128, 2, {0.60f, 1.09f, 0.52f}, 2.5f},
-                                   {64, 128, 3, {0.46f, 0.69f, 0.33f}, 1.7f}};
+  static const Option options[] = {{256, 256, 1, {1.66f, 1e9f, 1.50f}, 7.f},
+                                   {128, 256, 1, {1.01f, 1.92f, 0.94f}, 5.f},
+                                   {128, 128, 2, {0.57f, 1.06f, 0.47f}, 2.5f},
+                                   {64, 128, 3, {0.42f, 0.69f, 0.32f}, 1.7f}};
   constexpr float kLone = 0.6f, kSlabRate = 4e6f, kSlabLaunch = 5.f;   // us, bytes per us, us
   LinPlan p{};
   p.ks = 1;

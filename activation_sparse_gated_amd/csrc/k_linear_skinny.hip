@@ -146,15 +146,11 @@ __global__ __launch_bounds__(256) void k_linear_sum(const LinDesc d) {
   const long long at = (long long)blockIdx.x * 256 + threadIdx.x;
   const int row = (int)(at / groups4), col = (int)(at - (long long)row * groups4) * 4;
   if (row >= d.rows) return;
-  if (d.offsets) {
-    int lo, hi;
-    bool mine = false;
-    for (int g = 0; g < d.groups; ++g) {
-      expert_rows(d.offsets, g, d.rows, lo, hi);
-      mine |= row >= lo && row < hi;
-    }
-    if (!mine) return;
-  }
+  // the experts' rows follow each other: all between the first start and the last end
+  int end = expert_start(d.offsets, 0, d.rows);
+  if (row < end) return;
+  for (int g = 1; g <= d.groups; ++g) end = max(end, expert_start(d.offsets, g, d.rows));
+  if (row >= end) return;
   const bool vec = (d.cols & 3) == 0;
   f32x4_t a{0.f, 0.f, 0.f, 0.f};
   for (int z = 0; z < d.ks; ++z) {

@@ -85,30 +85,26 @@ __device__ __forceinline__ uint2 fp8_pack8(const float (&f)[8], float inv) {
   return uint2{(uint32_t)lo, (uint32_t)hi};
 }
 
-// Rows [lo, hi) of expert g, kept inside 0..m whatever the offsets hold.
-__device__ __forceinline__ void expert_rows(const int32_t* offsets, int g, int m, int& lo, int& hi) {
-  if (!offsets) {
-    lo = 0;
-    hi = m;
-    return;
-  }
-  lo = min(max(offsets[g], 0), m);
-  hi = max(min(max(offsets[g + 1], 0), m), lo);
+// Where the rows of expert g start (g = groups: where the last one's end),
+// whatever the offsets hold: inside 0..m here, and by the callers never before
+// an earlier one, so that every row belongs to one expert at most.
+__device__ __forceinline__ int expert_start(const int32_t* offsets, int g, int m) {
+  return offsets ? min(max(offsets[g], 0), m) : g ? m : 0;
 }
-
 // Tile `tile` of RT rows: expert g, first output row r0, end of its rows.
 // Tiles count expert by expert; false past the last one.
 template <int RT>
 __device__ __forceinline__ bool lin_tile(const LinDesc& d, int tile, int& g, int& r0, int& rend) {
+  int lo = expert_start(d.offsets, 0, d.rows);
   for (g = 0; g < d.groups; ++g) {
-    int lo;
-    expert_rows(d.offsets, g, d.rows, lo, rend);
+    rend = max(lo, expert_start(d.offsets, g + 1, d.rows));
     const int t = (rend - lo + RT - 1) / RT;
     if (tile < t) {
       r0 = lo + tile * RT;
       return true;
     }
     tile -= t;
+    lo = rend;
   }
   return false;
 }

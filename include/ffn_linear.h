@@ -31,8 +31,8 @@
  * to expert g, which may have none. It is read on the device, so routing needs
  * no host copy. Rows before offsets[0] and from offsets[groups] on belong to
  * no expert: they are not read, and those of the output are left as they were.
- * Offsets outside 0..m are taken as the nearest of the two, and an expert
- * whose end lies before its start has no rows.
+ * Offsets outside 0..m are taken as the nearest of the two, one below an
+ * earlier one as that one, so whatever they hold no row has two experts.
  */
 #ifndef FFN_LINEAR_H
 #define FFN_LINEAR_H
@@ -103,8 +103,9 @@ size_t ffn_fp8_linear_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t g
  *               w_block_rows 128
  *   offsets     NULL (one product, groups = 1), or the rows of each expert
  *   y           [m x n] of y_dtype; accumulate = 1 adds to it (FFN_F32 only)
- *   workspace   NULL, or ffn_fp8_linear_workspace_bytes of scratch
- * k: multiple of 16. Also the backward pass: dx = dy w is the product of dy's
+ *   workspace   NULL, or ffn_fp8_linear_workspace_bytes of scratch (a smaller
+ *               one is not used): with it, small products are cut along k
+ * k: multiple of 16; n, k <= 2^22. Also the backward pass: dx = dy w is the product of dy's
  * blocks with the transposed w, dw = dy^T x the product of dy's and x's
  * transposed blocks (w_block_rows = 1), all from ffn_fp8_quantize. */
 ffn_status ffn_fp8_linear(const uint8_t *x, const float *x_scale, const uint8_t *w, const float *w_scale,
@@ -118,8 +119,8 @@ size_t ffn_grouped_forward_workspace_bytes(int32_t m, int32_t n, int32_t k, int3
 /* y[t] = W_g x[t] for the rows t of each expert g, bf16.
  *   x [m x k] bf16; w [groups x n x k] bf16; offsets as above (required)
  *   y [m x n] of y_dtype
- *   workspace   NULL, or ffn_grouped_forward_workspace_bytes of scratch
- * n, k: multiples of 8. 1 <= groups <= FFN_LINEAR_MAX_GROUPS. */
+ *   workspace   as for ffn_fp8_linear
+ * n, k: multiples of 8, up to 2^22 as in ffn_fp8_linear. 1 <= groups <= FFN_LINEAR_MAX_GROUPS. */
 ffn_status ffn_grouped_forward(const void *x, const void *w, const int32_t *offsets, int32_t groups, int32_t m,
                                int32_t n, int32_t k, void *y, int32_t y_dtype, void *workspace,
                                size_t workspace_bytes, void *stream);
@@ -133,6 +134,7 @@ size_t ffn_grouped_backward_workspace_bytes(int32_t m, int32_t n, int32_t k, int
  *   dw NULL or [groups x n x k] fp32: dW_g = sum over the rows t of g of
  *      dy[t] x[t]^T, written (zeros for an expert without rows) or, with
  *      accumulate = 1, added to
+ *   workspace as for ffn_fp8_linear
  * One of dx and dw at least; x may be NULL without dw, w without dx. With m = 0,
  * dw is cleared unless it accumulates. Sums run in a fixed order. */
 ffn_status ffn_grouped_backward(const void *x, const void *w, const void *dy, const int32_t *offsets,

@@ -381,13 +381,32 @@ def test_offsets_out_of_range_stay_inside(asg):
     g = rng(11)
     x, w = dev(g.normal(0, 1, (20, 128))), dev(g.normal(0, 1, (3, 64, 128)))
     y0, dy = dev(g.normal(0, 1, (20, 64))), dev(g.normal(0, 1, (20, 64)))
-    for wild, same in (([-5, 7, 7, 99], [0, 7, 7, 20]), ([4, 2, 9, 9], [2, 2, 9, 9]), ([30, 40, 50, 60], [20] * 4),
+    for wild, same in (([-5, 7, 7, 99], [0, 7, 7, 20]), ([4, 2, 9, 9], [4, 4, 9, 9]), ([0, 12, 5, 20], [0, 12, 12, 20]), ([30, 40, 50, 60], [20] * 4),
                        ([-2 ** 31, 3, 2 ** 31 - 1, -1], [0, 3, 20, 20])):
         a, b = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in (wild, same))
         assert np.array_equal(bits(asg.grouped_forward(x, w, a, y=y0.clone())), bits(asg.grouped_forward(x, w, b, y=y0.clone())))
         p = asg.grouped_backward(x, w, dy, a, dx=x.clone())
         q = asg.grouped_backward(x, w, dy, b, dx=x.clone())
         assert np.array_equal(bits(p[0]), bits(q[0])) and np.array_equal(bits(p[1]), bits(q[1]))
+
+
+def test_wild_offsets_of_many_experts(asg):
+    say("wild offsets, many experts")
+    torch = torch_()
+    g = rng(15)
+    for m in (200, 3000):
+        x, w = dev(g.normal(0, 1, (m, 64))), dev(g.normal(0, 1, (256, 16, 64)))
+        wild = g.integers(-50, m + 400, 257)
+        wild[::2], wild[100] = 0, 2 ** 31 - 1
+        same = np.maximum.accumulate(np.clip(wild, 0, m))
+        y0, dy = dev(g.normal(0, 1, (m, 16))), dev(g.normal(0, 1, (m, 16)))
+        a, b = (torch.from_numpy(v.astype(np.int32)).cuda() for v in (wild, same))
+        assert np.array_equal(bits(asg.grouped_forward(x, w, a, y=y0.clone())), bits(asg.grouped_forward(x, w, b, y=y0.clone())))
+        p, q = (asg.grouped_backward(x, w, dy, o, dx=x.clone()) for o in (a, b))
+        assert np.array_equal(bits(p[0]), bits(q[0])) and np.array_equal(bits(p[1]), bits(q[1]))
+        want = L.grouped(f64(x), f64(w), same, f64(y0))
+        got = f64(asg.grouped_forward(x, w, b, y=y0.clone()))
+        near(got, want, 2 * U * 74 * 64 * 16 + B * np.abs(want) * (1 + 1e-4), "y")
 
 
 def test_bad_numbers_stay_in_their_rows(asg):
@@ -615,3 +634,67 @@ def test_outputs_stay_in_their_buffers(asg):
     torch.cuda.synchronize()
     for t in bufs:
         assert bool((t[:256] == 0xA5).all()) and bool((t[-256:] == 0xA5).all())
+
+
+# ---------------------------------------------------------------- past 2^31 elements
+def test_norm_and_blocks_past_32_bits(asg):
+    say("large norm")
+    torch = torch_()
+    m, d = 135_000, 16384                                # 2.2e9 elements
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(m, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    w = torch.empty(d, dtype=torch.bfloat16, device="cuda").normal_(1, 0.2, generator=gen)
+    rows = [0, 1, 131_072, m - 2, m - 1]
+    y, r = asg.rmsnorm_forward(x, w, residual=x)
+    q, _ = asg.rmsnorm_forward(x, w, residual=x, fp8=True)
+    want = L.rmsnorm(f64(r[rows]), f64(w), EPS)
+    near(f64(y[rows]), want, np.abs(want) * (B + 140 * U), "y")
+    part = asg.Fp8Tensor(q.q[rows].contiguous(), q.scale[:, rows].contiguous(), 1)
+    check_blocks_near(part, want, np.abs(want) * 140 * U, 1)
+    del y, r, q
+    dx, dw = asg.rmsnorm_backward(x, w, x, dr=x)
+    wdx, _ = L.rmsnorm_backward(f64(x[rows]), f64(w), f64(x[rows]), f64(x[rows]), EPS)
+    near(f64(dx[rows]), wdx, 400 * U * 3 * (1 + np.abs(f64(x[rows])) * 4) + B * np.abs(wdx), "dx")
+    del dx
+    a, b = asg.fp8_quantize(x, transposed=True)
+    codes, scales = L.blocks(x[rows].float().cpu().numpy(), 1)
+    same_codes(a.q[rows].contiguous(), codes)
+    assert np.array_equal(a.scale[:, rows].cpu().numpy().T, scales)
+    cols = [0, 8191, d - 1]
+    tail = m // 128 * 128                                # the last, partial block of the transposed rows
+    codes, scales = L.blocks(x[tail:][:, cols].float().cpu().numpy().T.copy(), 1)
+    same_codes(b.q[cols][:, tail:m].contiguous(), codes)
+    assert np.array_equal(b.scale[-1, cols].cpu().numpy(), scales[:, 0])
+
+
+def test_products_past_32_bits(asg):
+    say("large products")
+    torch = torch_()
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    normal = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)  # noqa: E731
+    m, k, n = 532_000, 4096, 64                          # x: 2.2e9 elements
+    x, w = normal(m, k), normal(2, n, k)
+    off = torch.tensor([0, 7, m], dtype=torch.int32, device="cuda")
+    y = asg.grouped_forward(x, w, off)
+    rows = [0, 7, 524_287, 524_288, m - 1]
+    X, W = f64(x[rows]), f64(w)
+    for i, t in enumerate(rows):
+        e = int(t >= 7)
+        near(f64(y[t]), X[i] @ W[e].T, product_slack(X[i:i + 1], W[e], "bf16")[0], t)
+    q, wq = asg.fp8_quantize(x), asg.fp8_quantize(w[0].contiguous(), block_rows=128)
+    v = asg.Fp8Tensor(q.q[rows].contiguous(), q.scale[:, rows].contiguous(), 1).dequantize().double().cpu().numpy()
+    wv = wq.dequantize().double().cpu().numpy()
+    y = asg.fp8_linear(q, wq)
+    near(f64(y[rows]), v @ wv.T, product_slack(v, wv, "bf16") + 7 * 2.0 ** -13 * eights(v, wv), "8-bit")
+    del x, y, q
+    # 9 x 16384 x 16384 gradients: 2.4e9 elements, and as many weights
+    g, n, k, m = 9, 16384, 16384, 40
+    w, x, dy = normal(g, n, k), normal(m, k), normal(m, n)
+    off = torch.tensor([0, 1, 2, 3, 4, 5, 6, 7, 8, m], dtype=torch.int32, device="cuda")
+    dx, dw = asg.grouped_backward(x, w, dy, off)
+    X, D = f64(x), f64(dy)
+    near(f64(dw[8, -3:]), D[8:, -3:].T @ X[8:], product_slack(D[8:, -3:].T, X[8:].T, "f32"), "dw")
+    near(f64(dw[7, :2]), np.outer(D[7, :2], X[7]), 4 * U * np.abs(np.outer(D[7, :2], X[7])), "dw of one row")
+    near(f64(dx[8:, -5:]), D[8:] @ f64(w[8, :, -5:]), product_slack(D[8:], f64(w[8, :, -5:]).T, "bf16"), "dx")
+    y = asg.grouped_forward(x, w, off)
+    near(f64(y[8:, -5:]), X[8:] @ f64(w[8, -5:]).T, product_slack(X[8:], f64(w[8, -5:]), "bf16"), "y")
