@@ -181,14 +181,14 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
   auto tile_at = [&](int at) {
     constexpr int PR = 8, PC = 4;
     Tile x;
-    x.z = at / tiles;
+    x.z = d.ks == 1 ? 0 : at / tiles;
     const int lin = at - x.z * tiles;
     const int strip = lin / (PC * rtiles), ins = lin - strip * PC * rtiles;
     const int sw = min(PC, ctiles - strip * PC);
-    const int patch = ins / (PR * sw), inp = ins - patch * PR * sw;
-    const int ph = min(PR, rtiles - patch * PR);
-    const int rt = patch * PR + inp % ph;
-    x.c0 = (strip * PC + inp / ph) * CT;
+    const int patch = sw == PC ? ins / (PR * PC) : ins / (PR * sw), inp = ins - patch * PR * sw;
+    const int ph = min(PR, rtiles - patch * PR), down = ph == PR ? inp / PR : inp / ph;
+    const int rt = patch * PR + inp - down * ph;
+    x.c0 = (strip * PC + down) * CT;
     int n = 0;                                   // the last expert that starts at or before row tile rt
 #pragma unroll
     for (int i = 0; i < kLinMaxGroups / 64; ++i) n += __popcll(ballot64(s_first[i * 64 + lane] <= rt));
@@ -214,6 +214,7 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
   LinSrc<CT, AALONG, ESZ> sa;
   LinSrc<RT, BALONG, ESZ> sb;
   int cat = begin - stride, cstep = 0, cfull = 0, cleft = 0, ckb = 0;
+  Tile ctile;                                    // the cursor's tile
   bool more = true;
   // 8-bit blocks: the step's scales travel with it, one float a row of B (threads 0 .. RT - 1) and a column of the
   // tile (the next CT threads; with blocks of 128 rows of A, columns of a block all get its scale)
@@ -233,6 +234,7 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
       if (!more) return;
       x = tile_at(cat);
     } while (x.steps == 0);
+    ctile = x;
     cstep = 0;
     cfull = x.full;
     cleft = x.left;
@@ -439,7 +441,7 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
     par ^= 1;
   };
   for (int at = begin; at < end; at += stride) {
-    const Tile x = tile_at(at);
+    const Tile x = cat == at ? ctile : tile_at(at);
 #pragma unroll
     for (int i = 0; i < AT; ++i)
 #pragma unroll
@@ -511,14 +513,18 @@ hipError_t launch_linear_tiled(const LinDesc& d, const LinPlan& p, hipStream_t s
 }
 
 // Which kernel, tile and slices, by the time that each would take, in
-// microseconds: what a CU spends on a step of a tile (measured over whole
-// rounds of large products, 8-bit / exact 8-bit / bf16), what a workgroup that
-// has its CU for itself needs for one at least (latency), what a tile costs
-// besides, and the slabs of a sliced product, written and read at 4 TB/s, with
-// their kernel. How the rows are spread over the experts only the device
-// knows: half a tile of each expert is taken to be empty, at least. A product too small for the chip ends up in small tiles and
-// slices (200 x 4096 x 14336: 256-row tiles 155 us, 128 x 128 in 4 slices 30),
-// a large one in large tiles (4096 x 4096 x 8192: 120 us, 128 x 128 160).
+// microseconds, round by round of the tiles that run at once. A step of a
+// round takes what the CU's tiles need for it (measured over whole rounds of
+// large products: 8-bit / exact 8-bit / bf16), or its latency where a CU has
+// one small tile, or, with more weights than the memory-side cache keeps, what
+// HBM takes to bring the round's; to that come what a tile costs besides and
+// the slabs of a sliced product, written and read, with their kernel. How the
+// rows are spread over the experts only the device knows: half a tile of each
+// is taken to be empty, at least. Small products end up in small tiles and
+// slices (200 x 4096 x 14336 8-bit: 256-row tiles 155 us, 128 x 128 in 4 slices
+// 31), weight streams in small tiles (500 rows over 5 experts of 14336 x 4096:
+// 256 x 256 224 us, 64 x 128 166), large ones in large tiles (4096 x 4096 x
+// 8192: 256 x 256 120 us, 128 x 128 160).
 LinPlan lin_plan(int kind, int exact, int rows, int cols, int K, int groups) {
   struct Option {
     int rt, ct, occ;
@@ -528,7 +534,8 @@ LinPlan lin_plan(int kind, int exact, int rows, int cols, int K, int groups) {
                                    {128, 256, 1, {1.01f, 1.92f, 0.94f}, 5.f},
                                    {128, 128, 2, {0.57f, 1.06f, 0.47f}, 2.5f},
                                    {64, 128, 3, {0.42f, 0.69f, 0.32f}, 1.7f}};
-  constexpr float kLone = 0.6f, kSlabRate = 4e6f, kSlabLaunch = 5.f;   // us, bytes per us, us
+  constexpr float kHbm = 4.5e6f, kSlabRate = 4e6f, kSlabLaunch = 5.f;   // bytes per us, us
+  constexpr double kCached = 128e6;
   LinPlan p{};
   p.ks = 1;
   const int per = kind == LIN_DW ? rows : (rows + groups - 1) / groups, bytes = kind == LIN_FP8 ? 1 : 2;
@@ -552,10 +559,14 @@ LinPlan lin_plan(int kind, int exact, int rows, int cols, int K, int groups) {
     long long rt = (long long)((per + o.rt - 1) / o.rt) * groups;
     if (kind != LIN_DW && groups > 1) rt = std::max<long long>(rt, (rows + o.rt - 1) / o.rt + groups / 2);
     const long long tiles = rt * ((cols + o.ct - 1) / o.ct);
-    for (int ks = 1; ks <= (kind == LIN_DW ? 1 : 16) && (ks == 1 || steps / ks >= 4); ks *= 2) {
-      const long long each = (tiles * ks + kCUs - 1) / kCUs;                     // tiles of a CU
-      const float step = std::max(o.step[kind == LIN_FP8 ? exact : 2] * each, kLone);
-      float t = step * ((steps + ks - 1) / ks) + o.tile * each;
+    for (const int ks : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (ks > 1 && (kind == LIN_DW || steps / ks < 4)) break;
+      const long long n = tiles * ks, slots = (long long)kCUs * o.occ, rounds = (n + slots - 1) / slots;
+      const long long at_once = std::min(n, slots), each = rounds > 1 ? o.occ : (n + kCUs - 1) / kCUs;   // of a CU
+      const bool cold = kind != LIN_DW && weights > kCached;
+      float step = std::max(o.step[kind == LIN_FP8 ? exact : 2] * each, cold ? 0.95f : 0.6f);
+      if (cold) step = std::max(step, (float)(weights / ((double)tiles * steps)) * at_once / kHbm);
+      float t = rounds * (step * ((steps + ks - 1) / ks) + o.tile * each);
       if (ks > 1) t += kSlabLaunch + 2.f * 4.f * ks * rows * (float)cols / kSlabRate;
       if (t < best) {
         best = t;
