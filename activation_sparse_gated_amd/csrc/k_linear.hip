@@ -288,16 +288,17 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
 
   // ---------------------------------------------------------------- operands and sums
   const int l16 = lane & 15, q4 = lane >> 4;
-  // operand reads of a 16-row tile. Along the contraction: bf16 chunk 4 kk + q4, or the 8-bit chunks 2 q4 and 2 q4 + 1,
-  // whose places differ in the lowest bit; the tile's rows are l16 modulo 16, so the places are those of row l16.
-  const int fo = l16 * LIN_BYTES + (((FP8 ? 2 * q4 : q4) ^ (l16 & 7)) << 4);
+  // operand reads of a 16-row tile. Along the contraction: chunks q4 and q4 + 4 of a row (bf16: one for each half step;
+  // 8-bit: both, in the same order for both operands); the tile's rows are l16 modulo 16, so the places are those of
+  // row l16, 64 bytes apart. (8-bit chunks 2 q4 and 2 q4 + 1 would meet in banks: half the reads' cycles.)
+  const int fo = l16 * LIN_BYTES + ((q4 ^ (l16 & 7)) << 4);
   // Across it (bf16), through the transposing read: in each 16 lanes, lane 4 v + u points at row 8 q4 + 4 h + v,
   // elements 4 u .. + 3, and lane j receives element j % 4 of lane 4 v + j / 4 as its value v.
   using Frag = std::conditional_t<FP8, i32x8_t, bf16x8_t>;
   auto along = [&](const char* t, int tile, int kk) -> Frag {
     const char* p = t + tile * (16 * LIN_BYTES);
     if constexpr (FP8) {
-      const uint4 a = *reinterpret_cast<const uint4*>(p + fo), b = *reinterpret_cast<const uint4*>(p + (fo ^ 16));
+      const uint4 a = *reinterpret_cast<const uint4*>(p + fo), b = *reinterpret_cast<const uint4*>(p + (fo ^ 64));
       return as_i32x8(a, b);
     } else {
       return as_bf16x8(*reinterpret_cast<const uint4*>(p + (fo ^ (kk * 64))));

@@ -103,7 +103,7 @@ def _on_stream(fn):
 def _workspace(workspace, nbytes, device):
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-    _check("workspace", workspace, torch.uint8, workspace.shape, device)
+    _check("workspace", workspace, torch.uint8, getattr(workspace, "shape", ()), device)
     return workspace
 
 
@@ -131,8 +131,8 @@ def rmsnorm_forward(x, w, *, residual=None, eps=1e-6, fp8=False, r=None, y=None)
         _check("r", r, x.dtype, x.shape, dev)
     if fp8:
         if y is None:
-            y = Fp8Tensor(torch.empty((m, d), dtype=FP8, device=dev),
-                          torch.empty((_blocks(d), m), dtype=torch.float32, device=dev), 1)
+            y = Fp8Tensor(torch.empty(m, d, dtype=FP8, device=dev),
+                          torch.empty(_blocks(d), m, dtype=torch.float32, device=dev), 1)
         else:
             _check_fp8("y", y, (m, d), 1, dev)
         out, q, scale = None, y.q, y.scale
@@ -176,7 +176,7 @@ def _accumulator(name, t, accumulate, shape, dev):
     if t is None:
         if accumulate:
             raise ValueError(f"{name}: accumulate needs the tensor that is added to")
-        return torch.empty(shape, dtype=torch.float32, device=dev)
+        return torch.empty(*shape, dtype=torch.float32, device=dev)
     _check(name, t, torch.float32, shape, dev)
     return t
 
@@ -201,14 +201,14 @@ def fp8_quantize(x, *, block_rows=1, transposed=False, out=None, out_t=None):
     *lead, m, k = x.shape
     shape_t = (*lead, k, (m + 15) // 16 * 16)
     if out is None:
-        out = Fp8Tensor(torch.empty(x.shape, dtype=FP8, device=dev),
-                        torch.empty(_scale_shape(x.shape, block_rows), dtype=torch.float32, device=dev), block_rows)
+        out = Fp8Tensor(torch.empty_like(x, dtype=FP8),
+                        torch.empty(*_scale_shape(x.shape, block_rows), dtype=torch.float32, device=dev), block_rows)
     else:
         _check_fp8("out", out, x.shape, block_rows, dev)
     if transposed:
         if out_t is None:
-            out_t = Fp8Tensor(torch.empty(shape_t, dtype=FP8, device=dev),
-                              torch.empty(_scale_shape(shape_t, block_rows), dtype=torch.float32, device=dev),
+            out_t = Fp8Tensor(torch.empty(*shape_t, dtype=FP8, device=dev),
+                              torch.empty(*_scale_shape(shape_t, block_rows), dtype=torch.float32, device=dev),
                               block_rows)
         else:
             _check_fp8("out_t", out_t, shape_t, block_rows, dev)
@@ -266,10 +266,11 @@ def _product_out(y, shape, out_dtype, dev, accumulate=False):
             raise ValueError("y: accumulate needs the tensor that is added to")
         if out_dtype not in _DTYPES:
             raise ValueError(f"out_dtype: bfloat16 or float32, got {out_dtype}")
-        return torch.empty(shape, dtype=out_dtype, device=dev)
-    if accumulate and y.dtype != torch.float32:
+        return torch.empty(*shape, dtype=out_dtype, device=dev)
+    dtype = getattr(y, "dtype", None)
+    if accumulate and dtype != torch.float32:
         raise ValueError("y: accumulate needs fp32")
-    _check("y", y, y.dtype if y.dtype in _DTYPES else torch.bfloat16, shape, dev)
+    _check("y", y, dtype if dtype in _DTYPES else torch.bfloat16, shape, dev)
     return y
 
 
