@@ -540,12 +540,15 @@ LinPlan lin_plan(int kind, int exact, int rows, int cols, int K, int groups) {
   LinPlan p{};
   p.ks = 1;
   const int per = kind == LIN_DW ? rows : (rows + groups - 1) / groups, bytes = kind == LIN_FP8 ? 1 : 2;
-  // Few rows: k_linear_skinny up to 16; up to 32 while the weights are few enough for latency to count (24 rows of five
-  // experts: 21 MB 13.5 us, 64 x 128 tiles 14.2; 587 MB 167 us, tiles 127)
+  // Few rows: k_linear_skinny up to 16, and up to 32 while the weights are few enough for latency to count (24 rows of
+  // five experts: 21 MB 13.5 us, 64 x 128 tiles 14.2; 587 MB 167 us, tiles 127). Experts of more than 10 rows on the
+  // average have some of more than 16: 32-row tiles then, or for large 8-bit weights k_linear (128 rows over 8 experts:
+  // 268 MB bf16 16-row tiles 90 us, 32-row 68, k_linear 69; 470 MB 8-bit 162, 143, 112).
   const double weights = (double)groups * cols * K * bytes;
-  if ((kind == LIN_FP8 || kind == LIN_FWD) && (per <= 16 || (per <= 32 && weights <= 48e6))) {
+  const bool few = weights <= 48e6, uneven = groups > 1 && per > 10;
+  if ((kind == LIN_FP8 || kind == LIN_FWD) && (per <= 16 ? few || !uneven || kind == LIN_FWD : per <= 32 && few)) {
     p.skinny = 1;
-    p.mb = per <= 16 ? 1 : 2;
+    p.mb = per <= 16 && !uneven ? 1 : 2;
     const int cw = p.mb == 1 || exact ? 16 : 32, nb = (K * bytes + 127) / 128;
     const int rt = (per + 16 * p.mb - 1) / (16 * p.mb) * groups;
     const long long wgs = (long long)(cols + cw - 1) / cw * rt;
