@@ -1,17 +1,30 @@
 // Products of 8-bit blocks and products grouped by expert on gfx950.
 //
 // out[r][c] = sum_j B[r][j] A[c][j]: a workgroup of eight waves owns an RT x CT
-// tile of the output (RT rows, CT columns) and walks the contraction in steps of 128 bytes
-// of a row: one 8-bit block, or 64 bf16 elements. Both operands' slices of the
-// next step travel from memory straight into the other of two LDS stages
-// (16-byte loads to LDS, no registers) while the matrix cores work on this
-// one; one barrier a step. Products run on 16 x 16 MFMA tiles (operand lane l:
-// row l % 16, contraction elements in group l / 16; accumulator lane l:
+// tile of the output (RT rows, CT columns) and walks the contraction in steps
+// of 128 bytes of a row: one 8-bit block, or 64 bf16 elements. Both operands'
+// slices of the next step travel from memory straight into the other of two LDS
+// stages (16-byte loads to LDS, no registers) while the matrix cores work on
+// this one; one barrier a step. Products run on 16 x 16 MFMA tiles (operand
+// lane l: row l % 16, contraction elements in group l / 16; accumulator lane l:
 // columns 4 (l / 16) + v of the output, row l % 16, so a lane stores four
-// neighbours).
+// neighbours). Workgroups stay and walk over the tiles, the next tile's loads
+// going out before this one is stored.
 //
-// LDS layouts, both free of bank conflicts beyond what the instruction width
-// costs. An operand whose rows run along the contraction keeps 128-byte rows,
+// What bounds it. A 256 x 256 step needs 2048 cycles of the matrix cores, 64 KB
+// into LDS and 192 KB out of it (770 cycles); whole rounds of such tiles run at
+// 1.37-1.40 PFLOP/s in bf16 (4096 x 8192 x 4096: 197-203 us) and 2.1-2.2 in 8
+// bits (4096 x 4096 x 8192: 120-124 us), where the chip is held by its power:
+// the bf16 product of zeros takes 190 us where normal numbers took 215-260 on
+// an earlier version of the loop. Beyond that it is shape: half-empty last
+// rounds (4096 x 4096 x 14336 8-bit, 3.5 rounds: 235 us, 2.05 PFLOP/s) and last
+// tiles of the experts (8192 rows over 8 experts, 4096 x 14336: 850-880 us, 1.1
+// PFLOP/s). Exact 8-bit sums take 128 x 256 tiles, whose registers also hold
+// the converted operand (14336 x 4096 over 4096: 470 us, 1.02 PFLOP/s). dW is
+// bound by its stores between short tiles (8 x 8192 x 2048 over 4095 rows: 250
+// us for 137 GFLOP and 537 MB; 165 without the stores).
+//
+// LDS layouts, both without bank conflicts. An operand whose rows run along the contraction keeps 128-byte rows,
 // chunk c of 16 bytes at c ^ (row % 8): the 16 rows of a 16-byte operand read
 // fall into different banks. An operand read across its rows (W in dx, both in
 // dW: the contraction is the slower index) keeps the rows as they lie in
@@ -24,8 +37,8 @@
 // 8 products (8 consecutive k of a row) to 13 bits below its largest product
 // and add such sums in fp32 (measured: 2^16 + 2^3 is exact, 2^16 + 2^2 is
 // 2^16, and sums of different eights are exact to 24 bits). That is about
-// 1.3e-5 of a sum of normal values, 2^-8 of it at worst: far below the
-// rounding of a bf16 output, but not fp32. So an fp32 output (a weight's
+// 1.3e-5 of a sum of normal values, and at most 7 * 2^-13 of each eight's
+// largest product: far below the rounding of a bf16 output, but not fp32. So an fp32 output (a weight's
 // gradient) is made on the bf16 instructions, at half their rate: every e4m3
 // value is a bf16 value, products of two are exact in fp32, and so are their
 // sums to fp32 roundings. A block's sum starts at zero, is scaled in fp32 and

@@ -3,8 +3,11 @@
 // A workgroup of 256 threads takes a 128 x 128 tile of x: 16 lanes hold a row
 // of it (eight elements a lane), so a row's maximum is four lane moves. The
 // values are read once; the transposed blocks come from the same tile through
-// LDS, where a thread reads half a column. Bound by HBM: x once in, one or
-// two bytes a value out.
+// LDS, where a thread reads half a column (neighbouring lanes neighbouring
+// columns: no bank conflicts) and writes 64 bytes of a transposed row. Bound by
+// HBM: x once in, one or two bytes a value out. Measured, both outputs, bf16:
+// 4091 x 8192 in rows 31.6 us, 14336 x 4096 in 128 x 128 blocks 54.4 us (4.3
+// TB/s; with x in the memory-side cache 39 us).
 #include "lin_util.cuh"
 
 namespace ffn {

@@ -480,6 +480,41 @@ def test_binding_refuses(asg):
         asg.rmsnorm_forward(odd, w)
 
 
+def test_workspaces_given_by_hand(asg):
+    say("workspaces")
+    torch = torch_()
+    from activation_sparse_gated_amd import _lib
+    lib, g = _lib.load(), rng(16)
+    byte = lambda n: torch.empty(n, dtype=torch.uint8, device="cuda")  # noqa: E731
+    m, n, k = 48, 128, 8192
+    x, w = dev(g.normal(0, 1, (m, k))), dev(g.normal(0, k ** -0.5, (2, n, k)))
+    off = torch.tensor([0, 17, m], dtype=torch.int32, device="cuda")
+    need = lib.ffn_grouped_forward_workspace_bytes(m, n, k, 2)
+    assert need > 0                                      # a shape that is cut along k
+    want = L.grouped(f64(x), f64(w), [0, 17, m], np.zeros((m, n)))
+    slack = np.concatenate([product_slack(f64(x)[a:b], f64(w[e]), "bf16") for e, (a, b) in enumerate(((0, 17), (17, m)))])
+    own = asg.grouped_forward(x, w, off)
+    full = asg.grouped_forward(x, w, off, workspace=byte(need))
+    assert np.array_equal(bits(full), bits(own))
+    for small in (byte(16), byte(need - 16)):            # too small: not used, not written
+        small.fill_(0x5A)
+        near(f64(asg.grouped_forward(x, w, off, workspace=small)), want, slack, "whole sums")
+        assert bool((small == 0x5A).all())
+    near(f64(own), want, slack, "slices")
+    with pytest.raises(asg.FFNError):
+        asg.grouped_forward(x, w, off, workspace=byte(need + 64)[8:])
+    with pytest.raises(ValueError):
+        asg.grouped_forward(x, w, off, workspace=torch.empty(4, device="cuda"))
+    with pytest.raises(asg.FFNError):
+        asg.rmsnorm_backward(x, dev(g.normal(1, .1, k)), x, workspace=byte(64))
+    # one workspace, one call after the other on the same stream
+    both = byte(max(need, lib.ffn_rmsnorm_backward_workspace_bytes(m, k)))
+    a = asg.grouped_forward(x, w, off, workspace=both)
+    asg.rmsnorm_backward(x, dev(g.normal(1, .1, k)), x, workspace=both)
+    b = asg.grouped_forward(x, w, off, workspace=both)
+    assert np.array_equal(bits(a), bits(own)) and np.array_equal(bits(b), bits(own))
+
+
 # ---------------------------------------------------------------- together
 def block_step(asg, s):
     """One training step of an 8-bit gated block's products with a residual
