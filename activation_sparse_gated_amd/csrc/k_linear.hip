@@ -24,13 +24,13 @@
 // bound by its stores between short tiles (8 x 8192 x 2048 over 4095 rows: 250
 // us for 137 GFLOP and 537 MB; 165 without the stores).
 //
-// LDS layouts, both without bank conflicts. An operand whose rows run along the contraction keeps 128-byte rows,
-// chunk c of 16 bytes at c ^ (row % 8): the 16 rows of a 16-byte operand read
-// fall into different banks. An operand read across its rows (W in dx, both in
-// dW: the contraction is the slower index) keeps the rows as they lie in
-// memory, 64 of them a step, and is transposed on the way to the registers by
-// ds_read_b64_tr_b16; chunk c lies at c ^ f(row), f spreading the 16 rows one
-// such read touches. Loads to LDS write 16 bytes a lane in lane order, so the
+// LDS layouts, both without bank conflicts. An operand whose rows run along the
+// contraction keeps 128-byte rows, chunk c of 16 bytes at c ^ (row % 8): the 16
+// rows of a 16-byte operand read fall into different banks. An operand read
+// across its rows (W in dx, both in dW: the contraction is the slower index)
+// keeps the rows as they lie in memory, 64 of them a step, and is transposed on
+// the way to the registers by ds_read_b64_tr_b16; chunk c lies at c ^ f(row), f
+// spreading the 16 rows one such read touches. Loads to LDS write 16 bytes a lane in lane order, so the
 // permutation is applied to the address that is read.
 //
 // How 8-bit products are summed. The e4m3 matrix instructions hold each sum of
@@ -38,10 +38,10 @@
 // and add such sums in fp32 (measured: 2^16 + 2^3 is exact, 2^16 + 2^2 is
 // 2^16, and sums of different eights are exact to 24 bits). That is about
 // 1.3e-5 of a sum of normal values, and at most 7 * 2^-13 of each eight's
-// largest product: far below the rounding of a bf16 output, but not fp32. So an fp32 output (a weight's
-// gradient) is made on the bf16 instructions, at half their rate: every e4m3
-// value is a bf16 value, products of two are exact in fp32, and so are their
-// sums to fp32 roundings. A block's sum starts at zero, is scaled in fp32 and
+// largest product: far below the rounding of a bf16 output, but not fp32. So an
+// fp32 output (a weight's gradient) is made on the bf16 instructions, at half
+// their rate: every e4m3 value is a bf16 value, products of two are exact in
+// fp32, and so are their sums to fp32 roundings. A block's sum starts at zero, is scaled in fp32 and
 // added to the accumulator.
 #include <algorithm>
 #include <type_traits>
@@ -117,7 +117,7 @@ struct LinSrc {
       base = p + ((size_t)r0 * ld + k0) * ESZ;
       step = LIN_BYTES;
       first = T::row_of(tid) * pitch + T::chunk_of(tid) * 16;
-      last = (uint32_t)(rend - 1 - r0) * pitch + T::chunk_of(tid) * 16;
+      last = (uint32_t)min(rend - 1 - r0, R - 1) * pitch + T::chunk_of(tid) * 16;   // of the tile: 32 bits hold that, not the operand
     } else {
       base = p + ((size_t)k0 * ld + r0) * ESZ;
       step = (size_t)64 * pitch;

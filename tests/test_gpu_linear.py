@@ -733,3 +733,28 @@ def test_products_past_32_bits(asg):
     near(f64(dx[8:, -5:]), D[8:] @ f64(w[8, :, -5:]), product_slack(D[8:], f64(w[8, :, -5:]).T, "bf16"), "dx")
     y = asg.grouped_forward(x, w, off)
     near(f64(y[8:, -5:]), X[8:] @ f64(w[8, -5:]).T, product_slack(X[8:], f64(w[8, -5:]), "bf16"), "y")
+
+
+def test_products_of_operands_of_4_gib(asg):
+    # the bytes from the first tile's first row to the operand's last one are 2^32 and seven rows
+    say("operands of 4 GiB")
+    torch = torch_()
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    normal = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)  # noqa: E731
+    big, few, k = 2 ** 18 + 8, 64, 8192
+    a, b = normal(big, k), normal(few, k)
+    A, Bv = f64(a[:256]), f64(b)
+    want, slack = A @ Bv.T, product_slack(A, Bv, "bf16")
+    off = lambda m: torch.tensor([0, m], dtype=torch.int32, device="cuda")  # noqa: E731
+    y = asg.grouped_forward(a, b[None], off(big))
+    near(f64(y[:256]), want, slack, "rows")
+    y = asg.grouped_forward(b, a[None], off(few))
+    near(f64(y[:, :256]), want.T, slack.T, "columns")
+    dx, _ = asg.grouped_backward(normal(big, few), b.t().contiguous()[None], a, off(big))
+    near(f64(dx[:256]), want, slack, "dx")
+    del a, y, dx
+    k *= 2
+    a, b = asg.fp8_quantize(normal(big, k)), asg.fp8_quantize(normal(few, k), block_rows=128)
+    A, Bv = (t.double().cpu().numpy() for t in (asg.Fp8Tensor(a.q[:256], a.scale[:, :256], 1).dequantize(), b.dequantize()))
+    y = asg.fp8_linear(a, b)
+    near(f64(y[:256]), A @ Bv.T, product_slack(A, Bv, "bf16") + 7 * 2.0 ** -13 * eights(A, Bv), "8-bit rows")
