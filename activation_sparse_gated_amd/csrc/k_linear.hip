@@ -559,7 +559,9 @@ LinPlan lin_plan(int kind, int exact, int rows, int cols, int K, int groups) {
   // 268 MB bf16 16-row tiles 90 us, 32-row 68, k_linear 69; 470 MB 8-bit 162, 143, 112).
   const double weights = (double)groups * cols * K * bytes;
   const bool few = weights <= 48e6, uneven = groups > 1 && per > 10;
-  if ((kind == LIN_FP8 || kind == LIN_FWD) && (per <= 16 ? few || !uneven || kind == LIN_FWD : per <= 32 && few)) {
+  // A grid holds fewer than 2^32 threads.
+  const bool fits = ((long long)(cols + 15) / 16) * (rows / 16 + groups) < 1 << 22;
+  if ((kind == LIN_FP8 || kind == LIN_FWD) && fits && (per <= 16 ? few || !uneven || kind == LIN_FWD : per <= 32 && few)) {
     p.skinny = 1;
     p.mb = per <= 16 && !uneven ? 1 : 2;
     const int cw = p.mb == 1 || exact ? 16 : 32, nb = (K * bytes + 127) / 128;

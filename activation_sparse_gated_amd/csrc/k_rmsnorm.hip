@@ -37,8 +37,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_fwd(const Nor
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
   __shared__ float s_red[TPR / 64];
   const int t = threadIdx.x % TPR;
-  const int row = blockIdx.x * RPB + threadIdx.x / TPR;
-  if (row >= n.m) return;                        // TPR > 64: one row a workgroup, never taken
+  const int row = (blockIdx.y * gridDim.x + blockIdx.x) * RPB + threadIdx.x / TPR;
+  if (row >= n.m) return;                        // TPR > 64: one row a workgroup, all of it returns
   const size_t base = (size_t)row * n.d;
   Row8<T> xv[NC], rv[NC], wv[NC];
 #pragma unroll
@@ -210,7 +210,9 @@ int rmsnorm_bwd_parts(int m, int d) {
 template <typename T, int TPR, int NC>
 static hipError_t go_fwd(const NormDesc& n, hipStream_t s) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-  ffn_launch((k_rmsnorm_fwd<T, TPR, NC>), dim3((n.m + RPB - 1) / RPB), dim3(TPR < 256 ? 256 : TPR), 0, s, n);
+  // a grid holds fewer than 2^32 threads a dimension
+  const int groups = (n.m + RPB - 1) / RPB, y = (groups + (1 << 21) - 1) >> 21;
+  ffn_launch((k_rmsnorm_fwd<T, TPR, NC>), dim3((groups + y - 1) / y, y), dim3(TPR < 256 ? 256 : TPR), 0, s, n);
   return hipGetLastError();
 }
 template <typename T>

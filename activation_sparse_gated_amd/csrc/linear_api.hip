@@ -23,13 +23,14 @@ hipStream_t st(void* stream) { return reinterpret_cast<hipStream_t>(stream); }
 
 constexpr int kMaxRowTiles = 1 << 30;
 constexpr int kMaxWidth = 1 << 22;   // 256 rows of it stay within 32-bit byte offsets
+constexpr int kMaxRows = 0x7FFF0000; // a row's number and a few tiles more stay within 32 bits
 
 bool norm_shape_ok(int32_t dtype, int32_t m, int32_t d, float eps) {
-  return dtype_ok(dtype) && m >= 0 && d >= 8 && d % 8 == 0 && d <= 16384 && std::isfinite(eps) && eps >= 0.f;
+  return dtype_ok(dtype) && m >= 0 && m <= kMaxRows && d >= 8 && d % 8 == 0 && d <= 16384 && std::isfinite(eps) && eps >= 0.f;
 }
 // Tiles of the largest grid any kernel makes for this product, in workgroups.
 bool product_shape_ok(int32_t m, int32_t n, int32_t k, int32_t groups) {
-  if (m < 0 || n < 1 || k < 1 || groups < 1 || groups > FFN_LINEAR_MAX_GROUPS) return false;
+  if (m < 0 || m > kMaxRows || n < 1 || k < 1 || groups < 1 || groups > FFN_LINEAR_MAX_GROUPS) return false;
   if (n > kMaxWidth || k > kMaxWidth) return false;
   const long long rt = m / 16 + groups, ct = n / 16 + 1, kt = k / 16 + 1;
   return rt * ct < kMaxRowTiles && ct * kt * groups < kMaxRowTiles && rt * kt < kMaxRowTiles;
@@ -101,7 +102,10 @@ ffn_status ffn_fp8_quantize(const void* x, int32_t dtype, int32_t groups, int32_
                             uint8_t* q, float* scale, uint8_t* qt, float* scale_t, void* stream) {
   if (!dtype_ok(dtype) || groups < 1 || m < 0 || k < 16 || k % 16 != 0 || (block_rows != 1 && block_rows != 128))
     return FFN_E_INVALID;
-  if ((long long)((k + 127) / 128) * ((m + 127) / 128) * groups > 0x7FFFFFFFll || m > 0x7FFFFF00) return FFN_E_UNSUPPORTED;
+  if (m > kMaxRows || k > kMaxRows) return FFN_E_UNSUPPORTED;
+  // a grid holds fewer than 2^32 threads: 256 for each tile
+  const long long tiles = (long long)((k + 127) / 128) * ((m + 127) / 128);
+  if (tiles >= 1 << 24 || tiles * groups >= 1 << 24) return FFN_E_UNSUPPORTED;
   if (m == 0) return FFN_OK;
   if (!need(x) || !need(q) || !need(scale) || !opt(qt) || !opt(scale_t) || (qt != nullptr) != (scale_t != nullptr))
     return FFN_E_INVALID;

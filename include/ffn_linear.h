@@ -13,7 +13,8 @@
  * streams, as long as no two of them share a workspace or an output. All may
  * be captured into a graph. A call with no rows (m = 0) does nothing but what
  * is said below, and takes null pointers. FFN_E_HIP reports a failed launch.
- * `dtype` is ffn_dtype (FFN_F32 or FFN_BF16); sums are held in fp32.
+ * `dtype` is ffn_dtype (FFN_F32 or FFN_BF16); sums are held in fp32, so rows
+ * whose squares pass its range have an infinite mean. m is at most 2^31 - 2^16.
  *
  * 8-bit blocks. A matrix [m x k] held in 8 bits is
  *   q      uint8 [m x k]: e4m3 (OCP; 1 sign, 4 exponent and 3 mantissa bits,
@@ -87,7 +88,8 @@ ffn_status ffn_rmsnorm_backward(const void *r, const void *w, const void *dy, co
  *               scales: of blocks of 1 x 128, that is of 128 rows of x
  *               (block_rows = 1: [groups x ceil(m/128) x k]), or the same blocks of
  *               128 x 128 (block_rows = 128: [groups x ceil(k/128) x ceil(m/128)])
- * k: multiple of 16. block_rows: 1 or 128. */
+ * k: multiple of 16. block_rows: 1 or 128. Fewer than 2^24 tiles of 128 x 128 in
+ * all, begun ones counted (FFN_E_UNSUPPORTED otherwise). */
 ffn_status ffn_fp8_quantize(const void *x, int32_t dtype, int32_t groups, int32_t m, int32_t k,
                             int32_t block_rows, uint8_t *q, float *scale, uint8_t *qt, float *scale_t,
                             void *stream);

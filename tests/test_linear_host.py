@@ -55,6 +55,16 @@ def test_norm_backward_refusals(lib, kw, want):
     assert lib.ffn_rmsnorm_backward_workspace_bytes(-1, 64) == 0 == lib.ffn_rmsnorm_backward_workspace_bytes(4, 12)
 
 
+def test_row_limits(lib):
+    top = 2 ** 31 - 2 ** 16
+    assert lib.ffn_rmsnorm_backward_workspace_bytes(top, 64) > 0 == lib.ffn_rmsnorm_backward_workspace_bytes(top + 1, 64)
+    assert norm(lib, m=top + 1) == INVALID == norm_b(lib, m=2 ** 31 - 1)
+    assert linear(lib, m=2 ** 31 - 1, n=16, k=16) == INVALID == fwd(lib, m=2 ** 31 - 1, n=16, k=16)
+    assert bwd(lib, m=top + 1, n=16, k=16) == INVALID
+    for kw in (dict(m=top + 1, k=16), dict(g=2 ** 24, m=1, k=16), dict(g=2 ** 31 - 1, m=2 ** 30, k=2 ** 30), dict(k=2 ** 31 - 16)):
+        assert quant(lib, **kw) == UNSUPPORTED
+
+
 def quant(lib, x=P, dtype=1, g=1, m=4, k=64, rows=1, q=P, s=P, qt=None, st=None):
     return lib.ffn_fp8_quantize(x, dtype, g, m, k, rows, q, s, qt, st, None)
 
