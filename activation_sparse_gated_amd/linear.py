@@ -91,9 +91,9 @@ def _on_stream(fn):
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
-        first = args[0] if args else next(iter(kw.values()))
-        device = getattr(first.q if isinstance(first, Fp8Tensor) else first, "device", None)
-        if device != stream.device:
+        tensors = (a.q if isinstance(a, Fp8Tensor) else a for a in (*args, *kw.values()))
+        device = next((t.device for t in tensors if isinstance(t, torch.Tensor)), None)
+        if device not in (None, stream.device):
             raise ValueError(f"stream: of {stream.device}, the tensors are on {device}")
         with torch.cuda.stream(stream):
             return fn(*args, **kw)

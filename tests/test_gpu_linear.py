@@ -758,3 +758,39 @@ def test_products_of_operands_of_4_gib(asg):
     A, Bv = (t.double().cpu().numpy() for t in (asg.Fp8Tensor(a.q[:256], a.scale[:, :256], 1).dequantize(), b.dequantize()))
     y = asg.fp8_linear(a, b)
     near(f64(y[:256]), A @ Bv.T, product_slack(A, Bv, "bf16") + 7 * 2.0 ** -13 * eights(A, Bv), "8-bit rows")
+
+
+def test_many_rows(asg):
+    # more rows than a grid of one dimension holds, more workgroups than one of few-row products may have
+    say("many rows")
+    torch = torch_()
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    normal = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)  # noqa: E731
+    m, d = 2 ** 26 + 5, 8
+    x, w = normal(m, d), normal(d)
+    y, _ = asg.rmsnorm_forward(x, w)
+    rows = [0, 3, 2 ** 25 - 1, 2 ** 25, 2 ** 26 - 1, 2 ** 26, m - 1]
+    want = L.rmsnorm(f64(x[rows]), f64(w), EPS)
+    near(f64(y[rows]), want, np.abs(want) * (B + 140 * U), "norm")
+    del x, y
+    g, n, k = 256, 2 ** 19, 16
+    m = 2 * g
+    x, w = normal(m, k), normal(g, n, k)
+    y = asg.grouped_forward(x, w, torch.arange(0, m + 1, 2, dtype=torch.int32, device="cuda"))
+    for e in (0, 1, 100, 255):
+        X, W = f64(x[2 * e:2 * e + 2]), f64(w[e, -300:])
+        near(f64(y[2 * e:2 * e + 2, -300:]), X @ W.T, product_slack(X, W, "bf16"), e)
+
+
+def test_stream_with_keywords_in_any_order(asg):
+    say("stream")
+    torch = torch_()
+    stream = torch.cuda.Stream()
+    x, w = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    stream.wait_stream(torch.cuda.current_stream())
+    y, _ = asg.rmsnorm_forward(eps=1e-6, fp8=False, residual=None, w=w, x=x, stream=stream)
+    q = asg.fp8_quantize(block_rows=128, x=x, stream=stream)
+    with pytest.raises(TypeError):
+        asg.fp8_quantize(block_rows=128, stream=stream)
+    stream.synchronize()
+    assert bool((y == 1).all()) and bool((q.dequantize() == 1).all())
