@@ -474,10 +474,16 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
     const int orow = KIND == LIN_DW ? x.g * d.rows : 0;
     if (x.r0 + RT <= x.rend && x.c0 + CT <= d.cols && (d.cols & 3) == 0 && !(d.accumulate && d.ks == 1)) {
 #pragma unroll
-      for (int j = 0; j < BT; ++j)
+      for (int j = 0; j < BT; ++j) {
+        const int row = orow + x.r0 + (wr * BT + j) * 16 + l16, col = x.c0 + wc * AT * 16 + 4 * q4;
+        // dW past the caches: 537 MB of it between the operands' tiles 278 us, so 224
+        f32x4_t* o = reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(d.out) + (size_t)row * d.cols + col);
 #pragma unroll
-        for (int i = 0; i < AT; ++i)
-          lin_store4<KIND == LIN_DW>(d, x.z, orow + x.r0 + (wr * BT + j) * 16 + l16, x.c0 + (wc * AT + i) * 16 + 4 * q4, acc[i][j]);
+        for (int i = 0; i < AT; ++i) {
+          if (KIND == LIN_DW) __builtin_nontemporal_store(acc[i][j], o + 4 * i);
+          else lin_store4(d, x.z, row, col + 16 * i, acc[i][j]);
+        }
+      }
       continue;
     }
 #pragma unroll

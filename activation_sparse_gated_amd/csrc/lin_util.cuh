@@ -111,11 +111,10 @@ __device__ __forceinline__ bool lin_tile(const LinDesc& d, int tile, int& g, int
 
 // Four neighbouring outputs (row, col ..) in one store of 16 (bf16: 8) bytes:
 // to the slab of slice z, or to the output. d.cols is a multiple of 4.
-template <bool F32 = false>                      // fp32, one slice
 __device__ __forceinline__ void lin_store4(const LinDesc& d, int z, int row, int col, f32x4_t a) {
   const size_t at = (size_t)row * d.cols + col;
-  if (!F32 && d.ks > 1) *reinterpret_cast<f32x4_t*>(d.part + (size_t)z * d.rows * d.cols + at) = a;
-  else if (F32 || d.out_f32) *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(d.out) + at) = a;
+  if (d.ks > 1) *reinterpret_cast<f32x4_t*>(d.part + (size_t)z * d.rows * d.cols + at) = a;
+  else if (d.out_f32) *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(d.out) + at) = a;
   else *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(d.out) + at) = uint2{pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
 }
 // The same, added to what the output holds if the product accumulates; columns
