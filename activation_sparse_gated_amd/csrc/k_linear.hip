@@ -21,7 +21,7 @@
 // tiles of the experts (8192 rows over 8 experts, 4096 x 14336: 850-880 us, 1.1
 // PFLOP/s). Exact 8-bit sums take 128 x 256 tiles, whose registers also hold
 // the converted operand (14336 x 4096 over 4096: 470 us, 1.02 PFLOP/s). dW is
-// bound by its stores between short tiles (8 x 8192 x 2048 over 4095 rows: 250
+// bound by its stores between short tiles (8 x 8192 x 2048 over 4095 rows: 224
 // us for 137 GFLOP and 537 MB; 165 without the stores).
 //
 // LDS layouts, both without bank conflicts. An operand whose rows run along the
