@@ -20,8 +20,8 @@
 // rounds (4096 x 4096 x 14336 8-bit, 3.5 rounds: 235 us, 2.05 PFLOP/s) and last
 // tiles of the experts (8192 rows over 8 experts, 4096 x 14336: 850-880 us, 1.1
 // PFLOP/s). Exact 8-bit sums take 128 x 256 tiles, whose registers also hold
-// the converted operand (14336 x 4096 over 4096: 470 us, 1.02 PFLOP/s). dW is
-// bound by its stores between short tiles (8 x 8192 x 2048 over 4095 rows: 224
+// the converted operand (14336 x 4096 over 4096: 464 us, 1.04 PFLOP/s). dW is
+// bound by its stores between short tiles (8 x 8192 x 2048 over 4095 rows: 192
 // us for 137 GFLOP and 537 MB; 165 without the stores).
 //
 // LDS layouts, both without bank conflicts. An operand whose rows run along the
@@ -473,17 +473,38 @@ __global__ __launch_bounds__(LIN_THREADS, RT * CT > 128 * 128 ? 2 : 4) void k_li
     if (KIND == LIN_DW && x.steps == 0 && d.accumulate) continue;
     const int orow = KIND == LIN_DW ? x.g * d.rows : 0;
     if (x.r0 + RT <= x.rend && x.c0 + CT <= d.cols && (d.cols & 3) == 0 && !(d.accumulate && d.ks == 1)) {
+      const int row0 = orow + x.r0 + wr * BT * 16, col0 = x.c0 + wc * AT * 16 + 4 * q4;
+      constexpr bool LINES = AT % 2 == 0 && !(EXACT && RT * CT <= 128 * 128);   // registers: 52 spilled there, 1% slower
+      if (LINES && (KIND == LIN_DW || EXACT || d.ks > 1 || d.out_f32)) {
+        // fp32 in whole lines of 128 bytes, past the caches: of two neighbouring 16 x 16 tiles, lanes 8 .. 15 of a DPP row
+        // swap their rows with lanes 0 .. 7 of the other tile, so that a store has 8 rows of 32 columns. (Both gradients
+        // of 4095 rows, 8 x 8192 x 2048: through the caches 462 us, past them 423, with whole lines 398; the 8-bit
+        // weight gradient 475 -> 464. bf16 outputs are parts of lines, which L2 has to join: 234 -> 270.)
+        float* out = d.ks > 1 ? d.part + (size_t)x.z * d.rows * d.cols : reinterpret_cast<float*>(d.out);
+        out += (size_t)(row0 + (l16 & 7)) * d.cols + col0 + (l16 >> 3) * 16;
 #pragma unroll
-      for (int j = 0; j < BT; ++j) {
-        const int row = orow + x.r0 + (wr * BT + j) * 16 + l16, col = x.c0 + wc * AT * 16 + 4 * q4;
-        // dW past the caches: 537 MB of it between the operands' tiles 278 us, so 224
-        f32x4_t* o = reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(d.out) + (size_t)row * d.cols + col);
+        for (int j = 0; j < BT; ++j) {
+          f32x4_t* o = reinterpret_cast<f32x4_t*>(out + (size_t)(j * 16) * d.cols);
+          f32x4_t* o8 = reinterpret_cast<f32x4_t*>(out + (size_t)(j * 16 + 8) * d.cols);
 #pragma unroll
-        for (int i = 0; i < AT; ++i) {
-          if (KIND == LIN_DW) __builtin_nontemporal_store(acc[i][j], o + 4 * i);
-          else lin_store4(d, x.z, row, col + 16 * i, acc[i][j]);
+          for (int i = 0; i + 1 < AT; i += 2) {
+            f32x4_t a = acc[i][j], b = acc[i + 1][j];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int av = __float_as_int(a[v]), bv = __float_as_int(b[v]);
+              a[v] = __int_as_float(__builtin_amdgcn_update_dpp(av, bv, 0x128, 0xf, 0xc, false));   // row_ror:8
+              b[v] = __int_as_float(__builtin_amdgcn_update_dpp(bv, av, 0x128, 0xf, 0x3, false));
+            }
+            __builtin_nontemporal_store(a, o + 4 * i);
+            __builtin_nontemporal_store(b, o8 + 4 * i);
+          }
         }
+        continue;
       }
+#pragma unroll
+      for (int j = 0; j < BT; ++j)
+#pragma unroll
+        for (int i = 0; i < AT; ++i) lin_store4(d, x.z, row0 + j * 16 + l16, col0 + 16 * i, acc[i][j]);
       continue;
     }
 #pragma unroll
