@@ -8,14 +8,22 @@
 // HBM: x once in, one or two bytes a value out. Measured, both outputs, bf16:
 // 4091 x 8192 in rows 31.6 us, 14336 x 4096 in 128 x 128 blocks 54.4 us (4.3
 // TB/s; with x in the memory-side cache 39 us).
+#include <type_traits>
+
 #include "lin_util.cuh"
 
 namespace ffn {
 
 constexpr int kQT = 128;                         // tile edge
+// The tile in LDS, written 16 bytes at a time: its start and every row of it lie on 16-byte boundaries.
 template <typename T>
-struct QTile {
+struct alignas(16) QTile {
   static constexpr int LD = kQT + 16 / sizeof(T);  // one 16-byte chunk of padding a row
+  static_assert(LD * sizeof(T) % 16 == 0, "rows of whole chunks");
+  T x[kQT * LD];
+};
+struct QNoTile {
+  static constexpr int LD = 0;
 };
 
 __device__ __forceinline__ float q_elem(const uint16_t* p) { return bf2f(*p); }
@@ -23,8 +31,10 @@ __device__ __forceinline__ float q_elem(const float* p) { return *p; }
 
 template <typename T, int ROWS, bool TRANS>
 __global__ __launch_bounds__(256) void k_fp8_quant(const QuantDesc d, int tiles_k, int tiles_m) {
-  constexpr int LD = QTile<T>::LD;
-  __shared__ T s_x[TRANS ? kQT * LD : 1];
+  using Tile = std::conditional_t<TRANS, QTile<T>, QNoTile>;
+  constexpr int LD = Tile::LD;
+  static_assert(!TRANS || alignof(Tile) % 16 == 0, "16-byte LDS stores");
+  __shared__ Tile s_x;
   __shared__ uint32_t s_max[4];
   __shared__ float s_scale[kQT];
   __shared__ uint32_t s_col[2][kQT];
@@ -65,14 +75,14 @@ __global__ __launch_bounds__(256) void k_fp8_quant(const QuantDesc d, int tiles_
     const float s = ROWS > 1 ? sall : fp8_scale(mx[i]);
     if (ROWS == 1 && c == 0) s_scale[lr] = s;
     if (row < d.m && col < d.k) *reinterpret_cast<uint2*>(d.q + base + (size_t)row * d.k + col) = fp8_pack8(f, 1.0f / s);
-    if constexpr (TRANS) Row8<T>::store(s_x, lr * LD + c * 8, f);
+    if constexpr (TRANS) Row8<T>::store(s_x.x, lr * LD + c * 8, f);
   }
   if (ROWS == 1 || TRANS) __syncthreads();
   if (ROWS == 1 && tid < kQT && m0 + tid < d.m) d.scale[((size_t)g * tiles_k + tk) * d.m + m0 + tid] = s_scale[tid];
   if constexpr (TRANS) {
     // column lc, rows 64 half .. + 63 of the tile
     const int lc = tid & (kQT - 1), half = tid >> 7;
-    const T* p = s_x + half * 64 * LD + lc;
+    const T* p = s_x.x + half * 64 * LD + lc;
     float s = sall;
     if constexpr (ROWS == 1) {
       uint32_t m = 0u;
