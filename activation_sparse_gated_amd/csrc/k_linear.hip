@@ -599,8 +599,9 @@ LinPlan lin_plan(int kind, int exact, int rows, int cols, int K, int groups) {
     while (wgs * p.ks < 256 && p.ks < 16 && nb / (p.ks * 2) >= 2 * p.nw) p.ks *= 2;
     return p;
   }
-  const int steps = ((kind == LIN_DW ? (K + groups - 1) / groups : K) * bytes + LIN_BYTES - 1) / LIN_BYTES;
-  float best = 1e30f;
+  // in 64 bits: the contraction of dW is the rows, up to 2^31
+  const int steps = (int)(((long long)(kind == LIN_DW ? (K + groups - 1) / groups : K) * bytes + LIN_BYTES - 1) / LIN_BYTES);
+  double best = 1e30;                            // us: a float would lose the tiles' own costs beside 2^24 steps
   for (const Option& o : options) {
     long long rt = (long long)((per + o.rt - 1) / o.rt) * groups;
     if (kind != LIN_DW && groups > 1) rt = std::max<long long>(rt, (rows + o.rt - 1) / o.rt + groups / 2);
@@ -612,8 +613,8 @@ LinPlan lin_plan(int kind, int exact, int rows, int cols, int K, int groups) {
       const bool cold = kind != LIN_DW && weights > kCached;
       float step = std::max(o.step[kind == LIN_FP8 ? exact : 2] * each, cold ? 0.95f : 0.6f);
       if (cold) step = std::max(step, (float)(weights / ((double)tiles * steps)) * at_once / kHbm);
-      float t = rounds * (step * ((steps + ks - 1) / ks) + o.tile * each);
-      if (ks > 1) t += kSlabLaunch + 2.f * 4.f * ks * rows * (float)cols / kSlabRate;
+      double t = rounds * ((double)step * ((steps + ks - 1) / ks) + o.tile * each);
+      if (ks > 1) t += kSlabLaunch + 2. * 4. * ks * rows * cols / kSlabRate;
       if (t < best) {
         best = t;
         p.rt = o.rt;
