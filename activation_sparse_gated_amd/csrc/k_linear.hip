@@ -36,9 +36,12 @@
 // How 8-bit products are summed. The e4m3 matrix instructions hold each sum of
 // 8 products (8 consecutive k of a row) to 13 bits below its largest product
 // and add such sums in fp32 (measured: 2^16 + 2^3 is exact, 2^16 + 2^2 is
-// 2^16, and sums of different eights are exact to 24 bits). That is about
-// 1.3e-5 of a sum of normal values, and at most 7 * 2^-13 of each eight's
-// largest product: far below the rounding of a bf16 output, but not fp32. So an
+// 2^16, and sums of different eights are exact to 24 bits). That is at most
+// 7 * 2^-13 of each eight's largest product; of the norm of a product of 4096
+// normal values 2e-5, with one channel in a hundred 20 times as large 6e-5, far
+// below a bf16 output's rounding. Where products cancel it is not: 0.5% of
+// those outputs lose more than half a bf16 step, with the large channels 1.2%.
+// So bf16 outputs are made this way, for twice the rate, as the header says, and an
 // fp32 output (a weight's gradient) is made on the bf16 instructions, at half
 // their rate: every e4m3 value is a bf16 value, products of two are exact in
 // fp32, and so are their sums to fp32 roundings. A block's sum starts at zero, is scaled in fp32 and

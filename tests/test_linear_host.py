@@ -139,3 +139,13 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         asg.grouped_forward(x, torch.zeros(2, 8, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32))
     with pytest.raises(ValueError):
         asg.fp8_linear(x, x)
+
+
+def test_contract_says_how_8_bit_sums_are_made():
+    # a bf16 output is summed to fewer bits than an fp32 one: the header and the binding say so, and by how much
+    import activation_sparse_gated_amd as asg
+    text = open(os.path.join(ROOT, "include", "ffn_linear.h")).read()
+    about = re.sub(r"\s*\n \* ?", " ", text[text.index("/* y = x w^T of 8-bit blocks"):text.index("ffn_status ffn_fp8_linear")])
+    for words in (about, re.sub(r"\s+", " ", asg.fp8_linear.__doc__)):
+        assert "7 * 2^-13 of the largest product of each eight" in words and "13 bits below" in words
+        assert "take FFN_F32" in words or "take fp32" in words
