@@ -13,7 +13,11 @@ FP8 = [
     (3, 136, 8208, 0), (3, 264, 4112, 0), (7, 77, 400, 0), (20, 136, 8208, 0), (24, 264, 2064, 0),
     (232, 130, 720, 0), (67, 144, 1840, 0), (8219, 1908, 864, 0), (652, 140, 7648, 0), (2772, 130, 4064, 0), (5096, 3078, 720, 0),
     (8723, 1848, 704, 0), (2747, 680, 9744, 0), (6662, 1169, 720, 0), (4128, 481, 6032, 0), (5477, 4444, 720, 0),
-    (8414, 420, 8224, 0), (4851, 793, 8432, 0)]
+    (8414, 420, 8224, 0), (4851, 793, 8432, 0),
+    (3, 136, 8208, 4), (9, 136, 4112, 2), (7, 77, 400, 3), (40, 136, 4112, 3), (29, 77, 656, 2),
+    (237, 129, 720, 3), (107, 132, 1744, 3), (738, 8861, 1888, 8), (3913, 3952, 720, 3), (1127, 140, 3680, 8), (4269, 3086, 704, 8),
+    (444, 129, 11600, 8), (1453, 6652, 720, 8), (432, 2844, 8880, 3), (8411, 933, 704, 8), (4037, 436, 6624, 3),
+    (3226, 6824, 720, 5), (8045, 393, 8640, 5)]
 FWD = [
     (3, 136, 4104, 1), (5, 72, 328, 3), (40, 136, 4104, 3), (29, 72, 328, 2), (3, 136, 8200, 4), (2, 520, 2056, 1),
     (221, 136, 456, 1), (104, 152, 848, 3), (780, 8840, 928, 8), (1294, 152, 1896, 3), (5902, 2568, 424, 3), (3545, 272, 6536, 5),

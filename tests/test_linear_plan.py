@@ -41,3 +41,8 @@ def test_the_cases_take_every_instance():
             assert cut == "sliced" or (P.DW, 0, 0, *t, cut) in got
     for f in few:
         assert all((P.FP8, exact, rows, *f) in got for exact in (0, 1) for rows in (1, 128)) and (P.FWD, 0, 0, *f) in got
+    # and both with offsets and without
+    for exact in (0, 1):
+        for key in [(*t, c) for t in tiles for c in ("whole", "sliced") if not (exact and t == (256, 256))] + few:
+            cases = got[(P.FP8, exact, 128, *key)]
+            assert any(c[3] for c in cases) and any(not c[3] for c in cases), (exact, key, cases)
