@@ -148,28 +148,44 @@ def rmsnorm_forward(x, w, *, residual=None, eps=1e-6, fp8=False, r=None, y=None)
 
 
 @_on_stream
-def rmsnorm_backward(r, w, dy, *, dr=None, eps=1e-6, dx=None, dw=None, accumulate=False, workspace=None):
+def rmsnorm_backward(r, w, dy, *, dr=None, eps=1e-6, need_dx=True, need_dw=True, dx=None, dw=None, accumulate=False,
+                     workspace=None):
     """Gradients of the norm of the rows r (ffn_rmsnorm_backward): (dx, dw).
 
     dx [m, d] of r's type is the gradient of x and of the residual, dr (the
     gradient that reaches r besides) included; dw [d] is fp32, written, or added
-    to with accumulate."""
+    to with accumulate. One that is not needed (need_dx, need_dw) is not
+    computed: None in its place."""
     dev = _first("r", r, (torch.bfloat16, torch.float32), (2,))
     m, d = r.shape
     _check("w", w, r.dtype, (d,), dev)
     _check("dy", dy, r.dtype, r.shape, dev)
     if dr is not None:
         _check("dr", dr, r.dtype, r.shape, dev)
-    if dx is None:
-        dx = torch.empty_like(r)
-    else:
-        _check("dx", dx, r.dtype, r.shape, dev)
-    dw = _accumulator("dw", dw, accumulate, (d,), dev)
+    _needs(need_dx, need_dw, dx, dw, accumulate)
+    if need_dx:
+        if dx is None:
+            dx = torch.empty_like(r)
+        else:
+            _check("dx", dx, r.dtype, r.shape, dev)
     lib = _lib.load()
-    workspace = _workspace(workspace, lib.ffn_rmsnorm_backward_workspace_bytes(m, d), dev)
+    if need_dw:
+        dw = _accumulator("dw", dw, accumulate, (d,), dev)
+        workspace = _workspace(workspace, lib.ffn_rmsnorm_backward_workspace_bytes(m, d), dev)
+    else:
+        workspace = None                                # what adds up dw is all that takes one
     _call(lib.ffn_rmsnorm_backward, dev, _ptr(r), _ptr(w), _ptr(dy), _ptr(dr), _DTYPES[r.dtype], m, d,
           float(eps), _ptr(dx), _ptr(dw), int(bool(accumulate)), _ptr(workspace), _nbytes(workspace))
     return dx, dw
+
+
+def _needs(need_dx, need_dw, dx, dw, accumulate):
+    if not (need_dx or need_dw):
+        raise ValueError("need_dx, need_dw: one of the gradients at least")
+    if not need_dx and dx is not None:
+        raise ValueError("dx: given without need_dx")
+    if not need_dw and (dw is not None or accumulate):
+        raise ValueError("dw, accumulate: given without need_dw")
 
 
 def _accumulator(name, t, accumulate, shape, dev):
@@ -304,26 +320,42 @@ def grouped_forward(x, w, offsets, *, y=None, out_dtype=torch.bfloat16, workspac
 
 
 @_on_stream
-def grouped_backward(x, w, dy, offsets, *, dx=None, dw=None, accumulate=False, workspace=None):
+def grouped_backward(x, w, dy, offsets, *, need_dx=True, need_dw=True, dx=None, dw=None, accumulate=False,
+                     workspace=None):
     """Gradients of grouped_forward (ffn_grouped_backward): (dx, dw).
 
     dy [m, n] bf16; dx [m, k] bf16, rows of no expert left as they were; dw
     [experts, n, k] fp32, written (zeros for an expert without rows) or added to
-    with accumulate."""
-    dev = _first("x", x, (torch.bfloat16,), (2,))
-    _first("w", w, (torch.bfloat16,), (3,))
-    m, k = x.shape
-    groups, n, _ = w.shape
-    _check("w", w, torch.bfloat16, (groups, n, k), dev)
-    _check("dy", dy, torch.bfloat16, (m, n), dev)
+    with accumulate. One that is not needed (need_dx, need_dw) is not computed:
+    None in its place. Without dw, x may be None, and w without dx."""
+    _needs(need_dx, need_dw, dx, dw, accumulate)
+    dev = _first("dy", dy, (torch.bfloat16,), (2,))
+    if need_dw or x is not None:
+        _first("x", x, (torch.bfloat16,), (2,))
+    if need_dx or w is not None:
+        _first("w", w, (torch.bfloat16,), (3,))
+    m, n = dy.shape
+    k = x.shape[1] if w is None else w.shape[2]
+    if w is None:
+        _first("offsets", offsets, (torch.int32,), (1,))
+    groups = offsets.shape[0] - 1 if w is None else w.shape[0]
+    if x is not None:
+        _check("x", x, torch.bfloat16, (m, k), dev)
+    if w is not None:
+        _check("w", w, torch.bfloat16, (groups, n, k), dev)
     _check("offsets", offsets, torch.int32, (groups + 1,), dev)
-    if dx is None:
-        dx = torch.empty_like(x)
-    else:
-        _check("dx", dx, torch.bfloat16, x.shape, dev)
-    dw = _accumulator("dw", dw, accumulate, (groups, n, k), dev)
+    if need_dx:
+        if dx is None:
+            dx = torch.empty(m, k, dtype=torch.bfloat16, device=dev)
+        else:
+            _check("dx", dx, torch.bfloat16, (m, k), dev)
+    if need_dw:
+        dw = _accumulator("dw", dw, accumulate, (groups, n, k), dev)
     lib = _lib.load()
-    workspace = _workspace(workspace, lib.ffn_grouped_backward_workspace_bytes(m, n, k, groups), dev)
+    if need_dx:
+        workspace = _workspace(workspace, lib.ffn_grouped_backward_workspace_bytes(m, n, k, groups), dev)
+    else:
+        workspace = None                                # only dx is ever cut along its contraction
     _call(lib.ffn_grouped_backward, dev, _ptr(x), _ptr(w), _ptr(dy), _ptr(offsets), groups, m, n, k, _ptr(dx),
           _ptr(dw), int(bool(accumulate)), _ptr(workspace), _nbytes(workspace))
     return dx, dw
