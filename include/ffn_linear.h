@@ -117,6 +117,10 @@ size_t ffn_fp8_linear_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t g
  * rounding. That is about 2e-5 of a product of normal values, 6e-5 with a few
  * channels 20 times as large; where large products cancel it can be all that is
  * left of an output (2^16 - 2^16 + 2^2 in one eight may come out as 0): take FFN_F32.
+ * A block's sum is multiplied by the product of its two scales, which is made in
+ * fp32 and has to lie in 2^-126 .. 2^128 unless one of the blocks holds zeros only
+ * (of blocks from ffn_fp8_quantize: max|x| max|w| in 2^-108 .. 2^145): above, the
+ * output is infinite, or NaN where the block's sum is 0; below, it loses bits.
  * k: multiple of 16; n, k <= 2^22. Also the backward pass: dx = dy w is the product of dy's
  * blocks with the transposed w, dw = dy^T x the product of dy's and x's
  * transposed blocks (w_block_rows = 1), all from ffn_fp8_quantize. */

@@ -95,3 +95,28 @@ def test_bits_kept_below_the_largest_product(asg, m):
         assert np.array_equal(got, want) if kept else np.all(np.abs(got - want) < 8), (v, apart)
         import torch
         assert np.array_equal(asg.fp8_linear(xb, wb, out_dtype=torch.float32).cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("m", [1, 24, 70, 300])
+def test_scales_at_both_ends_of_their_range(asg, m, rows):
+    """Products of two scales from 2^-126 to 2^127, and blocks of zeros whose scales' product is far below."""
+    import torch
+    print("[case] scales", m, rows, flush=True)
+    n, k = 136, 272
+    g = np.random.default_rng([53, m, rows])
+    kb, nb = 3, 2
+    x, w = np.zeros((m, k)), g.integers(-1, 2, (n, k)).astype(float)
+    x[np.arange(m), g.integers(0, k, m)] = g.choice([-1, 1], m)      # one product an output: -1, 0 or 1
+    for a, b in ((64, 63), (127, 0), (0, 127), (-63, -63), (-126, 0), (0, -126), (-100, 127), (127, -126)):
+        xs, ws = np.full((kb, m), 2.0 ** a), np.full((kb, n) if rows == 1 else (nb, kb), 2.0 ** b)
+        want = (x @ w.T) * 2.0 ** (a + b)
+        xb, wb = blocks_of(asg, x, xs, 1), blocks_of(asg, w, ws, rows)
+        for dtype in (torch.float32, torch.bfloat16):
+            assert np.array_equal(asg.fp8_linear(xb, wb, out_dtype=dtype).double().cpu().numpy(), want), (a, b, dtype)
+    # zeros from the quantiser have scales of 2^-100: nothing comes of them, whatever the other scale
+    zero = asg.fp8_quantize(torch.zeros(m, k, dtype=torch.bfloat16, device="cuda"))
+    for b in (-126, -100, 0, 127):
+        wb = blocks_of(asg, w, np.full((kb, n) if rows == 1 else (nb, kb), 2.0 ** b), rows)
+        for dtype in (torch.float32, torch.bfloat16):
+            assert not bool(asg.fp8_linear(zero, wb, out_dtype=dtype).any())

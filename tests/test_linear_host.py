@@ -149,3 +149,9 @@ def test_contract_says_how_8_bit_sums_are_made():
     for words in (about, re.sub(r"\s+", " ", asg.fp8_linear.__doc__)):
         assert "7 * 2^-13 of the largest product of each eight" in words and "13 bits below" in words
         assert "take FFN_F32" in words or "take fp32" in words
+
+
+def test_contract_gives_the_range_of_scales():
+    text = open(os.path.join(ROOT, "include", "ffn_linear.h")).read()
+    about = re.sub(r"\s*\n \* ?", " ", text[text.index("/* y = x w^T of 8-bit blocks"):text.index("ffn_status ffn_fp8_linear")])
+    assert "product of its two scales" in about and "has to lie in 2^-126 .. 2^128" in about
