@@ -75,14 +75,22 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The handle of torch.cuda.current_stream(index), without the object around it (2 us a call): an entry that torch keeps
+# to itself, so a torch that lacks it goes the long way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(index):
+    return torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
+
+
 def _call(fn, device, *args):
     """The C call on the tensors' own device, on its current stream."""
     index = device.index
     if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
             return _call(fn, device, *args)
-    # the handle of torch.cuda.current_stream(device), without the object around it (2 us a call)
-    check(fn(*args, torch._C._cuda_getCurrentRawStream(index)), fn.__name__)
+    check(fn(*args, _stream_handle(index)), fn.__name__)
 
 
 def _on_stream(fn):

@@ -104,3 +104,16 @@ def test_norm_plain_and_8_bit_at_once(asg, m, d, dtype):
                                            y.data_ptr(), q2.data_ptr(), s2.data_ptr(), stream)
     assert code == _lib.FFN_OK
     assert equal(y, want) and equal(r2, r) and equal(q2, q.q) and equal(s2, q.scale)
+
+
+def test_stream_handle_is_the_current_stream(asg, monkeypatch):
+    import torch
+    from activation_sparse_gated_amd import linear
+    print("[case] stream handle", flush=True)
+    streams = [torch.cuda.current_stream(), torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        with torch.cuda.stream(s):
+            fast = linear._stream_handle(torch.cuda.current_device())
+            with monkeypatch.context() as m:
+                m.setattr(linear, "_raw_stream", None)
+                assert fast == linear._stream_handle(torch.cuda.current_device()) == s.cuda_stream

@@ -155,3 +155,13 @@ def test_contract_gives_the_range_of_scales():
     text = open(os.path.join(ROOT, "include", "ffn_linear.h")).read()
     about = re.sub(r"\s*\n \* ?", " ", text[text.index("/* y = x w^T of 8-bit blocks"):text.index("ffn_status ffn_fp8_linear")])
     assert "product of its two scales" in about and "has to lie in 2^-126 .. 2^128" in about
+
+
+def test_stream_handle_without_the_private_entry(monkeypatch):
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+
+    from activation_sparse_gated_amd import linear
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: SimpleNamespace(cuda_stream=1000 + index))
+    monkeypatch.setattr(linear, "_raw_stream", None)
+    assert linear._stream_handle(3) == 1003
