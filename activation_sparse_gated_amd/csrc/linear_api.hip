@@ -83,7 +83,7 @@ ffn_status ffn_rmsnorm_backward(const void* r, const void* w, const void* dy, co
   }
   NormDesc n{};
   n.x = r;
-  n.res = dr;
+  n.res = dx ? dr : nullptr;                     // dr reaches dx alone: not read without it
   n.w = w;
   n.dy = dy;
   n.dtype = dtype;
