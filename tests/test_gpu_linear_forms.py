@@ -117,3 +117,26 @@ def test_stream_handle_is_the_current_stream(asg, monkeypatch):
             with monkeypatch.context() as m:
                 m.setattr(linear, "_raw_stream", None)
                 assert fast == linear._stream_handle(torch.cuda.current_device()) == s.cuda_stream
+
+
+@pytest.mark.parametrize("m,n,k", [(24, 72, 328), (40, 136, 4104), (300, 264, 520), (1294, 1888, 136), (6100, 408, 2360)])
+def test_rows_and_weights_that_nobody_uses_are_not_read(asg, m, n, k):
+    # NaN in the rows of no expert, and in the weights of experts without rows, reaches nothing
+    import torch
+    print("[case] unread", m, n, k, flush=True)
+    x, w, dy = normal(1, m, k), normal(2, 4, n, k), normal(3, m, n)
+    off = [5, 5, m // 2, m // 2, m - 7]
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    y0, dx0 = normal(4, m, n), normal(5, m, k)
+    want = asg.grouped_forward(x, w, o, y=y0.clone()), *asg.grouped_backward(x, w, dy, o, dx=dx0.clone())
+    q, wq = asg.fp8_quantize(x[:, :k // 16 * 16].contiguous()), asg.fp8_quantize(w[..., :k // 16 * 16].contiguous(), block_rows=128)
+    want8 = [asg.fp8_linear(q, wq, offsets=o, y=y0.to(t, copy=True)) for t in (torch.bfloat16, torch.float32)]
+    for t in (x, dy, q.q.view(torch.uint8)):
+        t[:5], t[m - 7:] = (float("nan"), float("nan")) if t.is_floating_point() else (0x7F, 0x7F)
+    q.scale[:, :5], q.scale[:, m - 7:] = float("nan"), float("nan")
+    for e in (0, 2):
+        w[e], wq.q.view(torch.uint8)[e], wq.scale[e] = float("nan"), 0x7F, float("nan")
+    got = asg.grouped_forward(x, w, o, y=y0.clone()), *asg.grouped_backward(x, w, dy, o, dx=dx0.clone())
+    got8 = [asg.fp8_linear(q, wq, offsets=o, y=y0.to(t, copy=True)) for t in (torch.bfloat16, torch.float32)]
+    for a, b in zip((*got, *got8), (*want, *want8)):
+        assert equal(a, b) and bool(torch.isfinite(a).all())
