@@ -18,11 +18,12 @@
 // the bf16 product of zeros takes 190 us where normal numbers took 215-260 on
 // an earlier version of the loop. Beyond that it is shape: half-empty last
 // rounds (4096 x 4096 x 14336 8-bit, 3.5 rounds: 235 us, 2.05 PFLOP/s) and last
-// tiles of the experts (8192 rows over 8 experts, 4096 x 14336: 850-880 us, 1.1
+// tiles of the experts (8192 rows over 8 experts, 4096 x 14336: 840-880 us, 1.1
 // PFLOP/s). Exact 8-bit sums take 128 x 256 tiles, whose registers also hold
-// the converted operand (14336 x 4096 over 4096: 464 us, 1.04 PFLOP/s). dW is
-// bound by its stores between short tiles (8 x 8192 x 2048 over 4095 rows: 192
-// us for 137 GFLOP and 537 MB; 165 without the stores).
+// the converted operand (14336 x 4096 over 4096: 446-464 us, 1.04-1.08 PFLOP/s).
+// dW is bound by the seams between short tiles and its stores there (8 x 8192 x
+// 2048 over 4095 rows: 187-196 us for 137 GFLOP and 537 MB; 165 without the
+// stores, its whole steps alone 105). Adding to old sums takes 330 us.
 //
 // LDS layouts, both without bank conflicts. An operand whose rows run along the
 // contraction keeps 128-byte rows, chunk c of 16 bytes at c ^ (row % 8): the 16

@@ -14,7 +14,9 @@
 // of whole blocks (blockIdx.y), each writing an fp32 slab that k_linear_sum
 // adds in slice order. An 8-bit 4096 x 14336 product of one token takes 13.0 us
 // (4.5 TB/s of weights), 16 rows over 8 experts of the same size in bf16
-// 125-142 us (5.9-6.7 TB/s of those that have rows).
+// 125-145 us (5.8-6.7 TB/s of those that have rows). Each workgroup finds its
+// tile by walking the experts, with a row tile for each in the grid: 8 rows over 8
+// experts of 2048 x 1024 take 8 us, over 16 15, over 64 175, over 256 2.76 ms.
 #include "lin_util.cuh"
 
 namespace ffn {

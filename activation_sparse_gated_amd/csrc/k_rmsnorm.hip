@@ -9,10 +9,11 @@
 // butterfly in the wave, and one LDS exchange where a row spans waves. With
 // 8-bit output the 16 lanes of a DPP row hold exactly one block of 128
 // columns, so a block's maximum is four lane moves and no LDS. Measured (bf16,
-// residual, 8-bit output): 4096 x 4096 22.1 us, 5.3 TB/s; 1 x 4096 2.4 us, all
-// latency. Backward with the residual's gradient, 4095 x 2048: 13.4-14.0 us
-// (5.0 TB/s) and 3-4 us for the sum of the workgroups' rows of dw: two a CU, so
-// that a row is in flight per wave while they hold 4 MB of partial sums.
+// residual, 8-bit output): 4096 x 4096 22.1 us, 5.3 TB/s (from fp32 39.3 us); 1 x
+// 4096 2.4 us, all latency. Backward with the residual's gradient, 4095 x 2048:
+// 13.4-14.0 us (5.0 TB/s) and 3-4 us for the sum of the workgroups' rows of dw:
+// two a CU, so that a row is in flight per wave while they hold 4 MB of partial
+// sums.
 #include "lin_util.cuh"
 
 namespace ffn {
