@@ -1,4 +1,5 @@
-"""ctypes view of the C ABI in include/ffn_sparse.h, ffn_gsi.h and ffn_linear.h (no computation here)."""
+"""ctypes view of the C ABI in include/ffn_sparse.h, ffn_gsi.h, ffn_linear.h, ffn_experts.h and
+ffn_adapter.h (no computation here)."""
 from __future__ import annotations
 
 import ctypes
@@ -34,6 +35,15 @@ LINEAR_EXPORTS = [
     "ffn_grouped_forward_workspace_bytes", "ffn_grouped_forward", "ffn_grouped_backward_workspace_bytes",
     "ffn_grouped_backward",
 ]
+EXPERTS_EXPORTS = [
+    "ffn_experts_abi_version", "ffn_route_forward", "ffn_route_backward", "ffn_group_rows_workspace_bytes",
+    "ffn_group_rows", "ffn_gather_forward", "ffn_combine_forward", "ffn_combine_backward",
+]
+ADAPTER_EXPORTS = [
+    "ffn_adapter_abi_version", "ffn_adapter_forward_workspace_bytes", "ffn_adapter_forward",
+    "ffn_adapter_backward_workspace_bytes", "ffn_adapter_backward",
+]
+SCORES = {"softmax": 0, "sigmoid": 1}
 GSI_KERNEL_KINDS = {"proj": 0, "resid": 1, "out": 2, "dense": 3}
 
 
@@ -131,6 +141,22 @@ def load() -> ctypes.CDLL:
         "ffn_grouped_backward_workspace_bytes": (c_size_t, [c_int32] * 4),
         "ffn_grouped_backward": (c_int32, [c_void_p] * 4 + [c_int32] * 4 + [c_void_p, c_void_p, c_int32, c_void_p,
                                                                             c_size_t, c_void_p]),
+        "ffn_experts_abi_version": (c_int32, []),
+        "ffn_route_forward": (c_int32, [c_void_p] + [c_int32] * 5 + [c_void_p] + [c_int32] * 4 + [c_float] +
+                              [c_void_p] * 4),
+        "ffn_route_backward": (c_int32, [c_void_p] + [c_int32] * 6 + [c_float] + [c_void_p] * 5),
+        "ffn_group_rows_workspace_bytes": (c_size_t, [c_int32] * 2),
+        "ffn_group_rows": (c_int32, [c_void_p] + [c_int32] * 2 + [c_void_p] * 4 + [c_size_t, c_void_p]),
+        "ffn_gather_forward": (c_int32, [c_void_p] + [c_int32] * 3 + [c_void_p, c_int32] + [c_void_p] * 4),
+        "ffn_combine_forward": (c_int32, [c_void_p] + [c_int32] * 3 + [c_void_p, c_int32] + [c_void_p] * 4),
+        "ffn_combine_backward": (c_int32, [c_void_p] + [c_int32] * 3 + [c_void_p, c_int32] + [c_void_p] * 5),
+        "ffn_adapter_abi_version": (c_int32, []),
+        "ffn_adapter_forward_workspace_bytes": (c_size_t, [c_int32] * 5),
+        "ffn_adapter_forward": (c_int32, [c_void_p] * 6 + [c_int32] * 5 + [c_void_p] * 2 + [c_int32, c_void_p, c_size_t,
+                                                                                         c_void_p]),
+        "ffn_adapter_backward_workspace_bytes": (c_size_t, [c_int32] * 5),
+        "ffn_adapter_backward": (c_int32, [c_void_p] * 7 + [c_int32] * 5 + [c_void_p] * 4 + [c_int32, c_void_p, c_size_t,
+                                                                                          c_void_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -1,0 +1,43 @@
+// Internal interface of the low-rank adapters (include/ffn_adapter.h):
+// descriptors and launches shared by the C ABI layer (adapter_api.hip) and the
+// kernels (k_adapter.hip).
+#pragma once
+#include "kernels.cuh"
+
+namespace ffn {
+
+constexpr int kAdapterMaxGroups = 1024;
+constexpr int kAdapterMaxRank = 256;
+
+// How a call is run (adapter_plan, a rule on sizes alone).
+struct AdapterPlan {
+  int rt;                        // rows of a tile: 16 or 32
+  int ks;                        // slices of the first product's contraction
+  int tiles;                     // tiles at most, those of rows without an adapter among them
+};
+
+struct AdapterDesc {
+  const uint16_t *x, *dy, *a, *b;
+  const float* scales;
+  const int32_t *offsets, *rows;
+  int groups, m, n, k, r;
+  const void* base;
+  void* out;                     // y or dx
+  int out_f32;
+  float *da, *db;
+  int accumulate;
+  AdapterPlan p;
+  // workspace
+  int4* tab;                     // [tiles]: adapter (-1: none), first place, end, index of the adapter's first tile
+  float *h, *dh;                 // [ks][tiles][rt][r]: x A^T and dy B
+};
+
+AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward);
+// first products: h (of x, if d.h) and dh (of dy, if d.dh), and the table of tiles
+hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s);
+// second product: out = base + scale h B^T, or with `back` base + scale dh A
+hipError_t launch_adapter_up(const AdapterDesc& d, bool back, hipStream_t s);
+// gradients of the adapters: da and db, those that are not null
+hipError_t launch_adapter_dw(const AdapterDesc& d, hipStream_t s);
+
+}  // namespace ffn
