@@ -11,7 +11,7 @@ constexpr int kAdapterMaxRank = 256;
 
 // How a call is run (adapter_plan, a rule on sizes alone).
 struct AdapterPlan {
-  int rt;                        // rows of a tile: 16 or 32
+  int rt;                        // rows of a tile: 16 or 64
   int ks;                        // slices of the first product's contraction
   int tiles;                     // tiles at most, those of rows without an adapter among them
 };
@@ -26,10 +26,12 @@ struct AdapterDesc {
   int out_f32;
   float *da, *db;
   int accumulate;
+  int back;                      // a backward pass
   AdapterPlan p;
   // workspace
-  int4* tab;                     // [tiles]: adapter (-1: none), first place, end, index of the adapter's first tile
+  int4* tab;                     // [tiles]: adapter (-1: none, -2: no tile), first place, end
   float *h, *dh;                 // [ks][tiles][rt][r]: x A^T and dy B
+  uint16_t *ht, *dht;            // null, or [tiles][3][r][rt]: the same in three bf16 numbers, rows along
 };
 
 AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward);

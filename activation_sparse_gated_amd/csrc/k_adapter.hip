@@ -15,6 +15,8 @@
 // output's rounding takes), for fp32 outputs as three (2^-24); with ranks up to 16
 // the first two share one instruction, hi in the contraction's first half and
 // lo in its second.
+#include <type_traits>
+
 #include "adapter.cuh"
 #include "lin_util.cuh"
 
@@ -23,46 +25,48 @@ namespace ffn {
 constexpr int kDownWaves = 8;
 
 // ---------------------------------------------------------------- tiles
-// The first place of group g, never before an earlier one's: lanes hold P = ceil(groups / 64) groups each, one after the
-// other; `before` is the largest start of the lanes before.
+// Running maximum over the wave's lanes (of values from 0 up), in DPP moves.
+__device__ __forceinline__ int wave_incl_max(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));
+  return v;
+}
+// Lanes hold `per` = ceil(groups / 64) groups each, one after the other. A group never starts before an earlier one:
+// `before` is the largest start of the lanes before, `first` and `second` the starts of this lane's first group and of
+// the one behind it as the offsets give them.
 struct Groups {
-  int per, before, lane;
+  int per, g0, before, first, second;
 };
 __device__ __forceinline__ Groups groups_of(const AdapterDesc& d) {
   Groups s;
-  s.lane = lane_id();
   s.per = (d.groups + 63) >> 6;
-  int mine = 0;
-  for (int i = 0; i < s.per; ++i) {
-    const int g = s.lane * s.per + i;
-    if (g < d.groups) mine = max(mine, expert_start(d.offsets, g, d.m));
-  }
-  int v = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const int w = __shfl_up(v, o, 64);
-    if (s.lane >= o) v = max(v, w);
-  }
-  const int w = __shfl_up(v, 1, 64);
-  s.before = s.lane ? w : 0;
+  s.g0 = lane_id() * s.per;
+  s.first = expert_start(d.offsets, min(s.g0, d.groups), d.m);
+  s.second = expert_start(d.offsets, min(s.g0 + 1, d.groups), d.m);
+  int mine = s.first;
+  for (int i = 1; i < s.per; ++i) mine = max(mine, expert_start(d.offsets, min(s.g0 + i, d.groups), d.m));
+  const int v = wave_incl_max(mine), w = __shfl_up(v, 1, 64);
+  s.before = lane_id() ? w : 0;
   return s;
 }
 // Calls f(g, first place, end) for this lane's groups in order.
 template <typename F>
 __device__ __forceinline__ void each_group(const AdapterDesc& d, const Groups& s, F f) {
-  int lo = s.before;
-  const int g0 = s.lane * s.per;
-  if (g0 < d.groups) lo = max(lo, expert_start(d.offsets, g0, d.m));
+  int lo = max(s.before, s.first);
   for (int i = 0; i < s.per; ++i) {
-    const int g = g0 + i;
+    const int g = s.g0 + i;
     if (g >= d.groups) break;
-    const int hi = max(lo, expert_start(d.offsets, g + 1, d.m));
+    const int hi = max(lo, i == 0 ? s.second : expert_start(d.offsets, g + 1, d.m));
     f(g, lo, hi);
     lo = hi;
   }
 }
-// Tile `tile`: {adapter, first place, end, index of the adapter's first tile}. Tiles of rows without an adapter (-1) stand
-// behind the others'. adapter -2: there is no such tile.
+// Tile `tile`: {adapter, first place, end, 0}. Tiles of rows without an adapter (-1) stand behind the others'. adapter -2:
+// there is no such tile.
 template <int RT>
 __device__ __forceinline__ int4 adapter_tile(const AdapterDesc& d, int tile) {
   const Groups s = groups_of(d);
@@ -81,18 +85,16 @@ __device__ __forceinline__ int4 adapter_tile(const AdapterDesc& d, int tile) {
       const int n = (hi - lo + RT - 1) / RT;
       if (tile >= first && tile < first + n) {
         const int r0 = lo + (tile - first) * RT;
-        t = int4{g, r0, min(hi, r0 + RT), first};
+        t = int4{g, r0, min(hi, r0 + RT), 0};
       }
       first += n;
     });
-    return int4{wave_read(t.x, from), wave_read(t.y, from), wave_read(t.z, from), wave_read(t.w, from)};
+    return int4{wave_read(t.x, from), wave_read(t.y, from), wave_read(t.z, from), 0};
   }
   // rows of no adapter: before the first group, and behind the last
   const int total = wave_read(incl, 63);
-  int end = last;
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) end = max(end, __shfl_xor(end, o, 64));
-  const int lead = expert_start(d.offsets, 0, d.m), n0 = (lead + RT - 1) / RT;
+  const int end = wave_read(wave_incl_max(last), 63);
+  const int lead = wave_read(s.first, 0), n0 = (lead + RT - 1) / RT;
   tile -= total;
   if (tile < n0) return int4{-1, tile * RT, min(lead, (tile + 1) * RT), 0};
   const int r0 = max(end, lead) + (tile - n0) * RT;
@@ -104,69 +106,146 @@ __device__ __forceinline__ int row_at(const AdapterDesc& d, int place) {
   const int row = d.rows ? d.rows[place] : place;
   return row < 0 || row >= d.m ? -1 : row;
 }
-
-__device__ __forceinline__ uint4 ldg16_if(bool in, const uint16_t* p) { return in ? ldg16(p) : uint4{0, 0, 0, 0}; }
+// v, or zeros. (Loads are made unconditionally, from a place that is there: a branch around each would end their overlap.)
+__device__ __forceinline__ uint4 keep_if(bool in, const uint4 v) { return uint4{in ? v.x : 0u, in ? v.y : 0u, in ? v.z : 0u, in ? v.w : 0u}; }
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return uint4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+}
+// f - bf16(f); nothing behind an infinity
+__device__ __forceinline__ void remainder8(float (&f)[8], const uint4 hi) {
+  float g[8];
+  unpack8(hi, g);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = fabsf(g[e]) == __builtin_huge_valf() ? 0.f : f[e] - g[e];
+}
 
 // ---------------------------------------------------------------- first product
-// h[place][j] = sum over i of u[row][i] A[j][i] for one tile and one slice of the contraction, whose steps the waves take
-// in turn; their sums are added in order. ALONG: the weights' rows run along the contraction (A), otherwise across it (B).
+// h[place][j] = sum over i of u[row][i] W[j][i] for one tile, one slice of the contraction and up to 16 RB ranks from j0
+// on. The waves take the slice's steps of 64 elements in turn, each with the loads of its next one under way; their sums
+// are added in order. ALONG: the weights' rows run along the contraction (A). Otherwise across it (B, rows of r
+// elements): a step's 64 rows go through the wave's own part of LDS, which the transposing read turns: in each 16 lanes,
+// lane 4 v + u points at row 8 q + 4 h + v, elements 4 u .. + 3, and lane j receives element j % 4 of lane 4 v + j / 4.
+constexpr int kDownRanks = 128;                  // of a workgroup
+template <int RT, int RB>
+struct DownLds {
+  static constexpr int PART = kDownWaves * RT * 16 * 4;          // bytes of the waves' sums of 16 ranks
+  static constexpr int W = 64 * 16 * RB * 2 + 32;                // of a wave's step of B; the last row's read runs on a little
+  static constexpr int BYTES = PART > kDownWaves * W ? PART : kDownWaves * W;
+};
 template <int RT, int RB, bool ALONG>
-__device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile, int z, const uint16_t* u, const uint16_t* w,
-                                          int K, float* out, float* s_part) {
+__device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile, int t, int z, int j0, char* lds) {
   constexpr int MB = RT / 16;
   const int lane = lane_id(), wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
+  const uint16_t* u = ALONG ? d.x : d.dy;
+  const int K = ALONG ? d.k : d.n;
   const uint16_t* up[MB];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int row = row_at(d, min(tile.y + i * 16 + l16, tile.z - 1));
-    up[i] = u + (size_t)max(row, 0) * K;
-  }
-  const uint16_t* wg = w + (size_t)tile.x * d.r * K;
+  for (int i = 0; i < MB; ++i) up[i] = u + (size_t)max(row_at(d, min(tile.y + i * 16 + l16, tile.z - 1)), 0) * K;
+  const uint16_t* wg = (ALONG ? d.a : d.b) + (size_t)tile.x * d.r * K + (ALONG ? (size_t)j0 * K : (size_t)j0);
+  const int rw = min(d.r - j0, 16 * RB);         // ranks here
+  const int lw = d.r <= kDownRanks ? d.r : kDownRanks;           // row of B in LDS
+  char* mine = lds + wave * DownLds<RT, RB>::W;
   f32x4_t acc[RB][MB];
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  // steps of 64 elements
   const int steps = (K + 63) / 64, s0 = (int)((long long)steps * z / d.p.ks), s1 = (int)((long long)steps * (z + 1) / d.p.ks);
-  auto step = [&](int at, bool whole) {
-    uint4 uv[MB][2], wv[RB][2];
+  uint4 uv[2][MB][2], wv[2][RB * 2];
+  int brow[RB * 2], bcol[RB * 2];                // this lane's chunks of eight elements of a step of B
+  if constexpr (!ALONG) {
+#pragma unroll
+    for (int n = 0; n < RB * 2; ++n) {
+      const int c = n * 64 + lane;
+      brow[n] = d.r <= kDownRanks ? c * 8 / lw : c >> 4;
+      bcol[n] = d.r <= kDownRanks ? c * 8 - brow[n] * lw : (c & 15) * 8;
+    }
+  }
+  auto load = [&](auto slot, int at) {
+    constexpr int D = decltype(slot)::value;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int c = at * 64 + h * 32 + q * 8;
-      const bool in = whole || c < K;
+      const int c = min(at * 64 + h * 32 + q * 8, K - 8);
 #pragma unroll
-      for (int i = 0; i < MB; ++i) uv[i][h] = ldg16_if(in, up[i] + c);
+      for (int i = 0; i < MB; ++i) uv[D][i][h] = ldg16(up[i] + c);
+      if constexpr (ALONG) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        const int j = b * 16 + l16;
+        for (int b = 0; b < RB; ++b) wv[D][b * 2 + h] = ldg16(wg + (size_t)min(b * 16 + l16, rw - 1) * K + c);
+      }
+    }
+    if constexpr (!ALONG) {
+#pragma unroll
+      for (int n = 0; n < RB * 2; ++n)
+        wv[D][n] = ldg16(wg + (size_t)min(at * 64 + brow[n], K - 1) * d.r + min(bcol[n], rw - 8));
+    }
+  };
+  auto use = [&](auto slot, int at) {
+    constexpr int D = decltype(slot)::value;
+    if (at * 64 + 64 > K) {                      // the last step: nothing behind the contraction's end
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = at * 64 + h * 32 + q * 8 < K;
+#pragma unroll
+        for (int i = 0; i < MB; ++i) uv[D][i][h] = keep_if(in, uv[D][i][h]);
         if constexpr (ALONG) {
-          wv[b][h] = ldg16_if(in, wg + (size_t)min(j, d.r - 1) * K + c);
-        } else {
-          uint32_t v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = in ? wg[(size_t)(c + e) * d.r + min(j, d.r - 1)] : 0u;
-          wv[b][h] = uint4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+          for (int b = 0; b < RB; ++b) wv[D][b * 2 + h] = keep_if(in, wv[D][b * 2 + h]);
         }
       }
+      if constexpr (!ALONG) {
+#pragma unroll
+        for (int n = 0; n < RB * 2; ++n) wv[D][n] = keep_if(at * 64 + brow[n] < K, wv[D][n]);
+      }
+    }
+    if constexpr (!ALONG) {
+#pragma unroll
+      for (int n = 0; n < RB * 2; ++n)
+        if (brow[n] < 64) *reinterpret_cast<uint4*>(mine + (brow[n] * lw + bcol[n]) * 2) = wv[D][n];
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
+      for (int b = 0; b < RB; ++b) {
+        bf16x8_t w;
+        if constexpr (ALONG) {
+          w = as_bf16x8(wv[D][b * 2 + h]);
+        } else {
+          typedef short s16x4 __attribute__((ext_vector_type(4)));
+          typedef short s16x8 __attribute__((ext_vector_type(8)));
+          const char* p = mine + ((h * 32 + 8 * q + (l16 >> 2)) * lw + b * 16 + 4 * (l16 & 3)) * 2;
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 4 * lw * 2));
+          w = __builtin_bit_cast(bf16x8_t, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+        }
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
-          acc[b][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wv[b][h]), as_bf16x8(uv[i][h]), acc[b][i], 0, 0, 0);
+        for (int i = 0; i < MB; ++i) acc[b][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, as_bf16x8(uv[D][i][h]), acc[b][i], 0, 0, 0);
+      }
   };
-  const int whole = min(s1, K / 64);
+  using Zero = std::integral_constant<int, 0>;
+  using One = std::integral_constant<int, 1>;
   int at = s0 + wave;
-#pragma unroll 2
-  for (; at < whole; at += kDownWaves) step(at, true);
-  if (at < s1) step(at, false);
+  if (at < s1) load(Zero{}, at);
+  while (at < s1) {
+    const bool more = at + kDownWaves < s1;
+    if (more) load(One{}, at + kDownWaves);
+    __builtin_amdgcn_sched_barrier(0);           // the loads go out before this step's products, not among them
+    use(Zero{}, at);
+    __builtin_amdgcn_sched_barrier(0);
+    at += kDownWaves;
+    if (!more) break;
+    if (at + kDownWaves < s1) load(Zero{}, at + kDownWaves);
+    __builtin_amdgcn_sched_barrier(0);
+    use(One{}, at);
+    __builtin_amdgcn_sched_barrier(0);
+    at += kDownWaves;
+  }
   // the waves' sums, a block of 16 ranks at a time
+  float* s_part = reinterpret_cast<float*>(lds);
+  float* out = (ALONG ? d.h : d.dh) + ((size_t)z * d.p.tiles + t) * RT * d.r;
+  uint16_t* turned = ALONG ? d.ht : d.dht;
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
-    if (b) __syncthreads();
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < MB; ++i)
       *reinterpret_cast<f32x4_t*>(s_part + ((wave * RT + i * 16 + l16) * 16 + q * 4)) = acc[b][i];
@@ -174,39 +253,223 @@ __device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile,
     for (int e = threadIdx.x; e < RT * 16; e += kDownWaves * 64) {
       float v = 0.f;
 #pragma unroll
-      for (int w8 = 0; w8 < kDownWaves; ++w8) v += s_part[w8 * RT * 16 + e];
-      const int row = e >> 4, j = b * 16 + (e & 15);
-      const bool live = tile.y + row < tile.z && row_at(d, tile.y + row) >= 0;
-      if (j < d.r) out[(size_t)row * d.r + j] = live ? v : 0.f;
+      for (int w = 0; w < kDownWaves; ++w) v += s_part[w * RT * 16 + e];
+      const int row = e >> 4, j = j0 + b * 16 + (e & 15);
+      if (tile.y + row >= tile.z || row_at(d, tile.y + row) < 0) v = 0.f;
+      if (j >= d.r) continue;
+      out[(size_t)row * d.r + j] = v;
+      if (turned) {                              // for the adapters' gradients: three bf16 numbers, rows along
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+          const uint32_t part = pack_bf16(v, 0.f) & 0xFFFFu;
+          turned[(((size_t)t * 3 + n) * d.r + j) * RT + row] = (uint16_t)part;
+          v = fabsf(bf2f(part)) == __builtin_huge_valf() ? 0.f : v - bf2f(part);
+        }
+      }
     }
   }
 }
 
 template <int RT, int RB>
-__global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down(const AdapterDesc d, int with_h, int with_dh) {
-  __shared__ __attribute__((aligned(16))) float s_part[kDownWaves * RT * 16];
+__global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down(const AdapterDesc d, int with_h, int chunks) {
+  __shared__ __attribute__((aligned(16))) char lds[DownLds<RT, RB>::BYTES];
   const int t = blockIdx.x, z = blockIdx.y;
   const int4 tile = adapter_tile<RT>(d, t);
-  const bool back = blockIdx.z != 0 || !with_h;
+  const bool back = (int)blockIdx.z >= chunks || !with_h;
+  const int j0 = (blockIdx.z % chunks) * kDownRanks;
   if (z == 0 && blockIdx.z == 0 && threadIdx.x == 0) d.tab[t] = tile;
   if (tile.x < 0) return;
-  const size_t at = ((size_t)z * d.p.tiles + t) * RT * d.r;
-  if (!back) down_tile<RT, RB, true>(d, tile, z, d.x, d.a, d.k, d.h + at, s_part);
-  else down_tile<RT, RB, false>(d, tile, z, d.dy, d.b, d.n, d.dh + at, s_part);
+  if (!back) down_tile<RT, RB, true>(d, tile, t, z, j0, lds);
+  else down_tile<RT, RB, false>(d, tile, t, z, j0, lds);
 }
 
-template <int RT>
-static hipError_t down(const AdapterDesc& d, hipStream_t s) {
-  const int with_h = d.h != nullptr, with_dh = d.dh != nullptr;
-  const dim3 grid(d.p.tiles, d.p.ks, with_h + with_dh), block(kDownWaves * 64);
-  if (d.r <= 16) ffn_launch((k_adapter_down<RT, 1>), grid, block, 0, s, d, with_h, with_dh);
-  else if (d.r <= 32) ffn_launch((k_adapter_down<RT, 2>), grid, block, 0, s, d, with_h, with_dh);
-  else if (d.r <= 64) ffn_launch((k_adapter_down<RT, 4>), grid, block, 0, s, d, with_h, with_dh);
-  else if (d.r <= 128) ffn_launch((k_adapter_down<RT, 8>), grid, block, 0, s, d, with_h, with_dh);
-  else ffn_launch((k_adapter_down<RT, 16>), grid, block, 0, s, d, with_h, with_dh);
+// The same for tiles of 64 rows: both operands' steps go straight from memory to LDS, whole lines of 128 bytes by
+// neighbouring lanes, STAGES - 1 steps ahead of the products (a lane of the version above takes 16 bytes of a row of its
+// own, and the weights come in anew for every 16 or 32 rows: 8192 x 4096, 64 ranks, 55 us). Wave (i, h) has rows 16 i ..
+// and half h of each step, for all ranks. Tiles start at different steps, or all of them would read the same few
+// channels of memory at a time. Rows of 128 bytes in LDS, chunk c at c ^ (row & 7): no bank conflicts.
+constexpr int kStepBytes = 128;
+__device__ const uint4 adapter_zero = {0, 0, 0, 0};              // what lies behind the contraction's end
+__device__ __forceinline__ void to_lds16(const void* p, const char* l) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)l;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(p) : "m0");
+}
+// At most N loads to LDS are under way in this wave and its LDS reads are done, then every wave's.
+template <int N>
+__device__ __forceinline__ void lds_sync() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+template <int RB>
+struct Down64 {
+  static constexpr int X = 64 * kStepBytes, W = 16 * RB * kStepBytes, STAGE = X + W;
+  static constexpr int STAGES = RB == 8 ? 4 : 6;
+  static constexpr int WL = (W / 1024 + kDownWaves - 1) / kDownWaves;          // loads of the weights, of the waves that have any
+  static constexpr int BYTES = STAGES * STAGE;
+  static_assert(BYTES >= 4 * RB * 64 * 16, "the second halves' sums");
+};
+template <int RB, bool ALONG>
+__device__ __forceinline__ void down64_tile(const AdapterDesc& d, const int4 tile, int t, int z, int j0, char* lds) {
+  using L = Down64<RB>;
+  constexpr int RT = 64, S = L::STAGES;
+  const int lane = lane_id(), l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wi = wave & 3, wh = wave >> 2;
+  const uint16_t* u = ALONG ? d.x : d.dy;
+  const int K = ALONG ? d.k : d.n;
+  const int rw = min(d.r - j0, 16 * RB);         // ranks here
+  const int lw = d.r <= kDownRanks ? d.r : kDownRanks;           // row of B in LDS
+  const int steps = (K + 63) / 64, s0 = (int)((long long)steps * z / d.p.ks), n = (int)((long long)steps * (z + 1) / d.p.ks) - s0;
+  // where this lane's loads come from: rows wave * 8 .. of the tile, chunk (lane % 8) ^ row of each
+  const int xr = wave * 8 + (lane >> 3), xc = (lane & 7) ^ (xr & 7);
+  const uint16_t* xp = u + (size_t)max(row_at(d, min(tile.y + xr, tile.z - 1)), 0) * K + xc * 8;
+  const uint16_t* wp[L::WL];
+  int wk[L::WL];                                 // contraction element of a step that the chunk starts at
+#pragma unroll
+  for (int i = 0; i < L::WL; ++i) {
+    const int c = (i * kDownWaves + wave) * 64 + lane;
+    if constexpr (ALONG) {
+      const int row = c >> 3;
+      wk[i] = ((c & 7) ^ (row & 7)) * 8;
+      wp[i] = d.a + ((size_t)tile.x * d.r + j0 + min(row, rw - 1)) * K + wk[i];
+    } else {
+      const int row = d.r <= kDownRanks ? c * 8 / lw : c >> 4, col = d.r <= kDownRanks ? c * 8 - row * lw : (c & 15) * 8;
+      wk[i] = min(row, 63);                      // chunks past the 64 rows: not read
+      wp[i] = d.b + ((size_t)tile.x * K + wk[i]) * d.r + j0 + min(col, rw - 8);
+    }
+  }
+  const bool has_w = L::W / 1024 >= kDownWaves || wave < L::W / 1024;
+  const size_t wstep = ALONG ? 64 : (size_t)64 * d.r;
+  const int turn = n > 0 ? (int)((unsigned)(t * 5) % (unsigned)n) : 0;
+  auto load = [&](int s) {
+    int at = s + turn;
+    at = s0 + (at >= n ? at - n : at);
+    char* stage = lds + s % S * L::STAGE;
+    const bool part = at * 64 + 64 > K;
+    const void* p = xp + (size_t)at * 64;
+    if (part && at * 64 + xc * 8 >= K) p = &adapter_zero;
+    to_lds16(p, stage + wave * 1024);
+    if (has_w) {
+#pragma unroll
+      for (int i = 0; i < L::WL; ++i) {
+        p = wp[i] + (size_t)at * wstep;
+        if (part && at * 64 + wk[i] >= K) p = &adapter_zero;
+        to_lds16(p, stage + L::X + (i * kDownWaves + wave) * 1024);
+      }
+    }
+  };
+  f32x4_t acc[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) acc[b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < S - 1 && s < n; ++s) load(s);
+  for (int s = 0; s < n; ++s) {
+    // step s is there; the S - 2 behind it may still be under way
+    if (s + S - 1 > n) lds_sync<0>();
+    else if (has_w) lds_sync<(S - 2) * (1 + L::WL)>();
+    else lds_sync<S - 2>();
+    if (s + S - 1 < n) load(s + S - 1);
+    const char* stage = lds + s % S * L::STAGE;
+    const int chunk = ((wh * 4 + q) ^ (l16 & 7)) << 4;
+    const bf16x8_t xv = as_bf16x8(*reinterpret_cast<const uint4*>(stage + (wi * 16 + l16) * kStepBytes + chunk));
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      bf16x8_t w;
+      if constexpr (ALONG) {
+        w = as_bf16x8(*reinterpret_cast<const uint4*>(stage + L::X + (b * 16 + l16) * kStepBytes + chunk));
+      } else {
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const char* p = stage + L::X + ((wh * 32 + 8 * q + (l16 >> 2)) * lw + min(b * 16 + 4 * (l16 & 3), lw - 4)) * 2;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 4 * lw * 2));
+        w = __builtin_bit_cast(bf16x8_t, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+      }
+      acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xv, acc[b], 0, 0, 0);
+    }
+  }
+  lds_sync<0>();
+  // the two halves' sums: lane l has ranks 16 b + 4 q .. of row 16 i + l16
+  f32x4_t* s_half = reinterpret_cast<f32x4_t*>(lds) + wi * RB * 64 + lane;
+  if (wh) {
+#pragma unroll
+    for (int b = 0; b < RB; ++b) s_half[b * 64] = acc[b];
+  }
+  __syncthreads();
+  if (wh) return;
+  const int row = wi * 16 + l16;
+  const bool live = tile.y + row < tile.z && row_at(d, min(tile.y + row, tile.z - 1)) >= 0;
+  float* out = (ALONG ? d.h : d.dh) + (((size_t)z * d.p.tiles + t) * RT + row) * d.r;
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    const int j = j0 + b * 16 + q * 4;
+    f32x4_t v = acc[b] + s_half[b * 64];
+    if (!live) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (j < d.r) *reinterpret_cast<f32x4_t*>(out + j) = v;
+  }
+}
+
+template <int RB>
+__global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down64(const AdapterDesc d, int with_h, int chunks) {
+  __shared__ __attribute__((aligned(16))) char lds[Down64<RB>::BYTES];
+  const int t = blockIdx.x, z = blockIdx.y;
+  const int4 tile = adapter_tile<64>(d, t);
+  const bool back = (int)blockIdx.z >= chunks || !with_h;
+  const int j0 = (blockIdx.z % chunks) * kDownRanks;
+  if (z == 0 && blockIdx.z == 0 && threadIdx.x == 0) d.tab[t] = tile;
+  if (tile.x < 0) return;
+  if (!back) down64_tile<RB, true>(d, tile, t, z, j0, lds);
+  else down64_tile<RB, false>(d, tile, t, z, j0, lds);
+}
+
+// The slices' sums, in the first slice's place, and the three bf16 numbers of each for the adapters' gradients: a
+// workgroup takes four rows (neighbours in `turned`) of 64 ranks.
+__global__ __launch_bounds__(256) void k_adapter_sum(const AdapterDesc d, int with_h) {
+  const int t = blockIdx.x, which = !with_h || blockIdx.z, RT = d.p.rt;
+  if (d.tab[t].x < 0) return;
+  float* h = (which ? d.dh : d.h) + (size_t)t * RT * d.r;
+  uint16_t* turned = which ? d.dht : d.ht;
+  const size_t slab = (size_t)d.p.tiles * RT * d.r;
+  for (int e = blockIdx.y * 256 + threadIdx.x; e < RT / 4 * d.r; e += gridDim.y * 256) {
+    const int j = e % d.r, r0 = e / d.r * 4;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = 0.f;
+      for (int z = 0; z < d.p.ks; ++z) v[i] += h[z * slab + (size_t)(r0 + i) * d.r + j];
+      h[(size_t)(r0 + i) * d.r + j] = v[i];
+    }
+    if (!turned) continue;
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      const uint32_t a = pack_bf16(v[0], v[1]), b = pack_bf16(v[2], v[3]);
+      *reinterpret_cast<uint2*>(turned + (((size_t)t * 3 + n) * d.r + j) * RT + r0) = uint2{a, b};
+      const float g[4] = {bf2f(a & 0xFFFFu), bf2f(a >> 16), bf2f(b & 0xFFFFu), bf2f(b >> 16)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fabsf(g[i]) == __builtin_huge_valf() ? 0.f : v[i] - g[i];
+    }
+  }
+}
+
+hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s) {
+  const int with_h = d.h != nullptr, with_dh = d.dh != nullptr, chunks = (d.r + kDownRanks - 1) / kDownRanks;
+  const dim3 grid(d.p.tiles, d.p.ks, (with_h + with_dh) * chunks), block(kDownWaves * 64);
+  if (d.p.rt == 16) {
+    if (d.r <= 16) ffn_launch((k_adapter_down<16, 1>), grid, block, 0, s, d, with_h, chunks);
+    else if (d.r <= 32) ffn_launch((k_adapter_down<16, 2>), grid, block, 0, s, d, with_h, chunks);
+    else if (d.r <= 64) ffn_launch((k_adapter_down<16, 4>), grid, block, 0, s, d, with_h, chunks);
+    else ffn_launch((k_adapter_down<16, 8>), grid, block, 0, s, d, with_h, chunks);
+    return hipGetLastError();
+  }
+  if (d.r <= 16) ffn_launch((k_adapter_down64<1>), grid, block, 0, s, d, with_h, chunks);
+  else if (d.r <= 32) ffn_launch((k_adapter_down64<2>), grid, block, 0, s, d, with_h, chunks);
+  else if (d.r <= 64) ffn_launch((k_adapter_down64<4>), grid, block, 0, s, d, with_h, chunks);
+  else ffn_launch((k_adapter_down64<8>), grid, block, 0, s, d, with_h, chunks);
+  const hipError_t e = hipGetLastError();
+  // backward: both consumers read the sums; forward, the second product adds the slices as it reads them
+  if (e != hipSuccess || !d.back) return e;
+  ffn_launch(k_adapter_sum, dim3(d.p.tiles, (d.r * 16 + 255) / 256, with_h + with_dh), dim3(256), 0, s, d, with_h);
   return hipGetLastError();
 }
-hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s) { return d.p.rt == 16 ? down<16>(d, s) : down<32>(d, s); }
 
 // ---------------------------------------------------------------- second product
 // 8 x 8 values of bf16, row e in in[e], as their columns.
@@ -226,28 +489,21 @@ __device__ __forceinline__ void transpose8(const uint4 (&in)[8], uint4 (&out)[8]
                    __builtin_amdgcn_perm(r[5][c >> 1], r[4][c >> 1], sel), __builtin_amdgcn_perm(r[7][c >> 1], r[6][c >> 1], sel)};
   }
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return uint4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
-}
-// f - bf16(f); nothing behind an infinity
-__device__ __forceinline__ void remainder8(float (&f)[8], const uint4 hi) {
-  float g[8];
-  unpack8(hi, g);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = fabsf(g[e]) == __builtin_huge_valf() ? 0.f : f[e] - g[e];
-}
 
-// out = base + s h W^T for a tile: wave w has 128 columns, column 8 (q + 4 v) + i of them in value v of accumulator i, so
-// that a lane reads and writes eight neighbours. F: groups of 32 ranks (0: up to 16, hi and lo in one group).
+// out = base + s h W^T for a tile: a wave has 128 columns, accumulator e of lane l column 8 (l % 16) + e of row 4 (l / 16) + v
+// in its value v, so that a lane reads and writes eight neighbours and 16 lanes 256 bytes of a row. (With the lanes' rows
+// and columns exchanged, 16 bytes a row from each of 16 lanes, 8192 x 4096 x 14336 took 160 us.) F: groups of 32 ranks (0: up to 16, hi and lo in one group).
 // ALONG: W = B, rows of r elements a column; otherwise W = A^T, rows of the output's columns.
 template <typename T, int RT, int F, bool ALONG>
 __global__ __launch_bounds__(256) void k_adapter_up(const AdapterDesc d) {
   constexpr int NF = F == 0 ? 1 : F;
   const int lane = lane_id(), wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
   const int cols = ALONG ? d.n : d.k;
-  const int c0 = (blockIdx.y * 4 + wave) * 128;
+  const int c0 = (blockIdx.x * 4 + wave) * 128;
   if (c0 >= cols) return;
-  const int4 tile = d.tab[blockIdx.x];
+  const int t = blockIdx.y + blockIdx.z * gridDim.y;
+  if (t >= d.p.tiles) return;
+  const int4 tile = d.tab[t];
   if (tile.x == -2) return;
   if (tile.x == -1) {                            // no adapter: the base alone
     if (d.base == d.out) return;
@@ -263,93 +519,131 @@ __global__ __launch_bounds__(256) void k_adapter_up(const AdapterDesc d) {
     }
     return;
   }
-  const float* hsrc = (ALONG ? d.h : d.dh) + (size_t)blockIdx.x * RT * d.r;
+  const float* hsrc = (ALONG ? d.h : d.dh) + (size_t)t * RT * d.r;
   const size_t slab = (size_t)d.p.tiles * RT * d.r;
+  const int slabs = d.back ? 1 : d.p.ks;         // backward, they have been added already
   const float scale = d.scales ? d.scales[tile.x] : 1.f;
   const uint16_t* w = ALONG ? d.b + (size_t)tile.x * d.n * d.r : d.a + (size_t)tile.x * d.r * d.k;
   const int jq = F == 0 ? (q & 1) * 8 : q * 8;   // this lane's first rank in a group
-  const int cb = c0 + 8 * ((l16 >> 2) + 4 * (l16 & 3));
+  const int wc = c0 + 8 * l16;                   // this lane's eight columns
+  // the weights of up to 64 ranks stay in registers for all of the tile's rows
+  constexpr bool STAY = NF <= 2;
+  uint4 wv[STAY ? NF : 1][8];
+  auto weights = [&](int g) {
+    uint4(&o)[8] = wv[STAY ? g : 0];
+    const int j = g * 32 + jq, jc = min(j, d.r - 8);
+    if constexpr (ALONG) {
 #pragma unroll
-  for (int i = 0; i < RT / 16; ++i) {
-    const int place = tile.y + i * 16 + l16;
-    if (tile.y + i * 16 >= tile.z) break;
-    const int row = place < tile.z ? row_at(d, place) : -1;
-    f32x4_t acc[8];
+      for (int e = 0; e < 8; ++e) o[e] = ldg16(w + (size_t)min(wc + e, cols - 1) * d.r + jc);
+    } else {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int c = c0 + 8 * (q + 4 * v);
-      Row8<T> b;
-      float f[8];
-      b.zero();
-      if (d.base && row >= 0 && c < cols) b.load(d.base, (size_t)row * cols + c);
-      b.get(f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e][v] = f[e];
+      for (int e = 0; e < 8; ++e) o[e] = ldg16(w + (size_t)(jc + e) * cols + min(wc, cols - 8));
     }
 #pragma unroll
-    for (int g = 0; g < NF; ++g) {
-      const int j = g * 32 + jq;
-      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (j < d.r) {
-        for (int z = 0; z < d.p.ks; ++z) {
-          const f32x4_t* p = reinterpret_cast<const f32x4_t*>(hsrc + z * slab + (size_t)(i * 16 + l16) * d.r + j);
-          const f32x4_t a = p[0], b = p[1];
+    for (int e = 0; e < 8; ++e) o[e] = keep_if(j < d.r, o[e]);
+    if constexpr (!ALONG) {
+      uint4 in[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[e] += a[e];
-            f[4 + e] += b[e];
-          }
+      for (int e = 0; e < 8; ++e) in[e] = o[e];
+      transpose8(in, o);
+    }
+  };
+  if constexpr (STAY) {
+#pragma unroll
+    for (int g = 0; g < NF; ++g) weights(g);
+  }
+  // lane l has the row of place l of the tile
+  const int mine = row_at(d, min(tile.y + min(lane, RT - 1), tile.z - 1)), rows = tile.z - tile.y;
+  auto run = [&](auto with_base) {
+    constexpr bool BASE = decltype(with_base)::value;
+    int row[4];
+    Row8<T> base[4];
+    auto fetch = [&](int i0) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        row[v] = __shfl(mine, min(i0 + 4 * q + v, rows - 1), 64);
+        base[v].zero();
+        if constexpr (BASE) base[v].load(d.base, (size_t)max(row[v], 0) * cols + min(wc, cols - 8));
+      }
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < rows; i0 += 16) {
+      f32x4_t ha[NF][2];
+      const float* hp = hsrc + (size_t)(i0 + l16) * d.r;
+#pragma unroll
+      for (int g = 0; g < NF; ++g) {
+        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(hp + min(g * 32 + jq, d.r - 8));
+        ha[g][0] = p[0];
+        ha[g][1] = p[1];
+      }
+      for (int z = 1; z < slabs; ++z) {
+#pragma unroll
+        for (int g = 0; g < NF; ++g) {
+          const f32x4_t* p = reinterpret_cast<const f32x4_t*>(hp + z * slab + min(g * 32 + jq, d.r - 8));
+          ha[g][0] += p[0];
+          ha[g][1] += p[1];
         }
       }
+      f32x4_t acc[8];                            // the sums start from the base
+      int to[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] *= scale;
-      uint4 hi = pack8(f);
-      remainder8(f, hi);
-      const uint4 lo = pack8(f);
-      uint4 rest = {0, 0, 0, 0};
-      if constexpr (sizeof(T) == 4) {
-        remainder8(f, lo);
-        if (F != 0 || q < 2) rest = pack8(f);
+      for (int v = 0; v < 4; ++v) {
+        float f[8];
+        base[v].get(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e][v] = f[e];
+        to[v] = i0 + 4 * q + v < rows ? row[v] : -1;
       }
-      if constexpr (F == 0) hi = q < 2 ? hi : lo;
-      uint4 wv[8];
-      if constexpr (ALONG) {
+      if (RT > 16) fetch(i0 + 16);               // the next rows' base (past the last: the last row again)
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wv[e] = ldg16_if(j < d.r, w + (size_t)min(cb + e, cols - 1) * d.r + j);
-      } else {
-        uint4 in[8];
+      for (int g = 0; g < NF; ++g) {
+        if constexpr (!STAY) weights(g);
+        const uint4(&o)[8] = wv[STAY ? g : 0];
+        const bool in = g * 32 + jq < d.r;
+        float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) in[e] = ldg16_if(j < d.r && cb < cols, w + (size_t)(j + e) * cols + cb);
-        transpose8(in, wv);
+        for (int e = 0; e < 8; ++e) f[e] = in ? ha[g][e >> 2][e & 3] * scale : 0.f;
+        const uint4 hi = pack8(f);
+        remainder8(f, hi);
+        const uint4 lo = pack8(f);
+        uint4 one = hi;
+        if constexpr (F == 0) one = q < 2 ? hi : lo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(one), as_bf16x8(o[e]), acc[e], 0, 0, 0);
+        if constexpr (F != 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(lo), as_bf16x8(o[e]), acc[e], 0, 0, 0);
+        }
+        if constexpr (sizeof(T) == 4) {
+          remainder8(f, lo);
+          const uint4 rest = keep_if(F != 0 || q < 2, pack8(f));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(rest), as_bf16x8(o[e]), acc[e], 0, 0, 0);
+        }
       }
+      if (wc >= cols) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wv[e]), as_bf16x8(hi), acc[e], 0, 0, 0);
-      if constexpr (F != 0) {
+      for (int v = 0; v < 4; ++v) {
+        if (to[v] < 0) continue;
+        float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wv[e]), as_bf16x8(lo), acc[e], 0, 0, 0);
-      }
-      if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(wv[e]), as_bf16x8(rest), acc[e], 0, 0, 0);
+        for (int e = 0; e < 8; ++e) f[e] = acc[e][v];
+        Row8<T>::store(d.out, (size_t)to[v] * cols + wc, f);
       }
     }
-    if (row < 0) continue;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int c = c0 + 8 * (q + 4 * v);
-      if (c >= cols) continue;
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = acc[e][v];
-      Row8<T>::store(d.out, (size_t)row * cols + c, f);
-    }
-  }
+  };
+  if (d.base) run(std::true_type{});
+  else run(std::false_type{});
 }
 
 template <typename T, int RT, bool ALONG>
 static hipError_t up(const AdapterDesc& d, hipStream_t s) {
   const int cols = ALONG ? d.n : d.k;
-  const dim3 grid(d.p.tiles, (cols + 511) / 512), block(256);
+  // a grid's second dimension holds 65535 workgroups: tiles go on in the third
+  const int ty = d.p.tiles < 32768 ? d.p.tiles : 32768;
+  const dim3 grid((cols + 511) / 512, ty, (d.p.tiles + ty - 1) / ty), block(256);
   if (d.r <= 16) ffn_launch((k_adapter_up<T, RT, 0, ALONG>), grid, block, 0, s, d);
   else if (d.r <= 32) ffn_launch((k_adapter_up<T, RT, 1, ALONG>), grid, block, 0, s, d);
   else if (d.r <= 64) ffn_launch((k_adapter_up<T, RT, 2, ALONG>), grid, block, 0, s, d);
@@ -358,17 +652,16 @@ static hipError_t up(const AdapterDesc& d, hipStream_t s) {
   return hipGetLastError();
 }
 hipError_t launch_adapter_up(const AdapterDesc& d, bool back, hipStream_t s) {
-  if (back) return d.p.rt == 16 ? up<uint16_t, 16, false>(d, s) : up<uint16_t, 32, false>(d, s);
-  if (d.out_f32) return d.p.rt == 16 ? up<float, 16, true>(d, s) : up<float, 32, true>(d, s);
-  return d.p.rt == 16 ? up<uint16_t, 16, true>(d, s) : up<uint16_t, 32, true>(d, s);
+  if (back) return d.p.rt == 16 ? up<uint16_t, 16, false>(d, s) : up<uint16_t, 64, false>(d, s);
+  if (d.out_f32) return d.p.rt == 16 ? up<float, 16, true>(d, s) : up<float, 64, true>(d, s);
+  return d.p.rt == 16 ? up<uint16_t, 16, true>(d, s) : up<uint16_t, 64, true>(d, s);
 }
 
 // ---------------------------------------------------------------- gradients of the adapters
 // dA[j][c] = s sum over the adapter's rows t of dh[t][j] x[t][c], and dB[c][j] = s sum of h[t][j] dy[t][c]: a workgroup
 // has 128 columns c of one adapter and up to 16 RB ranks; its waves take 32 rows in turn, whose 8 x 8 pieces are turned
-// in registers, and their sums are added in order. h enters as three bf16 numbers.
-constexpr int kDwWaves = 8;
-template <int RT, int RB, bool OF_A>
+// in registers, the next ones under way, and their sums are added in order. h enters as three bf16 numbers.
+template <int RT, int RB, int WAVES, bool OF_A>
 __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int c0, int j0, float* s_part) {
   const int lane = lane_id(), wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
   const int cols = OF_A ? d.k : d.n;
@@ -386,106 +679,141 @@ __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int c0, int
   });
   const int owner = g / s.per;
   const int before = wave_read(wave_incl_scan(mine) - mine, owner) + wave_read(tiles, owner);
-  const int lo = wave_read(start, owner), hi = wave_read(stop, owner);
-  const float* h = (OF_A ? d.dh : d.h) + (size_t)before * RT * d.r;
+  const int lo = wave_read(start, owner), rows = wave_read(stop, owner) - lo;
+  const uint16_t* h = (OF_A ? d.dht : d.ht) + (size_t)before * 3 * d.r * RT;
   f32x4_t acc[8][RB];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int b = 0; b < RB; ++b) acc[i][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int cb = c0 + 8 * ((l16 >> 2) + 4 * (l16 & 3));
-  for (int r0 = wave * 32; r0 < hi - lo; r0 += kDwWaves * 32) {
-    uint4 in[8], uv[8];
-    int live = 0;
+  const int cb = min(c0 + 8 * l16, cols - 8);
+  int at[8];
+  uint4 in[8];
+  // the rows of step r0 (clamped: what lies behind the last is cleared before it is used)
+  auto find = [&](int r0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int t = r0 + q * 8 + e;
-      const int row = t < hi - lo ? row_at(d, lo + t) : -1;
-      if (row >= 0) live |= 1 << e;
-      in[e] = ldg16_if(row >= 0 && cb < cols, u + (size_t)max(row, 0) * cols + cb);
-    }
-    transpose8(in, uv);
+    for (int e = 0; e < 8; ++e) at[e] = row_at(d, lo + min(r0 + q * 8 + e, rows - 1));
+  };
+  auto load = [&] {
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      const int j = j0 + b * 16 + l16;
-      float f[8];
+    for (int e = 0; e < 8; ++e) in[e] = ldg16(u + (size_t)max(at[e], 0) * cols + cb);
+  };
+  int r0 = wave * 32;
+  if (r0 < rows) {
+    find(r0);
+    load();
+    for (; r0 < rows; r0 += WAVES * 32) {
+      // places and rows past the adapter's: zeros
+      uint4 uv[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = j < d.r && (live >> e & 1) ? h[(size_t)(r0 + q * 8 + e) * d.r + j] : 0.f;
+      for (int e = 0; e < 8; ++e) in[e] = keep_if(at[e] >= 0 && r0 + q * 8 + e < rows, in[e]);
+      transpose8(in, uv);
+      const int next = min(r0 + WAVES * 32, rows - 1);
+      find(next);
+      load();
+      __builtin_amdgcn_sched_barrier(0);
+      const int first = r0 + q * 8, tile = min(first, rows - 1) / RT;
+      const uint16_t* hp = h + ((size_t)tile * 3 * d.r) * RT + (first & (RT - 1));
+      const bool has = first < rows;             // a tile of 16 rows may be the last
 #pragma unroll
-      for (int part = 0; part < 3; ++part) {
-        const uint4 hv = pack8(f);
-        remainder8(f, hv);
+      for (int b = 0; b < RB; ++b) {
+        const int j = min(j0 + b * 16 + l16, d.r - 1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if constexpr (OF_A) acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(uv[i]), as_bf16x8(hv), acc[i][b], 0, 0, 0);
-          else acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(hv), as_bf16x8(uv[i]), acc[i][b], 0, 0, 0);
+        for (int part = 0; part < 3; ++part) {
+          const uint4 hv = keep_if(has, ldg16(hp + ((size_t)part * d.r + j) * RT));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if constexpr (OF_A) acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(uv[i]), as_bf16x8(hv), acc[i][b], 0, 0, 0);
+            else acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(hv), as_bf16x8(uv[i]), acc[i][b], 0, 0, 0);
+          }
         }
       }
     }
   }
-  // the waves' sums, 16 ranks of the 128 columns at a time: s_part[wave][value][lane] in fours
+  // the waves' sums, 16 ranks of the 128 columns at a time: s_part[wave][accumulator][lane] in fours
   const float scale = d.scales ? d.scales[g] : 1.f;
+  auto part = [&](int w, int i, int l) { return s_part + ((w * 8 + i) * 64 + l) * 4; };
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     if (b) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<f32x4_t*>(s_part + ((wave * 8 + i) * 64 + lane) * 4) = acc[i][b];
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<f32x4_t*>(part(wave, i, lane)) = acc[i][b];
     __syncthreads();
-    // thread (wave, lane) finishes accumulator `wave` of lane `lane`
-    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (OF_A) {
+      // eight neighbouring columns of a rank a thread: those of blk = 4 q + v are value v of lane q * 16 + j's accumulators
+      for (int n = threadIdx.x; n < 256; n += WAVES * 64) {
+        const int blk = n & 15, j = j0 + b * 16 + (n >> 4), l = (blk >> 2) * 16 + (n >> 4), c = c0 + 8 * blk;
+        float f[8];
 #pragma unroll
-    for (int w = 0; w < kDwWaves; ++w) v += *reinterpret_cast<const f32x4_t*>(s_part + ((w * 8 + wave) * 64 + lane) * 4);
-    const int i = wave;
+        for (int i = 0; i < 8; ++i) {
+          f[i] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      int j, c;
-      if constexpr (OF_A) {
-        j = j0 + b * 16 + l16;
-        c = c0 + 8 * (q + 4 * e) + i;
-      } else {
-        j = j0 + b * 16 + 4 * q + e;
-        c = cb + i;
+          for (int w = 0; w < WAVES; ++w) f[i] += part(w, i, l)[blk & 3];
+        }
+        if (j >= d.r || c >= cols) continue;
+        float* out = d.da + ((size_t)g * d.r + j) * cols + c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = scale * f[i] + (d.accumulate ? out[i] : 0.f);
+        Row8<float>::store(out, 0, f);
       }
-      if (j >= d.r || c >= cols) continue;
-      float* out = OF_A ? d.da + ((size_t)g * d.r + j) * cols + c : d.db + ((size_t)g * cols + c) * d.r + j;
-      const float o = scale * v[e];
-      *out = d.accumulate ? *out + o : o;
+    } else {
+      // four neighbouring ranks of a column a thread: lane q * 16 + p of accumulator i has column 8 p + i
+      for (int n = threadIdx.x; n < 512; n += WAVES * 64) {
+        const int lq = n & 3, col = n >> 2, p = col >> 3;
+        const int j = j0 + b * 16 + 4 * lq, c = c0 + col;
+        f32x4_t f = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) f += *reinterpret_cast<const f32x4_t*>(part(w, col & 7, lq * 16 + p));
+        if (j >= d.r || c >= cols) continue;
+        f32x4_t* out = reinterpret_cast<f32x4_t*>(d.db + ((size_t)g * cols + c) * d.r + j);
+        f *= scale;
+        if (d.accumulate) f += *out;
+        *out = f;
+      }
     }
   }
 }
 
-template <int RT, int RB>
-__global__ __launch_bounds__(kDwWaves * 64) void k_adapter_dw(const AdapterDesc d, int cols_a) {
-  __shared__ __attribute__((aligned(16))) float s_part[kDwWaves * 8 * 64 * 4];
+template <int RT, int RB, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void k_adapter_dw(const AdapterDesc d, int cols_a) {
+  __shared__ __attribute__((aligned(16))) float s_part[WAVES * 8 * 64 * 4];
   const int j0 = blockIdx.z * (16 * RB);
-  if ((int)blockIdx.x < cols_a) dw_tile<RT, RB, true>(d, blockIdx.y, blockIdx.x * 128, j0, s_part);
-  else dw_tile<RT, RB, false>(d, blockIdx.y, (blockIdx.x - cols_a) * 128, j0, s_part);
+  if ((int)blockIdx.x < cols_a) dw_tile<RT, RB, WAVES, true>(d, blockIdx.y, blockIdx.x * 128, j0, s_part);
+  else dw_tile<RT, RB, WAVES, false>(d, blockIdx.y, (blockIdx.x - cols_a) * 128, j0, s_part);
 }
 
-template <int RT>
-static hipError_t dw(const AdapterDesc& d, hipStream_t s) {
+template <int RT, int RB>
+static hipError_t dw_ranks(const AdapterDesc& d, hipStream_t s) {
   const int ca = d.da ? (d.k + 127) / 128 : 0, cb = d.db ? (d.n + 127) / 128 : 0;
-  const dim3 block(kDwWaves * 64);
-  if (d.r <= 16) ffn_launch((k_adapter_dw<RT, 1>), dim3(ca + cb, d.groups, 1), block, 0, s, d, ca);
-  else if (d.r <= 32) ffn_launch((k_adapter_dw<RT, 2>), dim3(ca + cb, d.groups, 1), block, 0, s, d, ca);
-  else ffn_launch((k_adapter_dw<RT, 4>), dim3(ca + cb, d.groups, (d.r + 63) / 64), block, 0, s, d, ca);
+  const dim3 grid(ca + cb, d.groups, (d.r + 16 * RB - 1) / (16 * RB));
+  // eight waves where four would leave the chip half empty
+  if ((long long)grid.x * grid.y * grid.z >= 512) ffn_launch((k_adapter_dw<RT, RB, 4>), grid, dim3(256), 0, s, d, ca);
+  else ffn_launch((k_adapter_dw<RT, RB, 8>), grid, dim3(512), 0, s, d, ca);
   return hipGetLastError();
 }
-hipError_t launch_adapter_dw(const AdapterDesc& d, hipStream_t s) { return d.p.rt == 16 ? dw<16>(d, s) : dw<32>(d, s); }
+template <int RT>
+static hipError_t dw(const AdapterDesc& d, hipStream_t s) {
+  if (d.r <= 16) return dw_ranks<RT, 1>(d, s);
+  if (d.r <= 32) return dw_ranks<RT, 2>(d, s);
+  return dw_ranks<RT, 4>(d, s);
+}
+hipError_t launch_adapter_dw(const AdapterDesc& d, hipStream_t s) { return d.p.rt == 16 ? dw<16>(d, s) : dw<64>(d, s); }
 
 // ---------------------------------------------------------------- plan
 AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) {
   AdapterPlan p;
-  p.rt = m >= 1024 ? 32 : 16;
+  // tiles of 64 rows where adapters have that many to share their weights' reads, of 16 where rows are few
+  p.rt = m >= 512 && m / 16 >= groups ? 64 : 16;
   // every adapter's last tile may be short, and so may the two runs of rows without one
   const long long tiles = (long long)m / p.rt + groups + 2;
   p.tiles = (int)(tiles < m ? tiles : m);
-  // slices: enough workgroups for the chip, while a wave still has a whole step
+  // slices: enough workgroups for the chip
+  const int live = (m + p.rt - 1) / p.rt;
+  const int least = p.rt == 64 ? 8 : kDownWaves;  // steps of a slice
+  const int steps = (backward ? (n > k ? n : k) : k) / 64;
   int ks = 1;
-  if (!backward) {
-    const int live = (m + p.rt - 1) / p.rt;
-    while (ks < 8 && live * ks < 256 && k / (ks * 2) >= 64 * kDownWaves) ks *= 2;
-  }
+  if (p.rt == 64 || !backward)
+    while (ks < 8 && live * ks < 256 && steps / (ks * 2) >= least) ks *= 2;
   p.ks = ks;
   return p;
 }
