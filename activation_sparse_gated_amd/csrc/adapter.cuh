@@ -26,16 +26,16 @@ struct AdapterDesc {
   int out_f32;
   float *da, *db;
   int accumulate;
-  int back;                      // a backward pass
   AdapterPlan p;
   // workspace
   int4* tab;                     // [tiles]: adapter (-1: none, -2: no tile), first place, end
   float *h, *dh;                 // [ks][tiles][rt][r]: x A^T and dy B
-  uint16_t *ht, *dht;            // null, or [tiles][3][r][rt]: the same in three bf16 numbers, rows along
+  uint16_t *hp, *dhp;            // tiles of 64 rows: [tiles][3][64][r], s h and s dh in bf16 numbers
+  uint16_t *ht, *dht;            // null, or [tiles][3][r][rt]: the same with the rows along
 };
 
 AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward);
-// first products: h (of x, if d.h) and dh (of dy, if d.dh), and the table of tiles
+// first products: h (of x, if d.h) and dh (of dy, if d.dh), what is made of them, and the table of tiles
 hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s);
 // second product: out = base + scale h B^T, or with `back` base + scale dh A
 hipError_t launch_adapter_up(const AdapterDesc& d, bool back, hipStream_t s);

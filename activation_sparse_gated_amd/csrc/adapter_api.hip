@@ -29,7 +29,12 @@ bool shape_ok(int32_t m, int32_t n, int32_t k, int32_t r, int32_t groups) {
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 size_t tab_bytes(const AdapterPlan& p) { return up256((size_t)p.tiles * 16); }
 size_t h_bytes(const AdapterPlan& p, int32_t r) { return up256((size_t)p.ks * p.tiles * p.rt * r * 4); }
-size_t turned_bytes(const AdapterPlan& p, int32_t r) { return up256((size_t)p.tiles * p.rt * r * 6); }
+size_t parts_bytes(const AdapterPlan& p, int32_t r) { return up256((size_t)p.tiles * p.rt * r * 6); }
+size_t rows_bytes(const AdapterPlan& p, int32_t r) { return p.rt == 64 ? parts_bytes(p, r) : 0; }
+size_t forward_bytes(const AdapterPlan& p, int32_t r) { return tab_bytes(p) + h_bytes(p, r) + rows_bytes(p, r); }
+size_t backward_bytes(const AdapterPlan& p, int32_t r) {
+  return tab_bytes(p) + 2 * (h_bytes(p, r) + parts_bytes(p, r)) + rows_bytes(p, r);
+}
 
 }  // namespace
 
@@ -40,7 +45,7 @@ int32_t ffn_adapter_abi_version(void) { return FFN_ADAPTER_ABI_VERSION; }
 size_t ffn_adapter_forward_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t r, int32_t groups) {
   if (!shape_ok(m, n, k, r, groups) || m == 0) return 0;
   const AdapterPlan p = adapter_plan(m, n, k, r, groups, false);
-  return tab_bytes(p) + h_bytes(p, r);
+  return forward_bytes(p, r);
 }
 
 ffn_status ffn_adapter_forward(const void* x, const void* a, const void* b, const float* scales, const int32_t* offsets,
@@ -54,7 +59,7 @@ ffn_status ffn_adapter_forward(const void* x, const void* a, const void* b, cons
     return FFN_E_INVALID;
   AdapterDesc d{};
   d.p = adapter_plan(m, n, k, r, groups, false);
-  if (workspace_bytes < tab_bytes(d.p) + h_bytes(d.p, r)) return FFN_E_WORKSPACE;
+  if (workspace_bytes < forward_bytes(d.p, r)) return FFN_E_WORKSPACE;
   d.x = static_cast<const uint16_t*>(x);
   d.a = static_cast<const uint16_t*>(a);
   d.b = static_cast<const uint16_t*>(b);
@@ -71,6 +76,7 @@ ffn_status ffn_adapter_forward(const void* x, const void* a, const void* b, cons
   d.out_f32 = y_dtype == FFN_F32;
   d.tab = static_cast<int4*>(workspace);
   d.h = reinterpret_cast<float*>(static_cast<char*>(workspace) + tab_bytes(d.p));
+  d.hp = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(d.h) + h_bytes(d.p, r));
   const hipError_t e = launch_adapter_down(d, st(stream));
   if (e != hipSuccess) return FFN_E_HIP;
   return done(launch_adapter_up(d, false, st(stream)));
@@ -79,7 +85,7 @@ ffn_status ffn_adapter_forward(const void* x, const void* a, const void* b, cons
 size_t ffn_adapter_backward_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t r, int32_t groups) {
   if (!shape_ok(m, n, k, r, groups) || m == 0) return 0;
   const AdapterPlan p = adapter_plan(m, n, k, r, groups, true);
-  return tab_bytes(p) + 2 * (h_bytes(p, r) + turned_bytes(p, r));
+  return backward_bytes(p, r);
 }
 
 ffn_status ffn_adapter_backward(const void* x, const void* a, const void* b, const float* scales, const void* dy,
@@ -101,7 +107,7 @@ ffn_status ffn_adapter_backward(const void* x, const void* a, const void* b, con
   if ((!with_dh && !with_h) || (base && !dx) || ((da || db) && !x) || ((dx || db) && !a) || (with_dh && !b)) return FFN_E_INVALID;
   AdapterDesc d{};
   d.p = adapter_plan(m, n, k, r, groups, true);
-  if (workspace_bytes < tab_bytes(d.p) + 2 * (h_bytes(d.p, r) + turned_bytes(d.p, r))) return FFN_E_WORKSPACE;
+  if (workspace_bytes < backward_bytes(d.p, r)) return FFN_E_WORKSPACE;
   d.x = static_cast<const uint16_t*>(x);
   d.dy = static_cast<const uint16_t*>(dy);
   d.a = static_cast<const uint16_t*>(a);
@@ -119,14 +125,14 @@ ffn_status ffn_adapter_backward(const void* x, const void* a, const void* b, con
   d.da = da;
   d.db = db;
   d.accumulate = accumulate;
-  d.back = 1;
   d.tab = static_cast<int4*>(workspace);
   char* at = static_cast<char*>(workspace) + tab_bytes(d.p);
   if (with_h) d.h = reinterpret_cast<float*>(at);
   if (with_dh) d.dh = reinterpret_cast<float*>(at + h_bytes(d.p, r));
   at += 2 * h_bytes(d.p, r);
   if (db) d.ht = reinterpret_cast<uint16_t*>(at);
-  if (da) d.dht = reinterpret_cast<uint16_t*>(at + turned_bytes(d.p, r));
+  if (da) d.dht = reinterpret_cast<uint16_t*>(at + parts_bytes(d.p, r));
+  if (dx) d.dhp = reinterpret_cast<uint16_t*>(at + 2 * parts_bytes(d.p, r));
   hipError_t e = launch_adapter_down(d, st(stream));
   if (e == hipSuccess && dx) e = launch_adapter_up(d, true, st(stream));
   if (e == hipSuccess && (da || db)) e = launch_adapter_dw(d, st(stream));

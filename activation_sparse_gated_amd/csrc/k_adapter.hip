@@ -65,20 +65,24 @@ __device__ __forceinline__ void each_group(const AdapterDesc& d, const Groups& s
     lo = hi;
   }
 }
-// Tile `tile`: {adapter, first place, end, 0}. Tiles of rows without an adapter (-1) stand behind the others'. adapter -2:
-// there is no such tile.
+// The tile of workgroup `block` of `blocks` (a multiple of 8, no fewer than there are tiles): {adapter, first place, end,
+// number}. Workgroups go to the 8 XCDs in turn; each XCD takes a run of neighbouring tiles, so that an adapter's weights
+// are read into few of their L2s. Tiles of rows without an adapter (-1) stand behind the others'. adapter -2: no rows.
 template <int RT>
-__device__ __forceinline__ int4 adapter_tile(const AdapterDesc& d, int tile) {
+__device__ __forceinline__ int4 adapter_tile(const AdapterDesc& d, int block, int blocks) {
   const Groups s = groups_of(d);
   int mine = 0, last = 0;
   each_group(d, s, [&](int, int lo, int hi) {
     mine += (hi - lo + RT - 1) / RT;
     last = hi;
   });
-  const int incl = wave_incl_scan(mine);
-  const uint64_t at = ballot64(incl > tile);
-  if (at) {
-    const int from = __ffsll((unsigned long long)at) - 1;
+  const int incl = wave_incl_scan(mine), total = wave_read(incl, 63);
+  const int per = (total + 7) >> 3, xcd = block & 7, at = block >> 3;
+  int tile = xcd * per + at;
+  if (at >= per) tile = total + (at - per) * 8 + xcd;            // the workgroups that no tile with an adapter is left for
+  else if (tile >= total) tile += blocks - 8 * per;
+  if (tile < total) {
+    const int from = __ffsll((unsigned long long)ballot64(incl > tile)) - 1;
     int4 t = {0, 0, 0, 0};
     int first = incl - mine;
     each_group(d, s, [&](int g, int lo, int hi) {
@@ -89,17 +93,15 @@ __device__ __forceinline__ int4 adapter_tile(const AdapterDesc& d, int tile) {
       }
       first += n;
     });
-    return int4{wave_read(t.x, from), wave_read(t.y, from), wave_read(t.z, from), 0};
+    return int4{wave_read(t.x, from), wave_read(t.y, from), wave_read(t.z, from), tile};
   }
   // rows of no adapter: before the first group, and behind the last
-  const int total = wave_read(incl, 63);
   const int end = wave_read(wave_incl_max(last), 63);
-  const int lead = wave_read(s.first, 0), n0 = (lead + RT - 1) / RT;
-  tile -= total;
-  if (tile < n0) return int4{-1, tile * RT, min(lead, (tile + 1) * RT), 0};
-  const int r0 = max(end, lead) + (tile - n0) * RT;
-  if (r0 < d.m) return int4{-1, r0, min(d.m, r0 + RT), 0};
-  return int4{-2, 0, 0, 0};
+  const int lead = wave_read(s.first, 0), n0 = (lead + RT - 1) / RT, n = tile - total;
+  if (n < n0) return int4{-1, n * RT, min(lead, (n + 1) * RT), tile};
+  const int r0 = max(end, lead) + (n - n0) * RT;
+  if (r0 < d.m) return int4{-1, r0, min(d.m, r0 + RT), tile};
+  return int4{-2, 0, 0, tile};
 }
 // The row at a place, -1 where there is none.
 __device__ __forceinline__ int row_at(const AdapterDesc& d, int place) {
@@ -108,6 +110,7 @@ __device__ __forceinline__ int row_at(const AdapterDesc& d, int place) {
 }
 // v, or zeros. (Loads are made unconditionally, from a place that is there: a branch around each would end their overlap.)
 __device__ __forceinline__ uint4 keep_if(bool in, const uint4 v) { return uint4{in ? v.x : 0u, in ? v.y : 0u, in ? v.z : 0u, in ? v.w : 0u}; }
+__device__ const uint4 adapter_zero[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return uint4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
 }
@@ -243,6 +246,7 @@ __device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile,
   float* s_part = reinterpret_cast<float*>(lds);
   float* out = (ALONG ? d.h : d.dh) + ((size_t)z * d.p.tiles + t) * RT * d.r;
   uint16_t* turned = ALONG ? d.ht : d.dht;
+  const float scale = d.scales ? d.scales[tile.x] : 1.f;
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     __syncthreads();
@@ -258,7 +262,8 @@ __device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile,
       if (tile.y + row >= tile.z || row_at(d, tile.y + row) < 0) v = 0.f;
       if (j >= d.r) continue;
       out[(size_t)row * d.r + j] = v;
-      if (turned) {                              // for the adapters' gradients: three bf16 numbers, rows along
+      if (turned) {                              // for the adapters' gradients: s h in three bf16 numbers, rows along
+        v *= scale;
 #pragma unroll
         for (int n = 0; n < 3; ++n) {
           const uint32_t part = pack_bf16(v, 0.f) & 0xFFFFu;
@@ -273,8 +278,10 @@ __device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile,
 template <int RT, int RB>
 __global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down(const AdapterDesc d, int with_h, int chunks) {
   __shared__ __attribute__((aligned(16))) char lds[DownLds<RT, RB>::BYTES];
-  const int t = blockIdx.x, z = blockIdx.y;
-  const int4 tile = adapter_tile<RT>(d, t);
+  const int z = blockIdx.y;
+  const int4 tile = adapter_tile<RT>(d, blockIdx.x, gridDim.x);
+  const int t = tile.w;
+  if (t >= d.p.tiles) return;
   const bool back = (int)blockIdx.z >= chunks || !with_h;
   const int j0 = (blockIdx.z % chunks) * kDownRanks;
   if (z == 0 && blockIdx.z == 0 && threadIdx.x == 0) d.tab[t] = tile;
@@ -283,13 +290,12 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down(const AdapterD
   else down_tile<RT, RB, false>(d, tile, t, z, j0, lds);
 }
 
-// The same for tiles of 64 rows: both operands' steps go straight from memory to LDS, whole lines of 128 bytes by
+// The same for tiles of 64 rows: both operands' steps go straight from memory to LDS, 256 bytes of a row by
 // neighbouring lanes, STAGES - 1 steps ahead of the products (a lane of the version above takes 16 bytes of a row of its
 // own, and the weights come in anew for every 16 or 32 rows: 8192 x 4096, 64 ranks, 55 us). Wave (i, h) has rows 16 i ..
 // and half h of each step, for all ranks. Tiles start at different steps, or all of them would read the same few
-// channels of memory at a time. Rows of 128 bytes in LDS, chunk c at c ^ (row & 7): no bank conflicts.
-constexpr int kStepBytes = 128;
-__device__ const uint4 adapter_zero = {0, 0, 0, 0};              // what lies behind the contraction's end
+// channels of memory at a time. Rows of 256 bytes in LDS, chunk c at c ^ (row & 15): no bank conflicts.
+constexpr int kStep = 128, kStepBytes = 2 * kStep; // elements and bytes of a row in a step
 __device__ __forceinline__ void to_lds16(const void* p, const char* l) {
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)l;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(p) : "m0");
@@ -304,10 +310,11 @@ __device__ __forceinline__ void lds_sync() {
 template <int RB>
 struct Down64 {
   static constexpr int X = 64 * kStepBytes, W = 16 * RB * kStepBytes, STAGE = X + W;
-  static constexpr int STAGES = RB == 8 ? 4 : 6;
+  static constexpr int STAGES = RB == 1 ? 4 : RB == 2 ? 3 : RB == 4 ? 2 : 3;    // two workgroups (one with 128 ranks) on a CU's 160 KB
+  static constexpr int XL = X / 1024 / kDownWaves;                             // loads of a step of each wave
   static constexpr int WL = (W / 1024 + kDownWaves - 1) / kDownWaves;          // loads of the weights, of the waves that have any
   static constexpr int BYTES = STAGES * STAGE;
-  static_assert(BYTES >= 4 * RB * 64 * 16, "the second halves' sums");
+  static_assert(BYTES >= 4 * RB * 64 * 16 && (RB == 8 ? 1 : 2) * BYTES <= 160 * 1024, "the second halves' sums, LDS of a CU");
 };
 template <int RB, bool ALONG>
 __device__ __forceinline__ void down64_tile(const AdapterDesc& d, const int4 tile, int t, int z, int j0, char* lds) {
@@ -319,41 +326,51 @@ __device__ __forceinline__ void down64_tile(const AdapterDesc& d, const int4 til
   const int K = ALONG ? d.k : d.n;
   const int rw = min(d.r - j0, 16 * RB);         // ranks here
   const int lw = d.r <= kDownRanks ? d.r : kDownRanks;           // row of B in LDS
-  const int steps = (K + 63) / 64, s0 = (int)((long long)steps * z / d.p.ks), n = (int)((long long)steps * (z + 1) / d.p.ks) - s0;
-  // where this lane's loads come from: rows wave * 8 .. of the tile, chunk (lane % 8) ^ row of each
-  const int xr = wave * 8 + (lane >> 3), xc = (lane & 7) ^ (xr & 7);
-  const uint16_t* xp = u + (size_t)max(row_at(d, min(tile.y + xr, tile.z - 1)), 0) * K + xc * 8;
+  const int steps = (K + kStep - 1) / kStep, s0 = (int)((long long)steps * z / d.p.ks), n = (int)((long long)steps * (z + 1) / d.p.ks) - s0;
+  // where this lane's loads come from: four rows of the tile for each, chunk (lane % 16) ^ row of them
+  const uint16_t* xp[L::XL];
+  int xk[L::XL];
+#pragma unroll
+  for (int i = 0; i < L::XL; ++i) {
+    const int row = (i * kDownWaves + wave) * 4 + (lane >> 4);
+    xk[i] = ((lane & 15) ^ (row & 15)) * 8;
+    xp[i] = u + (size_t)max(row_at(d, min(tile.y + row, tile.z - 1)), 0) * K + xk[i];
+  }
   const uint16_t* wp[L::WL];
   int wk[L::WL];                                 // contraction element of a step that the chunk starts at
 #pragma unroll
   for (int i = 0; i < L::WL; ++i) {
     const int c = (i * kDownWaves + wave) * 64 + lane;
     if constexpr (ALONG) {
-      const int row = c >> 3;
-      wk[i] = ((c & 7) ^ (row & 7)) * 8;
+      const int row = c >> 4;
+      wk[i] = ((c & 15) ^ (row & 15)) * 8;
       wp[i] = d.a + ((size_t)tile.x * d.r + j0 + min(row, rw - 1)) * K + wk[i];
     } else {
       const int row = d.r <= kDownRanks ? c * 8 / lw : c >> 4, col = d.r <= kDownRanks ? c * 8 - row * lw : (c & 15) * 8;
-      wk[i] = min(row, 63);                      // chunks past the 64 rows: not read
+      wk[i] = min(row, kStep - 1);               // chunks past the step's rows: not read
       wp[i] = d.b + ((size_t)tile.x * K + wk[i]) * d.r + j0 + min(col, rw - 8);
     }
   }
   const bool has_w = L::W / 1024 >= kDownWaves || wave < L::W / 1024;
-  const size_t wstep = ALONG ? 64 : (size_t)64 * d.r;
+  const size_t wstep = ALONG ? kStep : (size_t)kStep * d.r;
   const int turn = n > 0 ? (int)((unsigned)(t * 5) % (unsigned)n) : 0;
   auto load = [&](int s) {
     int at = s + turn;
     at = s0 + (at >= n ? at - n : at);
     char* stage = lds + s % S * L::STAGE;
-    const bool part = at * 64 + 64 > K;
-    const void* p = xp + (size_t)at * 64;
-    if (part && at * 64 + xc * 8 >= K) p = &adapter_zero;
-    to_lds16(p, stage + wave * 1024);
+    const bool part = (at + 1) * kStep > K;
+    const void* p;
+#pragma unroll
+    for (int i = 0; i < L::XL; ++i) {
+      p = xp[i] + (size_t)at * kStep;
+      if (part && at * kStep + xk[i] >= K) p = adapter_zero;
+      to_lds16(p, stage + (i * kDownWaves + wave) * 1024);
+    }
     if (has_w) {
 #pragma unroll
       for (int i = 0; i < L::WL; ++i) {
         p = wp[i] + (size_t)at * wstep;
-        if (part && at * 64 + wk[i] >= K) p = &adapter_zero;
+        if (part && at * kStep + wk[i] >= K) p = adapter_zero;
         to_lds16(p, stage + L::X + (i * kDownWaves + wave) * 1024);
       }
     }
@@ -365,26 +382,29 @@ __device__ __forceinline__ void down64_tile(const AdapterDesc& d, const int4 til
   for (int s = 0; s < n; ++s) {
     // step s is there; the S - 2 behind it may still be under way
     if (s + S - 1 > n) lds_sync<0>();
-    else if (has_w) lds_sync<(S - 2) * (1 + L::WL)>();
-    else lds_sync<S - 2>();
+    else if (has_w) lds_sync<(S - 2) * (L::XL + L::WL)>();
+    else lds_sync<(S - 2) * L::XL>();
     if (s + S - 1 < n) load(s + S - 1);
     const char* stage = lds + s % S * L::STAGE;
-    const int chunk = ((wh * 4 + q) ^ (l16 & 7)) << 4;
-    const bf16x8_t xv = as_bf16x8(*reinterpret_cast<const uint4*>(stage + (wi * 16 + l16) * kStepBytes + chunk));
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      bf16x8_t w;
-      if constexpr (ALONG) {
-        w = as_bf16x8(*reinterpret_cast<const uint4*>(stage + L::X + (b * 16 + l16) * kStepBytes + chunk));
-      } else {
-        typedef short s16x4 __attribute__((ext_vector_type(4)));
-        typedef short s16x8 __attribute__((ext_vector_type(8)));
-        const char* p = stage + L::X + ((wh * 32 + 8 * q + (l16 >> 2)) * lw + min(b * 16 + 4 * (l16 & 3), lw - 4)) * 2;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 4 * lw * 2));
-        w = __builtin_bit_cast(bf16x8_t, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    for (int k = 0; k < kStep / 64; ++k) {       // 32 elements of the wave's half
+      const int h = wh * (kStep / 64) + k, chunk = ((h * 4 + q) ^ l16) << 4;
+      const bf16x8_t xv = as_bf16x8(*reinterpret_cast<const uint4*>(stage + (wi * 16 + l16) * kStepBytes + chunk));
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        bf16x8_t w;
+        if constexpr (ALONG) {
+          w = as_bf16x8(*reinterpret_cast<const uint4*>(stage + L::X + (b * 16 + l16) * kStepBytes + chunk));
+        } else {
+          typedef short s16x4 __attribute__((ext_vector_type(4)));
+          typedef short s16x8 __attribute__((ext_vector_type(8)));
+          const char* p = stage + L::X + ((h * 32 + 8 * q + (l16 >> 2)) * lw + min(b * 16 + 4 * (l16 & 3), lw - 4)) * 2;
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p + 4 * lw * 2));
+          w = __builtin_bit_cast(bf16x8_t, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+        }
+        acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xv, acc[b], 0, 0, 0);
       }
-      acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xv, acc[b], 0, 0, 0);
     }
   }
   lds_sync<0>();
@@ -411,8 +431,10 @@ __device__ __forceinline__ void down64_tile(const AdapterDesc& d, const int4 til
 template <int RB>
 __global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down64(const AdapterDesc d, int with_h, int chunks) {
   __shared__ __attribute__((aligned(16))) char lds[Down64<RB>::BYTES];
-  const int t = blockIdx.x, z = blockIdx.y;
-  const int4 tile = adapter_tile<64>(d, t);
+  const int z = blockIdx.y;
+  const int4 tile = adapter_tile<64>(d, blockIdx.x, gridDim.x);
+  const int t = tile.w;
+  if (t >= d.p.tiles) return;
   const bool back = (int)blockIdx.z >= chunks || !with_h;
   const int j0 = (blockIdx.z % chunks) * kDownRanks;
   if (z == 0 && blockIdx.z == 0 && threadIdx.x == 0) d.tab[t] = tile;
@@ -421,38 +443,72 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down64(const Adapte
   else down64_tile<RB, false>(d, tile, t, z, j0, lds);
 }
 
-// The slices' sums, in the first slice's place, and the three bf16 numbers of each for the adapters' gradients: a
-// workgroup takes four rows (neighbours in `turned`) of 64 ranks.
-__global__ __launch_bounds__(256) void k_adapter_sum(const AdapterDesc d, int with_h) {
-  const int t = blockIdx.x, which = !with_h || blockIdx.z, RT = d.p.rt;
-  if (d.tab[t].x < 0) return;
-  float* h = (which ? d.dh : d.h) + (size_t)t * RT * d.r;
+// Behind it, for each of h and dh: the slices' sums times the adapter's scale, as two bf16 numbers (three for fp32
+// outputs) in rows of ranks for the second product, and as three with the tile's rows along for the adapters' gradients.
+// Four rows of four ranks a thread.
+template <int KS>
+__device__ __forceinline__ void sum_rows(const AdapterDesc& d, const float* h, size_t slab, float (&f)[4][4], float scale) {
+  f32x4_t v[4][KS];
+#pragma unroll
+  for (int z = 0; z < KS; ++z)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i][z] = *reinterpret_cast<const f32x4_t*>(h + z * slab + (size_t)i * d.r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+#pragma unroll
+    for (int z = 1; z < KS; ++z) v[i][0] += v[i][z];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[i][e] = v[i][0][e] * scale;
+  }
+}
+__global__ __launch_bounds__(64) void k_adapter_sum(const AdapterDesc d, int with_h) {
+  const int t = blockIdx.x, which = !with_h || blockIdx.z, r4 = d.r >> 2;
+  const int e = blockIdx.y * 64 + threadIdx.x, r0 = e / r4 * 4, j = (e - e / r4 * r4) * 4;
+  const int g = d.tab[t].x;
+  if (g < 0 || r0 >= 64) return;
+  const size_t at = (size_t)t * 64 * d.r;
+  const float* h = (which ? d.dh : d.h) + at + (size_t)r0 * d.r + j;
+  uint16_t* rows = which ? d.dhp : d.hp;
   uint16_t* turned = which ? d.dht : d.ht;
-  const size_t slab = (size_t)d.p.tiles * RT * d.r;
-  for (int e = blockIdx.y * 256 + threadIdx.x; e < RT / 4 * d.r; e += gridDim.y * 256) {
-    const int j = e % d.r, r0 = e / d.r * 4;
-    float v[4];
+  const size_t slab = (size_t)d.p.tiles * 64 * d.r;
+  const float scale = d.scales ? d.scales[g] : 1.f;
+  float f[4][4];
+  switch (d.p.ks) {
+    case 1: sum_rows<1>(d, h, slab, f, scale); break;
+    case 2: sum_rows<2>(d, h, slab, f, scale); break;
+    case 4: sum_rows<4>(d, h, slab, f, scale); break;
+    default: sum_rows<8>(d, h, slab, f, scale);
+  }
+#pragma unroll
+  for (int n = 0; n < 3; ++n) {
+    uint32_t p[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[i] = 0.f;
-      for (int z = 0; z < d.p.ks; ++z) v[i] += h[z * slab + (size_t)(r0 + i) * d.r + j];
-      h[(size_t)(r0 + i) * d.r + j] = v[i];
+      p[i][0] = pack_bf16(f[i][0], f[i][1]);
+      p[i][1] = pack_bf16(f[i][2], f[i][3]);
+      if (rows && (n < 2 || d.out_f32)) *reinterpret_cast<uint2*>(rows + 3 * at + ((size_t)n * 64 + r0 + i) * d.r + j) = uint2{p[i][0], p[i][1]};
     }
-    if (!turned) continue;
+    if (turned) {
 #pragma unroll
-    for (int n = 0; n < 3; ++n) {
-      const uint32_t a = pack_bf16(v[0], v[1]), b = pack_bf16(v[2], v[3]);
-      *reinterpret_cast<uint2*>(turned + (((size_t)t * 3 + n) * d.r + j) * RT + r0) = uint2{a, b};
-      const float g[4] = {bf2f(a & 0xFFFFu), bf2f(a >> 16), bf2f(b & 0xFFFFu), bf2f(b >> 16)};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = fabsf(g[i]) == __builtin_huge_valf() ? 0.f : v[i] - g[i];
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t sel = k & 1 ? 0x07060302u : 0x05040100u;
+        *reinterpret_cast<uint2*>(turned + 3 * at + ((size_t)n * d.r + j + k) * 64 + r0) =
+            uint2{__builtin_amdgcn_perm(p[1][k >> 1], p[0][k >> 1], sel), __builtin_amdgcn_perm(p[3][k >> 1], p[2][k >> 1], sel)};
+      }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float v = __uint_as_float(k & 1 ? p[i][k >> 1] & 0xFFFF0000u : p[i][k >> 1] << 16);
+        f[i][k] = fabsf(v) == __builtin_huge_valf() ? 0.f : f[i][k] - v;
+      }
   }
 }
 
 hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s) {
   const int with_h = d.h != nullptr, with_dh = d.dh != nullptr, chunks = (d.r + kDownRanks - 1) / kDownRanks;
-  const dim3 grid(d.p.tiles, d.p.ks, (with_h + with_dh) * chunks), block(kDownWaves * 64);
+  const dim3 grid((d.p.tiles + 7) / 8 * 8, d.p.ks, (with_h + with_dh) * chunks), block(kDownWaves * 64);
   if (d.p.rt == 16) {
     if (d.r <= 16) ffn_launch((k_adapter_down<16, 1>), grid, block, 0, s, d, with_h, chunks);
     else if (d.r <= 32) ffn_launch((k_adapter_down<16, 2>), grid, block, 0, s, d, with_h, chunks);
@@ -465,9 +521,8 @@ hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s) {
   else if (d.r <= 64) ffn_launch((k_adapter_down64<4>), grid, block, 0, s, d, with_h, chunks);
   else ffn_launch((k_adapter_down64<8>), grid, block, 0, s, d, with_h, chunks);
   const hipError_t e = hipGetLastError();
-  // backward: both consumers read the sums; forward, the second product adds the slices as it reads them
-  if (e != hipSuccess || !d.back) return e;
-  ffn_launch(k_adapter_sum, dim3(d.p.tiles, (d.r * 16 + 255) / 256, with_h + with_dh), dim3(256), 0, s, d, with_h);
+  if (e != hipSuccess) return e;
+  ffn_launch(k_adapter_sum, dim3(d.p.tiles, (d.r * 4 + 63) / 64, with_h + with_dh), dim3(64), 0, s, d, with_h);
   return hipGetLastError();
 }
 
@@ -495,8 +550,9 @@ __device__ __forceinline__ void transpose8(const uint4 (&in)[8], uint4 (&out)[8]
 // and columns exchanged, 16 bytes a row from each of 16 lanes, 8192 x 4096 x 14336 took 160 us.) F: groups of 32 ranks (0: up to 16, hi and lo in one group).
 // ALONG: W = B, rows of r elements a column; otherwise W = A^T, rows of the output's columns.
 template <typename T, int RT, int F, bool ALONG>
-__global__ __launch_bounds__(256) void k_adapter_up(const AdapterDesc d) {
+__global__ __launch_bounds__(256, F == 0 ? (RT == 16 ? 4 : 3) : F == 1 ? 3 : 2) void k_adapter_up(const AdapterDesc d) {
   constexpr int NF = F == 0 ? 1 : F;
+  __shared__ __attribute__((aligned(16))) char s_w[ALONG ? 4 * (128 * (F == 0 ? 2 : 4) * 16 + 256) : 16];
   const int lane = lane_id(), wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
   const int cols = ALONG ? d.n : d.k;
   const int c0 = (blockIdx.x * 4 + wave) * 128;
@@ -519,28 +575,60 @@ __global__ __launch_bounds__(256) void k_adapter_up(const AdapterDesc d) {
     }
     return;
   }
+  constexpr bool READY = RT == 64;               // s h is there in bf16 numbers; otherwise it is made of the slices here
+  constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
   const float* hsrc = (ALONG ? d.h : d.dh) + (size_t)t * RT * d.r;
+  const uint16_t* hrow = (ALONG ? d.hp : d.dhp) + (size_t)t * 3 * RT * d.r;
   const size_t slab = (size_t)d.p.tiles * RT * d.r;
-  const int slabs = d.back ? 1 : d.p.ks;         // backward, they have been added already
   const float scale = d.scales ? d.scales[tile.x] : 1.f;
   const uint16_t* w = ALONG ? d.b + (size_t)tile.x * d.n * d.r : d.a + (size_t)tile.x * d.r * d.k;
   const int jq = F == 0 ? (q & 1) * 8 : q * 8;   // this lane's first rank in a group
   const int wc = c0 + 8 * l16;                   // this lane's eight columns
-  // the weights of up to 64 ranks stay in registers for all of the tile's rows
+  // lane l has the row of place l of the tile
+  const int mine = row_at(d, min(tile.y + min(lane, RT - 1), tile.z - 1)), rows = tile.z - tile.y;
+  // The weights of up to 64 ranks stay in registers for all of the tile's rows. B's come through the wave's own part of
+  // LDS: neighbouring lanes load neighbouring chunks of a column's ranks (`pieces` of them in a group), 16 bytes of
+  // padding every eight columns keep the operands' reads, eight columns apart, out of each other's banks.
   constexpr bool STAY = NF <= 2;
-  uint4 wv[STAY ? NF : 1][8];
-  auto weights = [&](int g) {
-    uint4(&o)[8] = wv[STAY ? g : 0];
-    const int j = g * 32 + jq, jc = min(j, d.r - 8);
+  constexpr int PIECES = F == 0 ? 2 : 4;
+  uint4 wv[STAY ? NF : 1][8], raw[ALONG ? 2 * PIECES : 8];
+  char* lds = s_w + wave * (ALONG ? 128 * PIECES * 16 + 256 : 0);
+  auto chunk = [&](int n, int& col, int& piece) {
+    const int c = n * 64 + lane;
+    col = c / PIECES;
+    piece = c % PIECES;
+  };
+  auto ask = [&](int g) {
     if constexpr (ALONG) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = ldg16(w + (size_t)min(wc + e, cols - 1) * d.r + jc);
+      for (int n = 0; n < 2 * PIECES; ++n) {
+        int col, piece;
+        chunk(n, col, piece);
+        raw[n] = ldg16(w + (size_t)min(c0 + col, cols - 1) * d.r + min(g * 32 + piece * 8, d.r - 8));
+      }
+    } else {
+      const int jc = min(g * 32 + jq, d.r - 8);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) raw[e] = ldg16(w + (size_t)(jc + e) * cols + min(wc, cols - 8));
+    }
+  };
+  auto weights = [&](int g) {
+    uint4(&o)[8] = wv[STAY ? g : 0];
+    if constexpr (ALONG) {
+#pragma unroll
+      for (int n = 0; n < 2 * PIECES; ++n) {
+        int col, piece;
+        chunk(n, col, piece);
+        *reinterpret_cast<uint4*>(lds + (col * PIECES + piece + (col >> 3)) * 16) = raw[n];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = *reinterpret_cast<const uint4*>(lds + ((8 * l16 + e) * PIECES + (jq >> 3) + l16) * 16);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = ldg16(w + (size_t)(jc + e) * cols + min(wc, cols - 8));
+      for (int e = 0; e < 8; ++e) o[e] = raw[e];
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = keep_if(j < d.r, o[e]);
+    for (int e = 0; e < 8; ++e) o[e] = keep_if(g * 32 + jq < d.r, o[e]);
     if constexpr (!ALONG) {
       uint4 in[8];
 #pragma unroll
@@ -548,36 +636,49 @@ __global__ __launch_bounds__(256) void k_adapter_up(const AdapterDesc d) {
       transpose8(in, o);
     }
   };
+  // without a base, every row is the same eight zeros
+  const void* from = d.base ? d.base : adapter_zero;
+  const size_t pitch = d.base ? cols : 0;
+  const int at = d.base ? min(wc, cols - 8) : 0;
+  int row[4];
+  Row8<T> base[4];
+  uint4 hv[NF][PARTS];                         // F = 0: hi for q < 2, lo for the others, in the first; then the third
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      row[v] = __shfl(mine, min(i0 + 4 * q + v, rows - 1), 64);
+      base[v].load(from, (size_t)max(row[v], 0) * pitch + at);
+    }
+    if constexpr (READY) {
+      const uint16_t* p = hrow + (size_t)min(i0 + l16, RT - 1) * d.r;
+#pragma unroll
+      for (int g = 0; g < NF; ++g)
+#pragma unroll
+        for (int n = 0; n < PARTS; ++n) {
+          if (F == 0 && n == 1) continue;
+          hv[g][n] = ldg16(p + (size_t)(F == 0 && n == 0 ? q >> 1 : n) * RT * d.r + min(g * 32 + jq, d.r - 8));
+        }
+    }
+  };
+  ask(0);
+  fetch(0);
+  __builtin_amdgcn_sched_barrier(0);
   if constexpr (STAY) {
-#pragma unroll
-    for (int g = 0; g < NF; ++g) weights(g);
+    weights(0);
+    if constexpr (NF > 1) {
+      ask(1);
+      weights(1);
+    }
   }
-  // lane l has the row of place l of the tile
-  const int mine = row_at(d, min(tile.y + min(lane, RT - 1), tile.z - 1)), rows = tile.z - tile.y;
-  auto run = [&](auto with_base) {
-    constexpr bool BASE = decltype(with_base)::value;
-    int row[4];
-    Row8<T> base[4];
-    auto fetch = [&](int i0) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        row[v] = __shfl(mine, min(i0 + 4 * q + v, rows - 1), 64);
-        base[v].zero();
-        if constexpr (BASE) base[v].load(d.base, (size_t)max(row[v], 0) * cols + min(wc, cols - 8));
-      }
-    };
-    fetch(0);
 #pragma unroll 1
-    for (int i0 = 0; i0 < rows; i0 += 16) {
+  for (int i0 = 0; i0 < rows; i0 += 16) {
+    if constexpr (!READY) {
       f32x4_t ha[NF][2];
       const float* hp = hsrc + (size_t)(i0 + l16) * d.r;
 #pragma unroll
-      for (int g = 0; g < NF; ++g) {
-        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(hp + min(g * 32 + jq, d.r - 8));
-        ha[g][0] = p[0];
-        ha[g][1] = p[1];
-      }
-      for (int z = 1; z < slabs; ++z) {
+      for (int g = 0; g < NF; ++g) ha[g][0] = ha[g][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int z = 0; z < d.p.ks; ++z) {
 #pragma unroll
         for (int g = 0; g < NF; ++g) {
           const f32x4_t* p = reinterpret_cast<const f32x4_t*>(hp + z * slab + min(g * 32 + jq, d.r - 8));
@@ -585,57 +686,69 @@ __global__ __launch_bounds__(256) void k_adapter_up(const AdapterDesc d) {
           ha[g][1] += p[1];
         }
       }
-      f32x4_t acc[8];                            // the sums start from the base
-      int to[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        float f[8];
-        base[v].get(f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e][v] = f[e];
-        to[v] = i0 + 4 * q + v < rows ? row[v] : -1;
-      }
-      if (RT > 16) fetch(i0 + 16);               // the next rows' base (past the last: the last row again)
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int g = 0; g < NF; ++g) {
-        if constexpr (!STAY) weights(g);
-        const uint4(&o)[8] = wv[STAY ? g : 0];
-        const bool in = g * 32 + jq < d.r;
         float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = in ? ha[g][e >> 2][e & 3] * scale : 0.f;
+        for (int e = 0; e < 8; ++e) f[e] = ha[g][e >> 2][e & 3] * scale;
         const uint4 hi = pack8(f);
         remainder8(f, hi);
         const uint4 lo = pack8(f);
-        uint4 one = hi;
-        if constexpr (F == 0) one = q < 2 ? hi : lo;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(one), as_bf16x8(o[e]), acc[e], 0, 0, 0);
-        if constexpr (F != 0) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(lo), as_bf16x8(o[e]), acc[e], 0, 0, 0);
-        }
-        if constexpr (sizeof(T) == 4) {
+        hv[g][0] = hi;
+        hv[g][1] = lo;
+        if constexpr (F == 0) hv[g][0] = q < 2 ? hi : lo;
+        if constexpr (PARTS == 3) {
           remainder8(f, lo);
-          const uint4 rest = keep_if(F != 0 || q < 2, pack8(f));
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(rest), as_bf16x8(o[e]), acc[e], 0, 0, 0);
+          hv[g][2] = pack8(f);
         }
-      }
-      if (wc >= cols) continue;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (to[v] < 0) continue;
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = acc[e][v];
-        Row8<T>::store(d.out, (size_t)to[v] * cols + wc, f);
       }
     }
-  };
-  if (d.base) run(std::true_type{});
-  else run(std::false_type{});
+    f32x4_t acc[8];                            // the sums start from the base
+    int to[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      float f[8];
+      base[v].get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e][v] = f[e];
+      to[v] = i0 + 4 * q + v < rows ? row[v] : -1;
+    }
+    uint4 now[NF][PARTS];
+#pragma unroll
+    for (int g = 0; g < NF; ++g)
+#pragma unroll
+      for (int n = 0; n < PARTS; ++n) {
+        if (F == 0 && n == 1) continue;
+        now[g][n] = keep_if(g * 32 + jq < d.r && (F != 0 || n == 0 || q < 2), hv[g][n]);
+      }
+    // the next rows' (past the last: the last row's again), ahead of this one's stores, which a wait for loads behind
+    // them would be a wait for
+    if (RT > 16) fetch(i0 + 16);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int g = 0; g < NF; ++g) {
+      if constexpr (!STAY) {
+        ask(g);
+        weights(g);
+      }
+      const uint4(&o)[8] = wv[STAY ? g : 0];
+#pragma unroll
+      for (int n = 0; n < PARTS; ++n) {
+        if (F == 0 && n == 1) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(now[g][n]), as_bf16x8(o[e]), acc[e], 0, 0, 0);
+      }
+    }
+    if (wc >= cols) continue;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if (to[v] < 0) continue;
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = acc[e][v];
+      Row8<T>::store(d.out, (size_t)to[v] * cols + wc, f);
+    }
+  }
 }
 
 template <typename T, int RT, bool ALONG>
@@ -658,9 +771,9 @@ hipError_t launch_adapter_up(const AdapterDesc& d, bool back, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- gradients of the adapters
-// dA[j][c] = s sum over the adapter's rows t of dh[t][j] x[t][c], and dB[c][j] = s sum of h[t][j] dy[t][c]: a workgroup
+// dA[j][c] = sum over the adapter's rows t of s dh[t][j] x[t][c], and dB[c][j] = sum of s h[t][j] dy[t][c]: a workgroup
 // has 128 columns c of one adapter and up to 16 RB ranks; its waves take 32 rows in turn, whose 8 x 8 pieces are turned
-// in registers, the next ones under way, and their sums are added in order. h enters as three bf16 numbers.
+// in registers, the next ones under way, and their sums are added in order. s h enters as three bf16 numbers.
 template <int RT, int RB, int WAVES, bool OF_A>
 __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int c0, int j0, float* s_part) {
   const int lane = lane_id(), wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
@@ -731,7 +844,6 @@ __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int c0, int
     }
   }
   // the waves' sums, 16 ranks of the 128 columns at a time: s_part[wave][accumulator][lane] in fours
-  const float scale = d.scales ? d.scales[g] : 1.f;
   auto part = [&](int w, int i, int l) { return s_part + ((w * 8 + i) * 64 + l) * 4; };
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
@@ -753,7 +865,7 @@ __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int c0, int
         if (j >= d.r || c >= cols) continue;
         float* out = d.da + ((size_t)g * d.r + j) * cols + c;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = scale * f[i] + (d.accumulate ? out[i] : 0.f);
+        for (int i = 0; i < 8; ++i) f[i] += d.accumulate ? out[i] : 0.f;
         Row8<float>::store(out, 0, f);
       }
     } else {
@@ -766,7 +878,6 @@ __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int c0, int
         for (int w = 0; w < WAVES; ++w) f += *reinterpret_cast<const f32x4_t*>(part(w, col & 7, lq * 16 + p));
         if (j >= d.r || c >= cols) continue;
         f32x4_t* out = reinterpret_cast<f32x4_t*>(d.db + ((size_t)g * cols + c) * d.r + j);
-        f *= scale;
         if (d.accumulate) f += *out;
         *out = f;
       }
@@ -809,8 +920,8 @@ AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) 
   p.tiles = (int)(tiles < m ? tiles : m);
   // slices: enough workgroups for the chip
   const int live = (m + p.rt - 1) / p.rt;
-  const int least = p.rt == 64 ? 8 : kDownWaves;  // steps of a slice
-  const int steps = (backward ? (n > k ? n : k) : k) / 64;
+  const int least = p.rt == 64 ? 4 : kDownWaves;  // steps of a slice
+  const int steps = (backward ? (n > k ? n : k) : k) / (p.rt == 64 ? kStep : 64);
   int ks = 1;
   if (p.rt == 64 || !backward)
     while (ks < 8 && live * ks < 256 && steps / (ks * 2) >= least) ks *= 2;
