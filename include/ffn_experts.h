@@ -50,9 +50,10 @@ int32_t ffn_experts_abi_version(void);
  *   weights [m x top_k] fp32: scale * s of the chosen, or with renormalize = 1
  *           scale * s / (the sum of the token's chosen s); without the bias
  *   scores  NULL or [m x experts] fp32: s (for losses on all of them)
- * Equal values go to the lower index (of the group, and of the expert). v is
- * compared in fp64, so that the choice is that of the exact scores; without a
- * bias the logits are compared themselves, unless group_best is 2.
+ * Equal values go to the lower index (of the group, and of the expert). Where
+ * scores decide they are told apart in fp64, so that the choice is that of the
+ * exact scores; without a bias experts stand in the order of their logits, and
+ * so do groups with group_best = 1.
  * An expert whose logit is -inf is never chosen, and a group with no other is
  * never kept; where fewer than top_k experts are left, the last slots have id
  * -1 and weight 0, and a token without any has scores of 0. A NaN counts as the

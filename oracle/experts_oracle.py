@@ -29,12 +29,13 @@ def route(logits, top_k, *, sigmoid=False, bias=None, groups=1, top_groups=1, gr
     for t in range(m):
         v = p[t] + (0 if bias is None else np.asarray(bias, np.float64))
         # without a bias the scores are in the logits' order, which does not saturate
-        order = v if bias is not None or (group_best == 2 and top_groups < groups) else l[t]
+        order = v if bias is not None else l[t]
+        of_group = v if bias is not None or group_best == 2 else l[t]
         alive = [e for e in range(experts) if not np.isneginf(l[t, e])]
         if top_groups < groups:
             of = {}
             for g in range(groups):
-                best = sorted((order[e] for e in alive if e // size == g), reverse=True)[:group_best]
+                best = sorted((of_group[e] for e in alive if e // size == g), reverse=True)[:group_best]
                 if best:
                     of[g] = sum(best)
             kept = sorted(of, key=lambda g: (-of[g], g))[:top_groups]
