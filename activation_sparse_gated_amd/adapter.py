@@ -15,7 +15,21 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .linear import _DTYPES, _accumulator, _call, _check, _first, _nbytes, _on_stream, _product_out, _ptr, _workspace
+from .linear import _DTYPES, _accumulator, _call, _check, _fail, _first, _nbytes, _on_stream, _product_out, _ptr, _workspace
+
+
+def _shapes(x, a, b):
+    """(device, m, k, adapters, r, n) of the rows and the adapters."""
+    dev = _first("x", x, (torch.bfloat16,), (2,))
+    for name, t in (("a", a), ("b", b)):
+        if getattr(t, "ndim", 0) != 3:
+            _fail(name, t, "bfloat16 tensor of 3 dimensions")
+    m, k = x.shape
+    groups, r, _ = a.shape
+    n = b.shape[1]
+    _check("a", a, torch.bfloat16, (groups, r, k), dev)
+    _check("b", b, torch.bfloat16, (groups, n, r), dev)
+    return dev, m, k, groups, r, n
 
 
 def _order(offsets, rows, groups, m, dev):
@@ -34,14 +48,7 @@ def adapter_forward(x, a, b, offsets, *, rows=None, scales=None, base=None, y=No
     [adapters] or None (ones); base [m, n], the shared projection's output, or
     None (zeros). y [m, n] of base's type (out_dtype without a base: bf16 or
     fp32); it may be base, which is then added to in place."""
-    dev = _first("x", x, (torch.bfloat16,), (2,))
-    _first("a", a, (torch.bfloat16,), (3,))
-    _first("b", b, (torch.bfloat16,), (3,))
-    m, k = x.shape
-    groups, r, _ = a.shape
-    n = b.shape[1]
-    _check("a", a, torch.bfloat16, (groups, r, k), dev)
-    _check("b", b, torch.bfloat16, (groups, n, r), dev)
+    dev, m, k, groups, r, n = _shapes(x, a, b)
     _order(offsets, rows, groups, m, dev)
     if scales is not None:
         _check("scales", scales, torch.float32, (groups,), dev)
@@ -49,9 +56,12 @@ def adapter_forward(x, a, b, offsets, *, rows=None, scales=None, base=None, y=No
         if getattr(base, "dtype", None) in _DTYPES:
             out_dtype = base.dtype
         _check("base", base, out_dtype, (m, n), dev)
-        if y is not None:
+        if y is None:
+            y = torch.empty_like(base)
+        elif y is not base:
             _check("y", y, out_dtype, (m, n), dev)
-    y = _product_out(y, (m, n), out_dtype, dev)
+    else:
+        y = _product_out(y, (m, n), out_dtype, dev)
     lib = _lib.load()
     workspace = _workspace(workspace, lib.ffn_adapter_forward_workspace_bytes(m, n, k, r, groups), dev)
     _call(lib.ffn_adapter_forward, dev, _ptr(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(offsets), _ptr(rows), groups, m, n,
@@ -77,14 +87,7 @@ def adapter_backward(x, a, b, dy, offsets, *, rows=None, scales=None, base=None,
             raise ValueError(f"{name}: given without need_{'dx' if name == 'base' else name}")
     if accumulate and not (need_da or need_db):
         raise ValueError("accumulate: given without need_da or need_db")
-    dev = _first("x", x, (torch.bfloat16,), (2,))
-    _first("a", a, (torch.bfloat16,), (3,))
-    _first("b", b, (torch.bfloat16,), (3,))
-    m, k = x.shape
-    groups, r, _ = a.shape
-    n = b.shape[1]
-    _check("a", a, torch.bfloat16, (groups, r, k), dev)
-    _check("b", b, torch.bfloat16, (groups, n, r), dev)
+    dev, m, k, groups, r, n = _shapes(x, a, b)
     _check("dy", dy, torch.bfloat16, (m, n), dev)
     _order(offsets, rows, groups, m, dev)
     if scales is not None:
@@ -93,7 +96,7 @@ def adapter_backward(x, a, b, dy, offsets, *, rows=None, scales=None, base=None,
         _check("base", base, torch.bfloat16, (m, k), dev)
     if need_dx:
         if dx is None:
-            dx = torch.empty(m, k, dtype=torch.bfloat16, device=dev)
+            dx = torch.empty_like(x)
         else:
             _check("dx", dx, torch.bfloat16, (m, k), dev)
     if need_da:

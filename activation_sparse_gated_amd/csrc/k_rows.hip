@@ -21,52 +21,56 @@ constexpr int kBlock = 4096;                     // entries of a block, where th
 
 // The place of each of this lane's entries (entry i * 64 + lane of the wave's run) among those of its group in the run,
 // and the run's counts in cnt[0 .. groups] (this wave's own, cleared). key: the group, `groups` for none, -1 past the end.
-template <int TURNS>
-__device__ __forceinline__ void rank_run(const int (&key)[TURNS], int (&rank)[TURNS], uint16_t* cnt, int bits) {
-  const uint64_t below = lanemask_lt();
+template <int TURNS, int BITS>
+__device__ __forceinline__ void rank_run(const int (&key)[TURNS], int (&rank)[TURNS], uint16_t* cnt) {
 #pragma unroll
   for (int i = 0; i < TURNS; ++i) {
     const bool in = key[i] >= 0;
-    uint64_t same = ballot64(in);
+    uint64_t same = ballot64(in);                // lanes of this lane's group
     if (same == 0) break;
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t set = ballot64(in && (key[i] >> b & 1));
-      same &= key[i] >> b & 1 ? set : ~set;
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) {
+      const int mine = (int)((uint32_t)key[i] << (31 - b)) >> 31;
+      const uint64_t set = ballot64(mine != 0);
+      same &= ~(set ^ ((uint64_t)(uint32_t)mine << 32 | (uint32_t)mine));
     }
-    rank[i] = in ? (int)cnt[key[i]] + __popcll(same & below) : 0;
+    const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0u));
+    const int had = cnt[max(key[i], 0)];
+    rank[i] = had + before;
     // every lane has read its count before the group's first lane adds to it (a wave's LDS accesses are in order)
     __builtin_amdgcn_wave_barrier();
-    if (in && (same & below) == 0) cnt[key[i]] = (uint16_t)(cnt[key[i]] + __popcll(same));
+    if (in && before == 0) cnt[key[i]] = (uint16_t)(had + __popcll(same));
     __builtin_amdgcn_wave_barrier();
   }
 }
 
 // COUNT: only the block's counts, to hist[block]. Otherwise the places, with the counts of the other blocks from hist if
 // there are any.
-template <int NT, int TURNS, bool COUNT>
+template <int NT, int TURNS, int BITS, bool COUNT>
 __global__ __launch_bounds__(NT) void k_group_rows(const GroupDesc d, int blocks) {
   constexpr int W = NT / 64, KPT = (kRowsMaxGroups + NT - 1) / NT;
   __shared__ uint16_t s_cnt[W][kRowsMaxGroups + 2];
   __shared__ int s_base[kRowsMaxGroups + 1];
   __shared__ int s_scan[W];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int G = d.groups, bits = 32 - __clz(G);
+  const int G = d.groups;
   const int begin = blockIdx.x * (NT * TURNS), run = begin + wave * (64 * TURNS);
   int key[TURNS], rank[TURNS];
 #pragma unroll
   for (int i = 0; i < TURNS; ++i) {
-    const int at = run + i * 64 + lane;
-    const int id = at < d.n ? d.ids[at] : 0;
-    key[i] = at >= d.n ? -1 : id >= 0 && id < G ? id : G;
+    key[i] = d.ids[min(run + i * 64 + lane, d.n - 1)];
     rank[i] = 0;
   }
   for (int c = lane; c <= G; c += 64) s_cnt[wave][c] = 0;
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i) key[i] = run + i * 64 + lane >= d.n ? -1 : key[i] >= 0 && key[i] < G ? key[i] : G;
   __builtin_amdgcn_wave_barrier();
-  rank_run<TURNS>(key, rank, s_cnt[wave], bits);
+  rank_run<TURNS, BITS>(key, rank, s_cnt[wave]);
   __syncthreads();
   if constexpr (COUNT) {
     for (int c = tid; c <= G; c += NT) {
       int v = 0;
+#pragma unroll
       for (int w = 0; w < W; ++w) v += s_cnt[w][c];
       d.hist[(size_t)blockIdx.x * (G + 1) + c] = (uint32_t)v;
     }
@@ -75,11 +79,13 @@ __global__ __launch_bounds__(NT) void k_group_rows(const GroupDesc d, int blocks
   // s_cnt becomes the counts of the waves before; `all` and `earlier`: of every block, and of the blocks before this one
   int all[KPT + 1], earlier[KPT + 1];
   auto count = [&](int c, int& total, int& before) {
-    int v = 0;
+    int v = 0, n[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) n[w] = s_cnt[w][c];
+#pragma unroll
     for (int w = 0; w < W; ++w) {
-      const int n = s_cnt[w][c];
       s_cnt[w][c] = (uint16_t)v;
-      v += n;
+      v += n[w];
     }
     total = v;
     before = 0;
@@ -129,19 +135,29 @@ __global__ __launch_bounds__(NT) void k_group_rows(const GroupDesc d, int blocks
 
 int group_rows_blocks(int n) { return n <= kOneBlock ? 1 : (n + kBlock - 1) / kBlock; }
 
-hipError_t launch_group_rows(const GroupDesc& d, hipStream_t s) {
+template <int BITS>
+static hipError_t group_rows(const GroupDesc& d, hipStream_t s) {
   const int blocks = group_rows_blocks(d.n);
   if (blocks > 1) {
-    ffn_launch((k_group_rows<1024, 4, true>), dim3(blocks), dim3(1024), 0, s, d, blocks);
-    ffn_launch((k_group_rows<1024, 4, false>), dim3(blocks), dim3(1024), 0, s, d, blocks);
+    ffn_launch((k_group_rows<1024, 4, BITS, true>), dim3(blocks), dim3(1024), 0, s, d, blocks);
+    ffn_launch((k_group_rows<1024, 4, BITS, false>), dim3(blocks), dim3(1024), 0, s, d, blocks);
   } else if (d.n <= 256) {
-    ffn_launch((k_group_rows<256, 1, false>), dim3(1), dim3(256), 0, s, d, 1);
+    ffn_launch((k_group_rows<256, 1, BITS, false>), dim3(1), dim3(256), 0, s, d, 1);
   } else if (d.n <= 4096) {
-    ffn_launch((k_group_rows<1024, 4, false>), dim3(1), dim3(1024), 0, s, d, 1);
+    ffn_launch((k_group_rows<1024, 4, BITS, false>), dim3(1), dim3(1024), 0, s, d, 1);
+  } else if (d.n <= 8192) {
+    ffn_launch((k_group_rows<1024, 8, BITS, false>), dim3(1), dim3(1024), 0, s, d, 1);
   } else {
-    ffn_launch((k_group_rows<1024, 16, false>), dim3(1), dim3(1024), 0, s, d, 1);
+    ffn_launch((k_group_rows<1024, 16, BITS, false>), dim3(1), dim3(1024), 0, s, d, 1);
   }
   return hipGetLastError();
+}
+hipError_t launch_group_rows(const GroupDesc& d, hipStream_t s) {
+  // bits of a group's number, `groups` (none) among them
+  if (d.groups < 16) return group_rows<4>(d, s);
+  if (d.groups < 64) return group_rows<6>(d, s);
+  if (d.groups < 512) return group_rows<9>(d, s);
+  return group_rows<11>(d, s);
 }
 
 // ---------------------------------------------------------------- gather

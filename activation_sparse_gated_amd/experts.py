@@ -17,7 +17,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .linear import _DTYPES, FP8, Fp8Tensor, _blocks, _call, _check, _check_fp8, _first, _nbytes, _on_stream, _ptr, _workspace
+from .linear import _DTYPES, FP8, Fp8Tensor, _blocks, _call, _check, _check_fp8, _fail, _first, _nbytes, _on_stream, _ptr, _workspace
 
 _TYPES = (torch.bfloat16, torch.float32)
 
@@ -33,6 +33,22 @@ def _out(name, t, dtype, shape, dev):
         return torch.empty(shape, dtype=dtype, device=dev)
     _check(name, t, dtype, shape, dev)
     return t
+
+
+def _out_like(name, t, ref, shape):
+    """The same in ref's type, on its device."""
+    if t is None:
+        return ref.new_empty(shape)
+    _check(name, t, ref.dtype, shape, ref.device)
+    return t
+
+
+def _pairs(name, t, m, dev):
+    """The second dimension of an int32 tensor [m, .]; m None: any."""
+    if getattr(t, "ndim", 0) != 2:
+        _fail(name, t, "int32 tensor of 2 dimensions")
+    _check(name, t, torch.int32, t.shape if m is None else (m, t.shape[1]), dev)
+    return t.shape[1]
 
 
 # ---------------------------------------------------------------- router
@@ -77,13 +93,11 @@ def route_backward(logits, ids, dweights, *, dscores=None, score="softmax", reno
     fp32 [m, experts] or None. score, renormalize and scale as there."""
     dev = _first("logits", logits, _TYPES, (2,))
     m, experts = logits.shape
-    _first("ids", ids, (torch.int32,), (2,))
-    top_k = ids.shape[1]
-    _check("ids", ids, torch.int32, (m, top_k), dev)
+    top_k = _pairs("ids", ids, m, dev)
     _check("dweights", dweights, torch.float32, (m, top_k), dev)
     if dscores is not None:
         _check("dscores", dscores, torch.float32, (m, experts), dev)
-    dlogits = _out("dlogits", dlogits, logits.dtype, (m, experts), dev)
+    dlogits = _out_like("dlogits", dlogits, logits, (m, experts))
     _call(_lib.load().ffn_route_backward, dev, logits.data_ptr(), _DTYPES[logits.dtype], m, experts, top_k, _score(score),
           int(bool(renormalize)), float(scale), ids.data_ptr(), dweights.data_ptr(), _ptr(dscores), dlogits.data_ptr())
     return dlogits
@@ -104,19 +118,13 @@ def group_rows(ids, groups, *, offsets=None, rows=None, slots=None, workspace=No
     if groups < 1:
         raise ValueError(f"groups: 1 at least, got {groups}")
     offsets = _out("offsets", offsets, torch.int32, (groups + 1,), dev)
-    rows = _out("rows", rows, torch.int32, (n,), dev)
-    slots = _out("slots", slots, torch.int32, ids.shape, dev)
+    rows = _out_like("rows", rows, ids, (n,))
+    slots = _out_like("slots", slots, ids, ids.shape)
     lib = _lib.load()
     workspace = _workspace(workspace, lib.ffn_group_rows_workspace_bytes(n, groups), dev)
     _call(lib.ffn_group_rows, dev, _ptr(ids), n, groups, _ptr(offsets), _ptr(rows), _ptr(slots), _ptr(workspace),
           _nbytes(workspace))
     return offsets, rows, slots
-
-
-def _rows_of(slots, m, dev):
-    _first("slots", slots, (torch.int32,), (2,))
-    _check("slots", slots, torch.int32, (m, slots.shape[1]), dev)
-    return slots.shape[1]
 
 
 @_on_stream
@@ -129,7 +137,7 @@ def gather_forward(x, slots, *, fp8=False, y=None):
     rows that no slot names are left as they were."""
     dev = _first("x", x, _TYPES, (2,))
     m, d = x.shape
-    top_k = _rows_of(slots, m, dev)
+    top_k = _pairs("slots", slots, m, dev)
     n = m * top_k
     if fp8:
         if y is None:
@@ -139,7 +147,7 @@ def gather_forward(x, slots, *, fp8=False, y=None):
             _check_fp8("y", y, (n, d), 1, dev)
         out, q, scale = None, y.q, y.scale
     else:
-        y = _out("y", y, x.dtype, (n, d), dev)
+        y = _out_like("y", y, x, (n, d))
         out, q, scale = y, None, None
     _call(_lib.load().ffn_gather_forward, dev, _ptr(x), _DTYPES[x.dtype], m, d, _ptr(slots), top_k, _ptr(out), _ptr(q),
           _ptr(scale))
@@ -166,16 +174,15 @@ def combine_forward(y, slots, weights=None, *, residual=None, out=None):
 
 def _combine(y, slots, weights, residual, out, y_name, out_name):
     dev = _first(y_name, y, _TYPES, (2,))
-    _first("slots", slots, (torch.int32,), (2,))
-    m, top_k = slots.shape
-    d = y.shape[1]
-    _check(y_name, y, y.dtype, (m * top_k, d), dev)
-    _check("slots", slots, torch.int32, (m, top_k), dev)
+    top_k = _pairs("slots", slots, None, dev)
+    m, (n, d) = slots.shape[0], y.shape
+    if n != m * top_k:
+        _fail(y_name, y, f"tensor of {m * top_k} rows")
     if weights is not None:
         _check("weights", weights, torch.float32, (m, top_k), dev)
     if residual is not None:
         _check("residual", residual, y.dtype, (m, d), dev)
-    out = _out(out_name, out, y.dtype, (m, d), dev)
+    out = _out_like(out_name, out, y, (m, d))
     _call(_lib.load().ffn_combine_forward, dev, _ptr(y), _DTYPES[y.dtype], m, d, _ptr(slots), top_k, _ptr(weights),
           _ptr(residual), _ptr(out))
     return out
@@ -196,13 +203,13 @@ def combine_backward(y, slots, weights, dout, *, need_dy=True, need_dweights=Tru
         raise ValueError("dy, dweights: given without need_dy or need_dweights")
     dev = _first("dout", dout, _TYPES, (2,))
     m, d = dout.shape
-    top_k = _rows_of(slots, m, dev)
+    top_k = _pairs("slots", slots, m, dev)
     if need_dweights or y is not None:
         _check("y", y, dout.dtype, (m * top_k, d), dev)
     if weights is not None:
         _check("weights", weights, torch.float32, (m, top_k), dev)
     if need_dy:
-        dy = _out("dy", dy, dout.dtype, (m * top_k, d), dev)
+        dy = _out_like("dy", dy, dout, (m * top_k, d))
     if need_dweights:
         dweights = _out("dweights", dweights, torch.float32, (m, top_k), dev)
     _call(_lib.load().ffn_combine_backward, dev, _ptr(y), _DTYPES[dout.dtype], m, d, _ptr(slots), top_k, _ptr(weights),
