@@ -12,8 +12,10 @@ constexpr int kAdapterMaxRank = 256;
 // How a call is run (adapter_plan, a rule on sizes alone).
 struct AdapterPlan {
   int rt;                        // rows of a tile: 16 or 64
-  int ks;                        // slices of the first product's contraction
+  int ks, kd;                    // slices of the contraction of x A^T and of dy B
   int tiles;                     // tiles at most, those of rows without an adapter among them
+  int split, slices;             // of an adapter's rows for its gradients: waves that share a column block, and slices besides
+  size_t part;                   // values of a slice's gradients
 };
 
 struct AdapterDesc {
@@ -29,9 +31,10 @@ struct AdapterDesc {
   AdapterPlan p;
   // workspace
   int4* tab;                     // [tiles]: adapter (-1: none, -2: no tile), first place, end
-  float *h, *dh;                 // [ks][tiles][rt][r]: x A^T and dy B
-  uint16_t *hp, *dhp;            // tiles of 64 rows: [tiles][3][64][r], s h and s dh in bf16 numbers
+  float *h, *dh;                 // [ks or kd][tiles][rt][r]: x A^T and dy B
+  uint16_t *hp, *dhp;            // [tiles][3][rt][r]: s h (tiles of 64 rows) and s dh in bf16 numbers
   uint16_t *ht, *dht;            // null, or [tiles][3][r][rt]: the same with the rows along
+  float* part;                   // [slices][part]: partial gradients, if slices > 1
 };
 
 AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward);

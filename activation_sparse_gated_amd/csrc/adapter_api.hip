@@ -29,11 +29,13 @@ bool shape_ok(int32_t m, int32_t n, int32_t k, int32_t r, int32_t groups) {
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 size_t tab_bytes(const AdapterPlan& p) { return up256((size_t)p.tiles * 16); }
 size_t h_bytes(const AdapterPlan& p, int32_t r) { return up256((size_t)p.ks * p.tiles * p.rt * r * 4); }
+size_t dh_bytes(const AdapterPlan& p, int32_t r) { return up256((size_t)p.kd * p.tiles * p.rt * r * 4); }
 size_t parts_bytes(const AdapterPlan& p, int32_t r) { return up256((size_t)p.tiles * p.rt * r * 6); }
-size_t rows_bytes(const AdapterPlan& p, int32_t r) { return p.rt == 64 ? parts_bytes(p, r) : 0; }
-size_t forward_bytes(const AdapterPlan& p, int32_t r) { return tab_bytes(p) + h_bytes(p, r) + rows_bytes(p, r); }
+size_t forward_bytes(const AdapterPlan& p, int32_t r) {
+  return tab_bytes(p) + h_bytes(p, r) + (p.rt == 64 ? parts_bytes(p, r) : 0);
+}
 size_t backward_bytes(const AdapterPlan& p, int32_t r) {
-  return tab_bytes(p) + 2 * (h_bytes(p, r) + parts_bytes(p, r)) + rows_bytes(p, r);
+  return tab_bytes(p) + h_bytes(p, r) + dh_bytes(p, r) + 3 * parts_bytes(p, r) + (p.slices > 1 ? p.slices * p.part * 4 : 0);
 }
 
 }  // namespace
@@ -128,11 +130,13 @@ ffn_status ffn_adapter_backward(const void* x, const void* a, const void* b, con
   d.tab = static_cast<int4*>(workspace);
   char* at = static_cast<char*>(workspace) + tab_bytes(d.p);
   if (with_h) d.h = reinterpret_cast<float*>(at);
-  if (with_dh) d.dh = reinterpret_cast<float*>(at + h_bytes(d.p, r));
-  at += 2 * h_bytes(d.p, r);
+  at += h_bytes(d.p, r);
+  if (with_dh) d.dh = reinterpret_cast<float*>(at);
+  at += dh_bytes(d.p, r);
   if (db) d.ht = reinterpret_cast<uint16_t*>(at);
   if (da) d.dht = reinterpret_cast<uint16_t*>(at + parts_bytes(d.p, r));
   if (dx) d.dhp = reinterpret_cast<uint16_t*>(at + 2 * parts_bytes(d.p, r));
+  if (d.p.slices > 1) d.part = reinterpret_cast<float*>(at + 3 * parts_bytes(d.p, r));
   hipError_t e = launch_adapter_down(d, st(stream));
   if (e == hipSuccess && dx) e = launch_adapter_up(d, true, st(stream));
   if (e == hipSuccess && (da || db)) e = launch_adapter_dw(d, st(stream));

@@ -128,7 +128,7 @@ __device__ __forceinline__ void remainder8(float (&f)[8], const uint4 hi) {
 // are added in order. ALONG: the weights' rows run along the contraction (A). Otherwise across it (B, rows of r
 // elements): a step's 64 rows go through the wave's own part of LDS, which the transposing read turns: in each 16 lanes,
 // lane 4 v + u points at row 8 q + 4 h + v, elements 4 u .. + 3, and lane j receives element j % 4 of lane 4 v + j / 4.
-constexpr int kDownRanks = 128;                  // of a workgroup
+constexpr int kDownRanks = 64, kDown64Ranks = 128;               // of a workgroup, with tiles of 16 and of 64 rows
 template <int RT, int RB>
 struct DownLds {
   static constexpr int PART = kDownWaves * RT * 16 * 4;          // bytes of the waves' sums of 16 ranks
@@ -153,15 +153,16 @@ __device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile,
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int i = 0; i < MB; ++i) acc[b][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int steps = (K + 63) / 64, s0 = (int)((long long)steps * z / d.p.ks), s1 = (int)((long long)steps * (z + 1) / d.p.ks);
+  const int ks = ALONG ? d.p.ks : d.p.kd;         // slices
+  const int steps = (K + 63) / 64, s0 = (int)((long long)steps * z / ks), s1 = (int)((long long)steps * (z + 1) / ks);
   uint4 uv[2][MB][2], wv[2][RB * 2];
   int brow[RB * 2], bcol[RB * 2];                // this lane's chunks of eight elements of a step of B
   if constexpr (!ALONG) {
 #pragma unroll
     for (int n = 0; n < RB * 2; ++n) {
       const int c = n * 64 + lane;
-      brow[n] = d.r <= kDownRanks ? c * 8 / lw : c >> 4;
-      bcol[n] = d.r <= kDownRanks ? c * 8 - brow[n] * lw : (c & 15) * 8;
+      brow[n] = d.r <= kDownRanks ? c * 8 / lw : c >> 3;
+      bcol[n] = d.r <= kDownRanks ? c * 8 - brow[n] * lw : (c & 7) * 8;
     }
   }
   auto load = [&](auto slot, int at) {
@@ -245,8 +246,6 @@ __device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile,
   // the waves' sums, a block of 16 ranks at a time
   float* s_part = reinterpret_cast<float*>(lds);
   float* out = (ALONG ? d.h : d.dh) + ((size_t)z * d.p.tiles + t) * RT * d.r;
-  uint16_t* turned = ALONG ? d.ht : d.dht;
-  const float scale = d.scales ? d.scales[tile.x] : 1.f;
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     __syncthreads();
@@ -262,15 +261,6 @@ __device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile,
       if (tile.y + row >= tile.z || row_at(d, tile.y + row) < 0) v = 0.f;
       if (j >= d.r) continue;
       out[(size_t)row * d.r + j] = v;
-      if (turned) {                              // for the adapters' gradients: s h in three bf16 numbers, rows along
-        v *= scale;
-#pragma unroll
-        for (int n = 0; n < 3; ++n) {
-          const uint32_t part = pack_bf16(v, 0.f) & 0xFFFFu;
-          turned[(((size_t)t * 3 + n) * d.r + j) * RT + row] = (uint16_t)part;
-          v = fabsf(bf2f(part)) == __builtin_huge_valf() ? 0.f : v - bf2f(part);
-        }
-      }
     }
   }
 }
@@ -285,7 +275,7 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down(const AdapterD
   const bool back = (int)blockIdx.z >= chunks || !with_h;
   const int j0 = (blockIdx.z % chunks) * kDownRanks;
   if (z == 0 && blockIdx.z == 0 && threadIdx.x == 0) d.tab[t] = tile;
-  if (tile.x < 0) return;
+  if (tile.x < 0 || z >= (back ? d.p.kd : d.p.ks)) return;
   if (!back) down_tile<RT, RB, true>(d, tile, t, z, j0, lds);
   else down_tile<RT, RB, false>(d, tile, t, z, j0, lds);
 }
@@ -325,8 +315,9 @@ __device__ __forceinline__ void down64_tile(const AdapterDesc& d, const int4 til
   const uint16_t* u = ALONG ? d.x : d.dy;
   const int K = ALONG ? d.k : d.n;
   const int rw = min(d.r - j0, 16 * RB);         // ranks here
-  const int lw = d.r <= kDownRanks ? d.r : kDownRanks;           // row of B in LDS
-  const int steps = (K + kStep - 1) / kStep, s0 = (int)((long long)steps * z / d.p.ks), n = (int)((long long)steps * (z + 1) / d.p.ks) - s0;
+  const int lw = d.r <= kDown64Ranks ? d.r : kDown64Ranks;           // row of B in LDS
+  const int ks = ALONG ? d.p.ks : d.p.kd;         // slices
+  const int steps = (K + kStep - 1) / kStep, s0 = (int)((long long)steps * z / ks), n = (int)((long long)steps * (z + 1) / ks) - s0;
   // where this lane's loads come from: four rows of the tile for each, chunk (lane % 16) ^ row of them
   const uint16_t* xp[L::XL];
   int xk[L::XL];
@@ -346,7 +337,7 @@ __device__ __forceinline__ void down64_tile(const AdapterDesc& d, const int4 til
       wk[i] = ((c & 15) ^ (row & 15)) * 8;
       wp[i] = d.a + ((size_t)tile.x * d.r + j0 + min(row, rw - 1)) * K + wk[i];
     } else {
-      const int row = d.r <= kDownRanks ? c * 8 / lw : c >> 4, col = d.r <= kDownRanks ? c * 8 - row * lw : (c & 15) * 8;
+      const int row = d.r <= kDown64Ranks ? c * 8 / lw : c >> 4, col = d.r <= kDown64Ranks ? c * 8 - row * lw : (c & 15) * 8;
       wk[i] = min(row, kStep - 1);               // chunks past the step's rows: not read
       wp[i] = d.b + ((size_t)tile.x * K + wk[i]) * d.r + j0 + min(col, rw - 8);
     }
@@ -436,9 +427,9 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down64(const Adapte
   const int t = tile.w;
   if (t >= d.p.tiles) return;
   const bool back = (int)blockIdx.z >= chunks || !with_h;
-  const int j0 = (blockIdx.z % chunks) * kDownRanks;
+  const int j0 = (blockIdx.z % chunks) * kDown64Ranks;
   if (z == 0 && blockIdx.z == 0 && threadIdx.x == 0) d.tab[t] = tile;
-  if (tile.x < 0) return;
+  if (tile.x < 0 || z >= (back ? d.p.kd : d.p.ks)) return;
   if (!back) down64_tile<RB, true>(d, tile, t, z, j0, lds);
   else down64_tile<RB, false>(d, tile, t, z, j0, lds);
 }
@@ -461,19 +452,20 @@ __device__ __forceinline__ void sum_rows(const AdapterDesc& d, const float* h, s
     for (int e = 0; e < 4; ++e) f[i][e] = v[i][0][e] * scale;
   }
 }
+template <int RT>
 __global__ __launch_bounds__(64) void k_adapter_sum(const AdapterDesc d, int with_h) {
   const int t = blockIdx.x, which = !with_h || blockIdx.z, r4 = d.r >> 2;
   const int e = blockIdx.y * 64 + threadIdx.x, r0 = e / r4 * 4, j = (e - e / r4 * r4) * 4;
   const int g = d.tab[t].x;
-  if (g < 0 || r0 >= 64) return;
-  const size_t at = (size_t)t * 64 * d.r;
+  if (g < 0 || r0 >= RT) return;
+  const size_t at = (size_t)t * RT * d.r;
   const float* h = (which ? d.dh : d.h) + at + (size_t)r0 * d.r + j;
   uint16_t* rows = which ? d.dhp : d.hp;
   uint16_t* turned = which ? d.dht : d.ht;
-  const size_t slab = (size_t)d.p.tiles * 64 * d.r;
+  const size_t slab = (size_t)d.p.tiles * RT * d.r;
   const float scale = d.scales ? d.scales[g] : 1.f;
   float f[4][4];
-  switch (d.p.ks) {
+  switch (which ? d.p.kd : d.p.ks) {
     case 1: sum_rows<1>(d, h, slab, f, scale); break;
     case 2: sum_rows<2>(d, h, slab, f, scale); break;
     case 4: sum_rows<4>(d, h, slab, f, scale); break;
@@ -486,13 +478,13 @@ __global__ __launch_bounds__(64) void k_adapter_sum(const AdapterDesc d, int wit
     for (int i = 0; i < 4; ++i) {
       p[i][0] = pack_bf16(f[i][0], f[i][1]);
       p[i][1] = pack_bf16(f[i][2], f[i][3]);
-      if (rows && (n < 2 || d.out_f32)) *reinterpret_cast<uint2*>(rows + 3 * at + ((size_t)n * 64 + r0 + i) * d.r + j) = uint2{p[i][0], p[i][1]};
+      if (rows && (n < 2 || d.out_f32)) *reinterpret_cast<uint2*>(rows + 3 * at + ((size_t)n * RT + r0 + i) * d.r + j) = uint2{p[i][0], p[i][1]};
     }
     if (turned) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t sel = k & 1 ? 0x07060302u : 0x05040100u;
-        *reinterpret_cast<uint2*>(turned + 3 * at + ((size_t)n * d.r + j + k) * 64 + r0) =
+        *reinterpret_cast<uint2*>(turned + 3 * at + ((size_t)n * d.r + j + k) * RT + r0) =
             uint2{__builtin_amdgcn_perm(p[1][k >> 1], p[0][k >> 1], sel), __builtin_amdgcn_perm(p[3][k >> 1], p[2][k >> 1], sel)};
       }
     }
@@ -507,22 +499,24 @@ __global__ __launch_bounds__(64) void k_adapter_sum(const AdapterDesc d, int wit
 }
 
 hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s) {
-  const int with_h = d.h != nullptr, with_dh = d.dh != nullptr, chunks = (d.r + kDownRanks - 1) / kDownRanks;
-  const dim3 grid((d.p.tiles + 7) / 8 * 8, d.p.ks, (with_h + with_dh) * chunks), block(kDownWaves * 64);
+  const int with_h = d.h != nullptr, with_dh = d.dh != nullptr, ranks = d.p.rt == 16 ? kDownRanks : kDown64Ranks;
+  const int chunks = (d.r + ranks - 1) / ranks, ks = d.p.ks > d.p.kd ? d.p.ks : d.p.kd;
+  const dim3 grid((d.p.tiles + 7) / 8 * 8, ks, (with_h + with_dh) * chunks), block(kDownWaves * 64);
   if (d.p.rt == 16) {
     if (d.r <= 16) ffn_launch((k_adapter_down<16, 1>), grid, block, 0, s, d, with_h, chunks);
     else if (d.r <= 32) ffn_launch((k_adapter_down<16, 2>), grid, block, 0, s, d, with_h, chunks);
-    else if (d.r <= 64) ffn_launch((k_adapter_down<16, 4>), grid, block, 0, s, d, with_h, chunks);
-    else ffn_launch((k_adapter_down<16, 8>), grid, block, 0, s, d, with_h, chunks);
-    return hipGetLastError();
+    else ffn_launch((k_adapter_down<16, 4>), grid, block, 0, s, d, with_h, chunks);
+  } else {
+    if (d.r <= 16) ffn_launch((k_adapter_down64<1>), grid, block, 0, s, d, with_h, chunks);
+    else if (d.r <= 32) ffn_launch((k_adapter_down64<2>), grid, block, 0, s, d, with_h, chunks);
+    else if (d.r <= 64) ffn_launch((k_adapter_down64<4>), grid, block, 0, s, d, with_h, chunks);
+    else ffn_launch((k_adapter_down64<8>), grid, block, 0, s, d, with_h, chunks);
   }
-  if (d.r <= 16) ffn_launch((k_adapter_down64<1>), grid, block, 0, s, d, with_h, chunks);
-  else if (d.r <= 32) ffn_launch((k_adapter_down64<2>), grid, block, 0, s, d, with_h, chunks);
-  else if (d.r <= 64) ffn_launch((k_adapter_down64<4>), grid, block, 0, s, d, with_h, chunks);
-  else ffn_launch((k_adapter_down64<8>), grid, block, 0, s, d, with_h, chunks);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  ffn_launch(k_adapter_sum, dim3(d.p.tiles, (d.r * 4 + 63) / 64, with_h + with_dh), dim3(64), 0, s, d, with_h);
+  // forward with tiles of 16 rows, the second product adds the slices as it reads them: a launch less
+  if (e != hipSuccess || (d.p.rt == 16 && !with_dh && !d.ht)) return e;
+  if (d.p.rt == 16) ffn_launch(k_adapter_sum<16>, dim3(d.p.tiles, (d.r + 63) / 64, with_h + with_dh), dim3(64), 0, s, d, with_h);
+  else ffn_launch(k_adapter_sum<64>, dim3(d.p.tiles, (d.r * 4 + 63) / 64, with_h + with_dh), dim3(64), 0, s, d, with_h);
   return hipGetLastError();
 }
 
@@ -575,7 +569,7 @@ __global__ __launch_bounds__(256, F == 0 ? (RT == 16 ? 4 : 3) : F == 1 ? 3 : 2) 
     }
     return;
   }
-  constexpr bool READY = RT == 64;               // s h is there in bf16 numbers; otherwise it is made of the slices here
+  constexpr bool READY = RT == 64 || !ALONG;     // s h is there in bf16 numbers; otherwise it is made of the slices here
   constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
   const float* hsrc = (ALONG ? d.h : d.dh) + (size_t)t * RT * d.r;
   const uint16_t* hrow = (ALONG ? d.hp : d.dhp) + (size_t)t * 3 * RT * d.r;
@@ -771,13 +765,18 @@ hipError_t launch_adapter_up(const AdapterDesc& d, bool back, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- gradients of the adapters
-// dA[j][c] = sum over the adapter's rows t of s dh[t][j] x[t][c], and dB[c][j] = sum of s h[t][j] dy[t][c]: a workgroup
-// has 128 columns c of one adapter and up to 16 RB ranks; its waves take 32 rows in turn, whose 8 x 8 pieces are turned
-// in registers, the next ones under way, and their sums are added in order. s h enters as three bf16 numbers.
-template <int RT, int RB, int WAVES, bool OF_A>
-__device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int c0, int j0, float* s_part) {
-  const int lane = lane_id(), wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
-  const int cols = OF_A ? d.k : d.n;
+// dA[j][c] = sum over the adapter's rows t of s dh[t][j] x[t][c], and dB[c][j] = sum of s h[t][j] dy[t][c]. A wave has 128
+// columns c of one adapter and up to 16 RB ranks, and takes 32 rows at a time: whose 8 x 8 pieces are turned in registers,
+// the next ones under way; s h enters as three bf16 numbers. A workgroup's four waves are `split` waves for each of its 4 /
+// split column blocks, which take the steps of 32 rows in turn and whose sums are added in order (waves of different
+// columns share the reads of s h, 1.5 times as many bytes as x with 64 ranks). Where that leaves the chip empty, the rows
+// are cut into slices besides, whose sums k_adapter_dw_sum adds.
+constexpr int kDwWaves = 4;
+template <int RT, int RB, bool OF_A>
+__device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int block, int j0, int slice, float* s_part) {
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
+  const int split = d.p.split, colw = kDwWaves / split, cw = wave % colw, rw = wave / colw;
+  const int cols = OF_A ? d.k : d.n, c0 = (block * colw + cw) * 128;
   const uint16_t* u = OF_A ? d.x : d.dy;
   // the adapter's places and its first tile
   const Groups s = groups_of(d);
@@ -793,6 +792,8 @@ __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int c0, int
   const int owner = g / s.per;
   const int before = wave_read(wave_incl_scan(mine) - mine, owner) + wave_read(tiles, owner);
   const int lo = wave_read(start, owner), rows = wave_read(stop, owner) - lo;
+  const bool whole = d.p.slices == 1;
+  if (rows == 0 && whole && d.accumulate) return;
   const uint16_t* h = (OF_A ? d.dht : d.ht) + (size_t)before * 3 * d.r * RT;
   f32x4_t acc[8][RB];
 #pragma unroll
@@ -803,112 +804,141 @@ __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int c0, int
   int at[8];
   uint4 in[8];
   // the rows of step r0 (clamped: what lies behind the last is cleared before it is used)
-  auto find = [&](int r0) {
+  auto load = [&](int r0) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) at[e] = row_at(d, lo + min(r0 + q * 8 + e, rows - 1));
-  };
-  auto load = [&] {
 #pragma unroll
     for (int e = 0; e < 8; ++e) in[e] = ldg16(u + (size_t)max(at[e], 0) * cols + cb);
   };
-  int r0 = wave * 32;
-  if (r0 < rows) {
-    find(r0);
-    load();
-    for (; r0 < rows; r0 += WAVES * 32) {
+  const int steps = (rows + 31) / 32, last = (int)((long long)steps * (slice + 1) / d.p.slices) * 32;
+  int r0 = ((int)((long long)steps * slice / d.p.slices) + rw) * 32;
+  if (r0 < last && c0 < cols) {
+    load(r0);
+    for (; r0 < last; r0 += split * 32) {
       // places and rows past the adapter's: zeros
       uint4 uv[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) in[e] = keep_if(at[e] >= 0 && r0 + q * 8 + e < rows, in[e]);
       transpose8(in, uv);
-      const int next = min(r0 + WAVES * 32, rows - 1);
-      find(next);
-      load();
-      __builtin_amdgcn_sched_barrier(0);
       const int first = r0 + q * 8, tile = min(first, rows - 1) / RT;
       const uint16_t* hp = h + ((size_t)tile * 3 * d.r) * RT + (first & (RT - 1));
       const bool has = first < rows;             // a tile of 16 rows may be the last
+      uint4 hv[RB > 1 ? 2 : 1][3];               // of two blocks of 16 ranks at a time
+      auto ranks = [&](int b) {
+#pragma unroll
+        for (int part = 0; part < 3; ++part) hv[b & 1][part] = ldg16(hp + ((size_t)part * d.r + min(j0 + b * 16 + l16, d.r - 1)) * RT);
+      };
+      ranks(0);
+      if constexpr (RB > 1) ranks(1);
+      if constexpr (RB <= 2) load(min(r0 + split * 32, rows - 1));
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
-        const int j = min(j0 + b * 16 + l16, d.r - 1);
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
-          const uint4 hv = keep_if(has, ldg16(hp + ((size_t)part * d.r + j) * RT));
+          const bf16x8_t hb = as_bf16x8(keep_if(has, hv[b & 1][part]));
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if constexpr (OF_A) acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(uv[i]), as_bf16x8(hv), acc[i][b], 0, 0, 0);
-            else acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(hv), as_bf16x8(uv[i]), acc[i][b], 0, 0, 0);
+            if constexpr (OF_A) acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(uv[i]), hb, acc[i][b], 0, 0, 0);
+            else acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hb, as_bf16x8(uv[i]), acc[i][b], 0, 0, 0);
           }
+        }
+        if (b + 2 < RB) {
+          __builtin_amdgcn_sched_barrier(0);
+          ranks(b + 2);
+          if (b + 3 == RB) load(min(r0 + split * 32, rows - 1));
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
   }
-  // the waves' sums, 16 ranks of the 128 columns at a time: s_part[wave][accumulator][lane] in fours
-  auto part = [&](int w, int i, int l) { return s_part + ((w * 8 + i) * 64 + l) * 4; };
+  // the waves' sums, 16 ranks of the 128 columns at a time: part(wave, accumulator, lane) in fours
+  float* to = OF_A ? d.da : d.db;
+  if (!whole) to = d.part + (size_t)slice * d.p.part + (OF_A || !d.da ? 0 : (size_t)d.groups * d.r * d.k);
+  const bool add = whole && d.accumulate;
+  auto part = [&](int w, int i, int l) { return s_part + (((w * colw + cw) * 8 + i) * 64 + l) * 4; };
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     if (b) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<f32x4_t*>(part(wave, i, lane)) = acc[i][b];
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<f32x4_t*>(part(rw, i, lane)) = acc[i][b];
     __syncthreads();
     if constexpr (OF_A) {
       // eight neighbouring columns of a rank a thread: those of blk = 4 q + v are value v of lane q * 16 + j's accumulators
-      for (int n = threadIdx.x; n < 256; n += WAVES * 64) {
+      for (int n = rw * 64 + lane; n < 256; n += split * 64) {
         const int blk = n & 15, j = j0 + b * 16 + (n >> 4), l = (blk >> 2) * 16 + (n >> 4), c = c0 + 8 * blk;
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f[i] = 0.f;
+        for (int i = 0; i < 8; ++i) f[i] = part(0, i, l)[blk & 3];
+        for (int w = 1; w < split; ++w)
 #pragma unroll
-          for (int w = 0; w < WAVES; ++w) f[i] += part(w, i, l)[blk & 3];
-        }
+          for (int i = 0; i < 8; ++i) f[i] += part(w, i, l)[blk & 3];
         if (j >= d.r || c >= cols) continue;
-        float* out = d.da + ((size_t)g * d.r + j) * cols + c;
+        float* out = to + ((size_t)g * d.r + j) * cols + c;
+        if (add) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += d.accumulate ? out[i] : 0.f;
+          for (int i = 0; i < 8; ++i) f[i] += out[i];
+        }
         Row8<float>::store(out, 0, f);
       }
     } else {
       // four neighbouring ranks of a column a thread: lane q * 16 + p of accumulator i has column 8 p + i
-      for (int n = threadIdx.x; n < 512; n += WAVES * 64) {
+      for (int n = rw * 64 + lane; n < 512; n += split * 64) {
         const int lq = n & 3, col = n >> 2, p = col >> 3;
         const int j = j0 + b * 16 + 4 * lq, c = c0 + col;
-        f32x4_t f = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) f += *reinterpret_cast<const f32x4_t*>(part(w, col & 7, lq * 16 + p));
+        f32x4_t f = *reinterpret_cast<const f32x4_t*>(part(0, col & 7, lq * 16 + p));
+        for (int w = 1; w < split; ++w) f += *reinterpret_cast<const f32x4_t*>(part(w, col & 7, lq * 16 + p));
         if (j >= d.r || c >= cols) continue;
-        f32x4_t* out = reinterpret_cast<f32x4_t*>(d.db + ((size_t)g * cols + c) * d.r + j);
-        if (d.accumulate) f += *out;
+        f32x4_t* out = reinterpret_cast<f32x4_t*>(to + ((size_t)g * cols + c) * d.r + j);
+        if (add) f += *out;
         *out = f;
       }
     }
   }
 }
 
-template <int RT, int RB, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void k_adapter_dw(const AdapterDesc d, int cols_a) {
-  __shared__ __attribute__((aligned(16))) float s_part[WAVES * 8 * 64 * 4];
-  const int j0 = blockIdx.z * (16 * RB);
-  if ((int)blockIdx.x < cols_a) dw_tile<RT, RB, WAVES, true>(d, blockIdx.y, blockIdx.x * 128, j0, s_part);
-  else dw_tile<RT, RB, WAVES, false>(d, blockIdx.y, (blockIdx.x - cols_a) * 128, j0, s_part);
+// blocks_a: workgroups of A's columns, B's behind them
+template <int RT, int RB>
+__global__ __launch_bounds__(kDwWaves * 64) void k_adapter_dw(const AdapterDesc d, int blocks_a) {
+  __shared__ __attribute__((aligned(16))) float s_part[kDwWaves * 8 * 64 * 4];
+  const int slice = blockIdx.z % d.p.slices, j0 = blockIdx.z / d.p.slices * (16 * RB);
+  if ((int)blockIdx.x < blocks_a) dw_tile<RT, RB, true>(d, blockIdx.y, blockIdx.x, j0, slice, s_part);
+  else dw_tile<RT, RB, false>(d, blockIdx.y, blockIdx.x - blocks_a, j0, slice, s_part);
+}
+// The slices' sums, to da (na values) and db (nb behind them), four values a thread.
+__global__ __launch_bounds__(256) void k_adapter_dw_sum(const AdapterDesc d, size_t na, size_t nb) {
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < na + nb; i += (size_t)gridDim.x * 1024) {
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(d.part + i);
+    for (int z = 1; z < d.p.slices; ++z) v += *reinterpret_cast<const f32x4_t*>(d.part + z * d.p.part + i);
+    f32x4_t* out = reinterpret_cast<f32x4_t*>(i < na ? d.da + i : d.db + (i - na));
+    if (d.accumulate) v += *out;
+    *out = v;
+  }
 }
 
 template <int RT, int RB>
-static hipError_t dw_ranks(const AdapterDesc& d, hipStream_t s) {
-  const int ca = d.da ? (d.k + 127) / 128 : 0, cb = d.db ? (d.n + 127) / 128 : 0;
-  const dim3 grid(ca + cb, d.groups, (d.r + 16 * RB - 1) / (16 * RB));
-  // eight waves where four would leave the chip half empty
-  if ((long long)grid.x * grid.y * grid.z >= 512) ffn_launch((k_adapter_dw<RT, RB, 4>), grid, dim3(256), 0, s, d, ca);
-  else ffn_launch((k_adapter_dw<RT, RB, 8>), grid, dim3(512), 0, s, d, ca);
-  return hipGetLastError();
+static void dw_ranks(const AdapterDesc& d, hipStream_t s) {
+  const int w = 128 * kDwWaves / d.p.split;      // columns of a workgroup
+  const int ba = d.da ? (d.k + w - 1) / w : 0, bb = d.db ? (d.n + w - 1) / w : 0;
+  const dim3 grid(ba + bb, d.groups, (d.r + 16 * RB - 1) / (16 * RB) * d.p.slices);
+  ffn_launch((k_adapter_dw<RT, RB>), grid, dim3(kDwWaves * 64), 0, s, d, ba);
 }
 template <int RT>
-static hipError_t dw(const AdapterDesc& d, hipStream_t s) {
-  if (d.r <= 16) return dw_ranks<RT, 1>(d, s);
-  if (d.r <= 32) return dw_ranks<RT, 2>(d, s);
-  return dw_ranks<RT, 4>(d, s);
+static void dw(const AdapterDesc& d, hipStream_t s) {
+  if (d.r <= 16) dw_ranks<RT, 1>(d, s);
+  else if (d.r <= 32) dw_ranks<RT, 2>(d, s);
+  else dw_ranks<RT, 4>(d, s);
 }
-hipError_t launch_adapter_dw(const AdapterDesc& d, hipStream_t s) { return d.p.rt == 16 ? dw<16>(d, s) : dw<64>(d, s); }
+hipError_t launch_adapter_dw(const AdapterDesc& d, hipStream_t s) {
+  if (d.p.rt == 16) dw<16>(d, s);
+  else dw<64>(d, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || d.p.slices == 1) return e;
+  const size_t na = d.da ? (size_t)d.groups * d.r * d.k : 0, nb = d.db ? (size_t)d.groups * d.r * d.n : 0;
+  const size_t blocks = (na + nb + 1023) / 1024;
+  ffn_launch(k_adapter_dw_sum, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, d, na, nb);
+  return hipGetLastError();
+}
 
 // ---------------------------------------------------------------- plan
 AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) {
@@ -918,14 +948,24 @@ AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) 
   // every adapter's last tile may be short, and so may the two runs of rows without one
   const long long tiles = (long long)m / p.rt + groups + 2;
   p.tiles = (int)(tiles < m ? tiles : m);
-  // slices: enough workgroups for the chip
+  // slices of the first products: enough workgroups for the chip
   const int live = (m + p.rt - 1) / p.rt;
-  const int least = p.rt == 64 ? 4 : kDownWaves;  // steps of a slice
-  const int steps = (backward ? (n > k ? n : k) : k) / (p.rt == 64 ? kStep : 64);
-  int ks = 1;
-  if (p.rt == 64 || !backward)
+  auto slices = [&](int width) {
+    const int steps = width / (p.rt == 64 ? kStep : 64), least = p.rt == 64 ? 4 : kDownWaves;
+    int ks = 1;
     while (ks < 8 && live * ks < 256 && steps / (ks * 2) >= least) ks *= 2;
-  p.ks = ks;
+    return ks;
+  };
+  p.ks = slices(k);
+  p.kd = backward ? slices(n) : 1;
+  // waves of the adapters' gradients: two for each SIMD, if there are steps of 32 rows for as many
+  const int steps = (m / groups + 31) / 32;
+  const long long waves = ((long long)(n + 127) / 128 + (k + 127) / 128) * groups * ((r + 63) / 64);
+  p.split = 1;
+  while (p.split < kDwWaves && waves * p.split < 2048 && p.split * 2 <= steps) p.split *= 2;
+  p.slices = 1;
+  while (p.split == kDwWaves && p.slices < 16 && waves * p.split * p.slices < 1024 && p.slices * p.split * 4 <= steps) p.slices *= 2;
+  p.part = (size_t)groups * r * ((size_t)n + k);
   return p;
 }
 
