@@ -300,11 +300,11 @@ __device__ __forceinline__ void lds_sync() {
 template <int RB>
 struct Down64 {
   static constexpr int X = 64 * kStepBytes, W = 16 * RB * kStepBytes, STAGE = X + W;
-  static constexpr int STAGES = RB == 1 ? 4 : RB == 2 ? 3 : RB == 4 ? 2 : 3;    // two workgroups (one with 128 ranks) on a CU's 160 KB
+  static constexpr int STAGES = RB == 8 ? 3 : 4;
   static constexpr int XL = X / 1024 / kDownWaves;                             // loads of a step of each wave
   static constexpr int WL = (W / 1024 + kDownWaves - 1) / kDownWaves;          // loads of the weights, of the waves that have any
   static constexpr int BYTES = STAGES * STAGE;
-  static_assert(BYTES >= 4 * RB * 64 * 16 && (RB == 8 ? 1 : 2) * BYTES <= 160 * 1024, "the second halves' sums, LDS of a CU");
+  static_assert(BYTES >= 4 * RB * 64 * 16 && BYTES <= 160 * 1024, "the second halves' sums, LDS of a CU");
 };
 template <int RB, bool ALONG>
 __device__ __forceinline__ void down64_tile(const AdapterDesc& d, const int4 tile, int t, int z, int j0, char* lds) {
@@ -409,13 +409,42 @@ __device__ __forceinline__ void down64_tile(const AdapterDesc& d, const int4 til
   if (wh) return;
   const int row = wi * 16 + l16;
   const bool live = tile.y + row < tile.z && row_at(d, min(tile.y + row, tile.z - 1)) >= 0;
-  float* out = (ALONG ? d.h : d.dh) + (((size_t)z * d.p.tiles + t) * RT + row) * d.r;
+  if (ks > 1) {                                  // a slice of the sum
+    float* out = (ALONG ? d.h : d.dh) + (((size_t)z * d.p.tiles + t) * RT + row) * d.r;
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const int j = j0 + b * 16 + q * 4;
+      f32x4_t v = acc[b] + s_half[b * 64];
+      if (!live) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (j < d.r) *reinterpret_cast<f32x4_t*>(out + j) = v;
+    }
+    return;
+  }
+  // the whole of it: what k_adapter_sum makes of slices
+  const float scale = d.scales ? d.scales[tile.x] : 1.f;
+  uint16_t* rows = (ALONG ? d.hp : d.dhp);
+  uint16_t* turned = ALONG ? d.ht : d.dht;
+  const size_t at = (size_t)t * 3 * RT * d.r;
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     const int j = j0 + b * 16 + q * 4;
-    f32x4_t v = acc[b] + s_half[b * 64];
-    if (!live) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (j < d.r) *reinterpret_cast<f32x4_t*>(out + j) = v;
+    const f32x4_t v = acc[b] + s_half[b * 64];
+    float f[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = live ? v[k] * scale : 0.f;
+    if (j >= d.r) continue;
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      const uint32_t p[2] = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+      if (rows && (n < 2 || d.out_f32)) *reinterpret_cast<uint2*>(rows + at + ((size_t)n * RT + row) * d.r + j) = uint2{p[0], p[1]};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t one = k & 1 ? p[k >> 1] >> 16 : p[k >> 1] & 0xFFFFu;
+        if (turned) turned[at + ((size_t)n * d.r + j + k) * RT + row] = (uint16_t)one;
+        const float g = bf2f(one);
+        f[k] = fabsf(g) == __builtin_huge_valf() ? 0.f : f[k] - g;
+      }
+    }
   }
 }
 
@@ -457,7 +486,7 @@ __global__ __launch_bounds__(64) void k_adapter_sum(const AdapterDesc d, int wit
   const int t = blockIdx.x, which = !with_h || blockIdx.z, r4 = d.r >> 2;
   const int e = blockIdx.y * 64 + threadIdx.x, r0 = e / r4 * 4, j = (e - e / r4 * r4) * 4;
   const int g = d.tab[t].x;
-  if (g < 0 || r0 >= RT) return;
+  if (g < 0 || r0 >= RT || (RT == 64 && (which ? d.p.kd : d.p.ks) == 1)) return;
   const size_t at = (size_t)t * RT * d.r;
   const float* h = (which ? d.dh : d.h) + at + (size_t)r0 * d.r + j;
   uint16_t* rows = which ? d.dhp : d.hp;
@@ -515,6 +544,8 @@ hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   // forward with tiles of 16 rows, the second product adds the slices as it reads them: a launch less
   if (e != hipSuccess || (d.p.rt == 16 && !with_dh && !d.ht)) return e;
+  // and with tiles of 64 rows a product that is not sliced is finished by its own kernel
+  if (d.p.rt == 64 && (!with_h || d.p.ks == 1) && (!with_dh || d.p.kd == 1)) return e;
   if (d.p.rt == 16) ffn_launch(k_adapter_sum<16>, dim3(d.p.tiles, (d.r + 63) / 64, with_h + with_dh), dim3(64), 0, s, d, with_h);
   else ffn_launch(k_adapter_sum<64>, dim3(d.p.tiles, (d.r * 4 + 63) / 64, with_h + with_dh), dim3(64), 0, s, d, with_h);
   return hipGetLastError();
@@ -541,16 +572,31 @@ __device__ __forceinline__ void transpose8(const uint4 (&in)[8], uint4 (&out)[8]
 
 // out = base + s h W^T for a tile: a wave has 128 columns, accumulator e of lane l column 8 (l % 16) + e of row 4 (l / 16) + v
 // in its value v, so that a lane reads and writes eight neighbours and 16 lanes 256 bytes of a row. (With the lanes' rows
-// and columns exchanged, 16 bytes a row from each of 16 lanes, 8192 x 4096 x 14336 took 160 us.) F: groups of 32 ranks (0: up to 16, hi and lo in one group).
-// ALONG: W = B, rows of r elements a column; otherwise W = A^T, rows of the output's columns.
+// and columns exchanged, 16 bytes a row from each of 16 lanes, 8192 x 4096 x 14336 took 160 us.) ALONG: W = B, rows of r
+// elements a column; otherwise W = A^T, rows of the output's columns. F: groups of 32 ranks (0: up to 16, hi and lo in one
+// group).
+// READY: s h is there in bf16 numbers, which the four waves share through LDS (rows of an odd number of 16-byte chunks: no
+// bank conflicts); otherwise each wave makes them of the slices, for its one tile of 16 rows.
+template <typename T, int RT, int F, bool ALONG>
+struct Up {
+  static constexpr bool READY = RT == 64 || !ALONG;
+  static constexpr int NF = F == 0 ? 1 : F;
+  static constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
+  static constexpr int PIECES = F == 0 ? 2 : 4;  // 16-byte chunks of a column's ranks in a group
+  static constexpr bool STAY = NF <= 2;          // weights of up to 64 ranks stay in registers for all of the tile's rows
+  static constexpr int MB = RT == 64 && !STAY ? 2 : 1;           // 16 rows each, for a group's weights
+  static constexpr int AHEAD = RT == 16 && NF > 1 ? (NF < 4 ? NF : 4) : 1;     // groups whose loads are under way
+  static constexpr int W = ALONG ? 128 * PIECES * 16 + 256 : 0;  // LDS of a wave's weights
+  static constexpr int H = READY ? PARTS * RT * ((F == 0 ? 2 : NF * 4) + 1) * 16 : 0;
+};
 template <typename T, int RT, int F, bool ALONG>
 __global__ __launch_bounds__(256, F == 0 ? (RT == 16 ? 4 : 3) : F == 1 ? 3 : 2) void k_adapter_up(const AdapterDesc d) {
-  constexpr int NF = F == 0 ? 1 : F;
-  __shared__ __attribute__((aligned(16))) char s_w[ALONG ? 4 * (128 * (F == 0 ? 2 : 4) * 16 + 256) : 16];
+  using U = Up<T, RT, F, ALONG>;
+  constexpr int NF = U::NF, PARTS = U::PARTS, PIECES = U::PIECES, MB = U::MB, AHEAD = U::AHEAD;
+  __shared__ __attribute__((aligned(16))) char s_mem[4 * U::W + U::H + 16];
   const int lane = lane_id(), wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
   const int cols = ALONG ? d.n : d.k;
   const int c0 = (blockIdx.x * 4 + wave) * 128;
-  if (c0 >= cols) return;
   const int t = blockIdx.y + blockIdx.z * gridDim.y;
   if (t >= d.p.tiles) return;
   const int4 tile = d.tab[t];
@@ -569,179 +615,186 @@ __global__ __launch_bounds__(256, F == 0 ? (RT == 16 ? 4 : 3) : F == 1 ? 3 : 2) 
     }
     return;
   }
-  constexpr bool READY = RT == 64 || !ALONG;     // s h is there in bf16 numbers; otherwise it is made of the slices here
-  constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
-  const float* hsrc = (ALONG ? d.h : d.dh) + (size_t)t * RT * d.r;
-  const uint16_t* hrow = (ALONG ? d.hp : d.dhp) + (size_t)t * 3 * RT * d.r;
-  const size_t slab = (size_t)d.p.tiles * RT * d.r;
-  const float scale = d.scales ? d.scales[tile.x] : 1.f;
   const uint16_t* w = ALONG ? d.b + (size_t)tile.x * d.n * d.r : d.a + (size_t)tile.x * d.r * d.k;
   const int jq = F == 0 ? (q & 1) * 8 : q * 8;   // this lane's first rank in a group
   const int wc = c0 + 8 * l16;                   // this lane's eight columns
   // lane l has the row of place l of the tile
   const int mine = row_at(d, min(tile.y + min(lane, RT - 1), tile.z - 1)), rows = tile.z - tile.y;
-  // The weights of up to 64 ranks stay in registers for all of the tile's rows. B's come through the wave's own part of
-  // LDS: neighbouring lanes load neighbouring chunks of a column's ranks (`pieces` of them in a group), 16 bytes of
-  // padding every eight columns keep the operands' reads, eight columns apart, out of each other's banks.
-  constexpr bool STAY = NF <= 2;
-  constexpr int PIECES = F == 0 ? 2 : 4;
-  uint4 wv[STAY ? NF : 1][8], raw[ALONG ? 2 * PIECES : 8];
-  char* lds = s_w + wave * (ALONG ? 128 * PIECES * 16 + 256 : 0);
+
+  // ---------------------------------------------------------------- weights
+  // B's come through the wave's own part of LDS: neighbouring lanes load neighbouring chunks of a column's ranks, and 16
+  // bytes of padding every eight columns keep the operands' reads, eight columns apart, out of each other's banks.
+  uint4 wv[U::STAY ? NF : 1][8], raw[AHEAD][ALONG ? 2 * PIECES : 8];
+  char* lds = s_mem + U::H + wave * U::W;
   auto chunk = [&](int n, int& col, int& piece) {
     const int c = n * 64 + lane;
     col = c / PIECES;
     piece = c % PIECES;
   };
   auto ask = [&](int g) {
+    uint4(&to)[ALONG ? 2 * PIECES : 8] = raw[g % AHEAD];
     if constexpr (ALONG) {
 #pragma unroll
       for (int n = 0; n < 2 * PIECES; ++n) {
         int col, piece;
         chunk(n, col, piece);
-        raw[n] = ldg16(w + (size_t)min(c0 + col, cols - 1) * d.r + min(g * 32 + piece * 8, d.r - 8));
+        to[n] = ldg16(w + (size_t)min(c0 + col, cols - 1) * d.r + min(g * 32 + piece * 8, d.r - 8));
       }
     } else {
       const int jc = min(g * 32 + jq, d.r - 8);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) raw[e] = ldg16(w + (size_t)(jc + e) * cols + min(wc, cols - 8));
+      for (int e = 0; e < 8; ++e) to[e] = ldg16(w + (size_t)(jc + e) * cols + min(wc, cols - 8));
     }
   };
   auto weights = [&](int g) {
-    uint4(&o)[8] = wv[STAY ? g : 0];
+    uint4(&o)[8] = wv[U::STAY ? g : 0];
+    uint4(&got)[ALONG ? 2 * PIECES : 8] = raw[g % AHEAD];
     if constexpr (ALONG) {
 #pragma unroll
       for (int n = 0; n < 2 * PIECES; ++n) {
         int col, piece;
         chunk(n, col, piece);
-        *reinterpret_cast<uint4*>(lds + (col * PIECES + piece + (col >> 3)) * 16) = raw[n];
+        *reinterpret_cast<uint4*>(lds + (col * PIECES + piece + (col >> 3)) * 16) = got[n];
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = *reinterpret_cast<const uint4*>(lds + ((8 * l16 + e) * PIECES + (jq >> 3) + l16) * 16);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = keep_if(g * 32 + jq < d.r, o[e]);
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = raw[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = keep_if(g * 32 + jq < d.r, o[e]);
-    if constexpr (!ALONG) {
       uint4 in[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) in[e] = o[e];
+      for (int e = 0; e < 8; ++e) in[e] = keep_if(g * 32 + jq < d.r, got[e]);
       transpose8(in, o);
     }
   };
-  // without a base, every row is the same eight zeros
+  // ---------------------------------------------------------------- s h
+  const int r8 = d.r >> 3, hpitch = (r8 | 1) * 16;
+  uint4 made[NF][PARTS];                         // not READY: of the tile's 16 rows
+  auto part_of = [&](int i0, int g, int n) {     // F = 0: hi for q < 2 and lo for the others in part 0; then the third
+    uint4 v;
+    if constexpr (U::READY) {
+      const int which = F == 0 && n == 0 ? q >> 1 : n;
+      v = *reinterpret_cast<const uint4*>(s_mem + (which * RT + min(i0 + l16, RT - 1)) * hpitch + min(g * 32 + jq, d.r - 8) * 2);
+    } else {
+      v = made[g][n];
+    }
+    return as_bf16x8(keep_if(g * 32 + jq < d.r && (F != 0 || n == 0 || q < 2), v));
+  };
+  // ---------------------------------------------------------------- base
+  // without one, every row is the same eight zeros
   const void* from = d.base ? d.base : adapter_zero;
   const size_t pitch = d.base ? cols : 0;
   const int at = d.base ? min(wc, cols - 8) : 0;
-  int row[4];
-  Row8<T> base[4];
-  uint4 hv[NF][PARTS];                         // F = 0: hi for q < 2, lo for the others, in the first; then the third
+  int row[MB][4];
+  Row8<T> base[MB][4];
   auto fetch = [&](int i0) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      row[v] = __shfl(mine, min(i0 + 4 * q + v, rows - 1), 64);
-      base[v].load(from, (size_t)max(row[v], 0) * pitch + at);
-    }
-    if constexpr (READY) {
-      const uint16_t* p = hrow + (size_t)min(i0 + l16, RT - 1) * d.r;
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int g = 0; g < NF; ++g)
-#pragma unroll
-        for (int n = 0; n < PARTS; ++n) {
-          if (F == 0 && n == 1) continue;
-          hv[g][n] = ldg16(p + (size_t)(F == 0 && n == 0 ? q >> 1 : n) * RT * d.r + min(g * 32 + jq, d.r - 8));
-        }
-    }
+      for (int v = 0; v < 4; ++v) {
+        row[i][v] = __shfl(mine, min(i0 + i * 16 + 4 * q + v, rows - 1), 64);
+        base[i][v].load(from, (size_t)max(row[i][v], 0) * pitch + at);
+      }
   };
-  ask(0);
+
+#pragma unroll
+  for (int g = 0; g < AHEAD; ++g) ask(g);
   fetch(0);
   __builtin_amdgcn_sched_barrier(0);
-  if constexpr (STAY) {
+  if constexpr (U::READY) {
+    const uint16_t* hrow = (ALONG ? d.hp : d.dhp) + (size_t)t * 3 * RT * d.r;
+    for (int c = threadIdx.x; c < PARTS * RT * r8; c += 256) {
+      const int line = c / r8;
+      *reinterpret_cast<uint4*>(s_mem + line * hpitch + (c - line * r8) * 16) = ldg16(hrow + (size_t)c * 8);
+    }
+    __syncthreads();
+  } else {
+    const float* hp = (ALONG ? d.h : d.dh) + ((size_t)t * RT + l16) * d.r;
+    const size_t slab = (size_t)d.p.tiles * RT * d.r;
+    const float scale = d.scales ? d.scales[tile.x] : 1.f;
+    f32x4_t ha[NF][2];
+#pragma unroll
+    for (int g = 0; g < NF; ++g) ha[g][0] = ha[g][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int z = 0; z < d.p.ks; ++z) {
+#pragma unroll
+      for (int g = 0; g < NF; ++g) {
+        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(hp + z * slab + min(g * 32 + jq, d.r - 8));
+        ha[g][0] += p[0];
+        ha[g][1] += p[1];
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < NF; ++g) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = ha[g][e >> 2][e & 3] * scale;
+      const uint4 hi = pack8(f);
+      remainder8(f, hi);
+      const uint4 lo = pack8(f);
+      made[g][0] = hi;
+      made[g][1] = lo;
+      if constexpr (F == 0) made[g][0] = q < 2 ? hi : lo;
+      if constexpr (PARTS == 3) {
+        remainder8(f, lo);
+        made[g][2] = pack8(f);
+      }
+    }
+  }
+  if (c0 >= cols) return;
+  if constexpr (U::STAY) {
     weights(0);
     if constexpr (NF > 1) {
-      ask(1);
+      if constexpr (AHEAD == 1) ask(1);
       weights(1);
     }
   }
 #pragma unroll 1
-  for (int i0 = 0; i0 < rows; i0 += 16) {
-    if constexpr (!READY) {
-      f32x4_t ha[NF][2];
-      const float* hp = hsrc + (size_t)(i0 + l16) * d.r;
+  for (int i0 = 0; i0 < rows; i0 += 16 * MB) {
+    f32x4_t acc[MB][8];                          // the sums start from the base
+    int to[MB][4];
 #pragma unroll
-      for (int g = 0; g < NF; ++g) ha[g][0] = ha[g][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (int z = 0; z < d.p.ks; ++z) {
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int g = 0; g < NF; ++g) {
-          const f32x4_t* p = reinterpret_cast<const f32x4_t*>(hp + z * slab + min(g * 32 + jq, d.r - 8));
-          ha[g][0] += p[0];
-          ha[g][1] += p[1];
-        }
-      }
-#pragma unroll
-      for (int g = 0; g < NF; ++g) {
+      for (int v = 0; v < 4; ++v) {
         float f[8];
+        base[i][v].get(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = ha[g][e >> 2][e & 3] * scale;
-        const uint4 hi = pack8(f);
-        remainder8(f, hi);
-        const uint4 lo = pack8(f);
-        hv[g][0] = hi;
-        hv[g][1] = lo;
-        if constexpr (F == 0) hv[g][0] = q < 2 ? hi : lo;
-        if constexpr (PARTS == 3) {
-          remainder8(f, lo);
-          hv[g][2] = pack8(f);
-        }
-      }
-    }
-    f32x4_t acc[8];                            // the sums start from the base
-    int to[4];
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      float f[8];
-      base[v].get(f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e][v] = f[e];
-      to[v] = i0 + 4 * q + v < rows ? row[v] : -1;
-    }
-    uint4 now[NF][PARTS];
-#pragma unroll
-    for (int g = 0; g < NF; ++g)
-#pragma unroll
-      for (int n = 0; n < PARTS; ++n) {
-        if (F == 0 && n == 1) continue;
-        now[g][n] = keep_if(g * 32 + jq < d.r && (F != 0 || n == 0 || q < 2), hv[g][n]);
+        for (int e = 0; e < 8; ++e) acc[i][e][v] = f[e];
+        to[i][v] = i0 + i * 16 + 4 * q + v < rows ? row[i][v] : -1;
       }
     // the next rows' (past the last: the last row's again), ahead of this one's stores, which a wait for loads behind
     // them would be a wait for
-    if (RT > 16) fetch(i0 + 16);
+    if (RT > 16) fetch(i0 + 16 * MB);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int g = 0; g < NF; ++g) {
-      if constexpr (!STAY) {
-        ask(g);
+      if constexpr (!U::STAY) {
         weights(g);
+        if (g + AHEAD < NF || RT > 16) ask((g + AHEAD) % NF);
       }
-      const uint4(&o)[8] = wv[STAY ? g : 0];
+      const uint4(&o)[8] = wv[U::STAY ? g : 0];
 #pragma unroll
-      for (int n = 0; n < PARTS; ++n) {
-        if (F == 0 && n == 1) continue;
+      for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(now[g][n]), as_bf16x8(o[e]), acc[e], 0, 0, 0);
-      }
+        for (int n = 0; n < PARTS; ++n) {
+          if (F == 0 && n == 1) continue;
+          const bf16x8_t h = part_of(i0 + i * 16, g, n);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[i][e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, as_bf16x8(o[e]), acc[i][e], 0, 0, 0);
+        }
     }
     if (wc >= cols) continue;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (to[v] < 0) continue;
-      float f[8];
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = acc[e][v];
-      Row8<T>::store(d.out, (size_t)to[v] * cols + wc, f);
-    }
+      for (int v = 0; v < 4; ++v) {
+        if (to[i][v] < 0) continue;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = acc[i][e][v];
+        Row8<T>::store(d.out, (size_t)to[i][v] * cols + wc, f);
+      }
   }
 }
 
@@ -953,7 +1006,9 @@ AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) 
   auto slices = [&](int width) {
     const int steps = width / (p.rt == 64 ? kStep : 64), least = p.rt == 64 ? 4 : kDownWaves;
     int ks = 1;
-    while (ks < 8 && live * ks < 256 && steps / (ks * 2) >= least) ks *= 2;
+    // (backward, slices of both products besides that are about as long as each other)
+    while (ks < 8 && steps / (ks * 2) >= least &&
+           (live * ks < (p.rt == 64 ? 128 : 256) || (backward && p.rt == 64 && steps / ks > 32))) ks *= 2;
     return ks;
   };
   p.ks = slices(k);
