@@ -79,7 +79,11 @@ def check_forward(asg, s, base, out):
 SHAPES = [(1, 72, 136, 8, 1), (1, 520, 264, 16, 5), (3, 136, 72, 24, 2), (17, 264, 520, 16, 3), (48, 1032, 2056, 16, 33),
           (16, 8, 8, 8, 2), (130, 136, 264, 40, 7), (33, 2056, 1032, 64, 70), (257, 520, 136, 72, 4), (70, 264, 328, 136, 3),
           (40, 136, 264, 256, 2), (1024, 264, 200, 32, 5), (1030, 392, 264, 16, 9), (2100, 200, 136, 64, 300), (1500, 136, 72, 8, 1024),
-          (1111, 72, 136, 128, 3), (1033, 136, 200, 200, 6), (5, 200, 4104, 16, 4)]
+          (1111, 72, 136, 128, 3), (1033, 136, 200, 200, 6), (5, 200, 4104, 16, 4),
+          # contractions in slices, rows in slices, both
+          (700, 264, 2056, 16, 3), (1030, 1048, 1032, 64, 4), (600, 136, 4104, 128, 2), (520, 2056, 264, 200, 3), (4200, 264, 136, 16, 1),
+          (2600, 136, 72, 64, 1), (3000, 72, 72, 136, 1), (8500, 72, 136, 24, 5), (2056, 1160, 1096, 32, 1), (90, 1032, 1544, 72, 3),
+          (17, 4104, 136, 128, 2)]
 
 
 @pytest.mark.parametrize("kind", ["rows", "ordered"])
@@ -180,6 +184,27 @@ def test_bad_numbers_stay_in_their_rows(asg):
     dx0, da0, db0 = asg.adapter_backward(s["x"], s["a"], s["b"], s["dy"], dev(s["offsets"]), **call(s))
     assert torch.equal(dx, dx0) and torch.equal(da[3], da0[3]) and torch.equal(db[3], db0[3])
     assert not da[1].any() and not db[1].any() and bool(torch.isnan(da[0]).all())
+
+
+def test_rows_past_2_to_the_31_elements(asg):
+    say("adapter large")
+    torch = torch_()
+    m, n, k, r = 140_000, 16384, 16448, 8               # 2.3e9 elements of x, y and dy
+    x = torch.randn(m, k, device="cuda", dtype=torch.bfloat16)
+    a, b = (torch.randn(1, *shape, device="cuda", dtype=torch.bfloat16) / 16 for shape in ((r, k), (n, r)))
+    off = torch.tensor([3, m - 5], dtype=torch.int32, device="cuda")
+    y = asg.adapter_forward(x, a, b, off)
+    at = [0, 2, 3, 70_001, m - 70, m - 6, m - 5, m - 1]
+    want = E.adapter(f64(x[at]), f64(a), f64(b), None, [2, 6], None, None)
+    size = E.adapter(np.abs(f64(x[at])), np.abs(f64(a)), np.abs(f64(b)), None, [2, 6], None, None)
+    near(f64(y[at]), want, ((k / 8 + 80 + 3 * r + 101) * 2 * U + B ** 2) * size + B * np.abs(want) * (1 + 1e-3), "y")
+    dx, da, _ = asg.adapter_backward(x, a, b, y, off, need_db=False)
+    y[3:m - 5] = 0                                      # one row of gradient alone: its outer product
+    y[m - 70] = 1.0
+    _, da, _ = asg.adapter_backward(x, a, b, y, off, need_dx=False, need_db=False)
+    want = E.adapter_backward(f64(x[m - 70:m - 69]), f64(a), f64(b), None, f64(y[m - 70:m - 69]), [0, 1], None, None)[1]
+    size = np.abs(f64(b)).sum(1)[:, :, None] * np.abs(f64(x[m - 70]))
+    near(f64(da), want, (n / 8 + m / 8 + 200) * 2 * U * size + 1e-30, "da")
 
 
 def test_same_from_run_to_run(asg):

@@ -126,6 +126,25 @@ def test_route(asg, form, dtype):
         check_route(asg, g.normal(0, 2, (m, experts)), dtype, top_k, kw, bias)
 
 
+# more tokens than a wave each would take: 16 lanes a token
+MANY = [(1100, 256, 8, 8, 4), (1030, 128, 6, 16, 5), (1060, 100, 4, 10, 3), (1027, 250, 16, 2, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("form", range(len(FORMS)))
+def test_route_many_tokens(asg, form, dtype):
+    for i, (m, experts, top_k, groups, top_groups) in enumerate(MANY):
+        say("route many", FORMS[form], dtype, m, experts, top_k)
+        g = rng(9, form, i)
+        kw, bias = settings(FORMS[form], m, experts, top_k, groups, top_groups, g)
+        l = g.normal(0, 2, (m, experts))
+        l[g.random((m, experts)) < 0.1] = -np.inf
+        l[5] = 1.0                                      # equal values: the lowest indices
+        l[6] = -np.inf
+        l[7] = np.round(l[7])
+        check_route(asg, l, dtype, top_k, kw, bias)
+
+
 @pytest.mark.parametrize("form", range(len(FORMS)))
 def test_route_masked_logits(asg, form):
     # experts that may not be chosen, tokens with fewer of them than slots, one without any
@@ -155,15 +174,23 @@ def test_route_ties_go_to_the_lower_index(asg, sigmoid, biased):
             check_route(asg, l, "f32", top_k, dict(sigmoid=sigmoid), bias)
 
 
-def test_route_close_values_are_told_apart(asg):
+@pytest.mark.parametrize("m", [33, 1040])
+@pytest.mark.parametrize("experts", [64, 256])
+def test_route_close_values_are_told_apart(asg, m, experts):
     # scores that are equal in fp32 and not in fp64: logits one fp32 step apart at 9 differ by 1e-10 in their sigmoids
-    say("route close")
-    l = np.float32(9.0) + np.arange(64, dtype=np.float32) * np.float32(2.0 ** -20)
-    g = rng(4)
-    l = np.stack([g.permutation(l) for _ in range(33)])
-    check_route(asg, l, "f32", 8, dict(sigmoid=True), np.zeros(64, np.float32))
-    check_route(asg, l, "f32", 8, dict(sigmoid=True, groups=8, top_groups=2, group_best=2), None)
-    check_route(asg, l, "f32", 8, dict(groups=8, top_groups=2, group_best=2), np.zeros(64, np.float32))
+    say("route close", m, experts)
+    l = np.float32(9.0) + np.arange(experts, dtype=np.float32) * np.float32(2.0 ** -20)
+    g = rng(4, m, experts)
+    l = np.stack([g.permutation(l) for _ in range(m)])
+    # and a few such among ordinary ones
+    l[1::2] = np.where(g.random(l[1::2].shape) < 0.05, l[1::2], g.normal(0, 2, l[1::2].shape))
+    zero = np.zeros(experts, np.float32)
+    for kw in (dict(sigmoid=True), dict()):
+        check_route(asg, l, "f32", 8, kw, zero)
+        check_route(asg, l, "f32", 16, kw, None)
+        for best in (1, 2):
+            check_route(asg, l, "f32", 8, dict(kw, groups=8, top_groups=2, group_best=best), None)
+            check_route(asg, l, "f32", 8, dict(kw, groups=8, top_groups=2, group_best=best), zero)
 
 
 def test_route_far_logits(asg):
@@ -195,6 +222,24 @@ def test_route_bad_numbers(asg):
                 assert ids[1, 0] == 5 and ids[3, 0] == 2 and ids[2, 0] == 7 and np.isnan(w[[1, 3]]).all() and np.isfinite(w[2]).all()
 
 
+def route_backward_slack(l, ids, dw, ds, *, sigmoid=False, renormalize=True, scale=1.0):
+    """What the module's bounds allow: of the sizes of all products that make up a logit's gradient."""
+    p = E.scores(l, sigmoid)
+    G = np.abs(np.zeros(l.shape) if ds is None else ds).astype(np.float64)
+    part = np.zeros(l.shape)
+    for r in range(len(l)):
+        live = ids[r] >= 0
+        e, d = ids[r][live], np.abs(dw[r][live]).astype(np.float64)
+        if renormalize:
+            w = E.weights(l[r, e], p[r, e], sigmoid, True)
+            np.add.at(part[r], e, scale * w * (d + np.sum(d * w)))
+        else:
+            np.add.at(G[r], e, scale * d)
+    size = part + p * G + (0 if sigmoid else p * np.sum(p * G, 1, keepdims=True))
+    big = np.abs(np.where(np.isfinite(l), l, 0)).max(1, keepdims=True)
+    return (4 * big + 104) * 2 * U * size
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("renormalize", [False, True])
@@ -212,20 +257,8 @@ def test_route_backward(asg, dtype, sigmoid, renormalize):
             got = asg.route_backward(t, dev(ids), dev(dw), dscores=None if ds is None else dev(ds), **args(kw))
             assert got.dtype == t.dtype
             want = E.route_backward(f64(t), ids, dw, ds, **kw)
-            p = E.scores(f64(t), sigmoid)
-            live = ids >= 0
-            G = np.abs(np.zeros((m, experts)) if ds is None else ds).astype(np.float64)
-            part = np.zeros((m, experts))
-            for r in range(m):
-                e, d = ids[r][live[r]], np.abs(dw[r][live[r]]).astype(np.float64)
-                if renormalize:
-                    w = E.weights(f64(t)[r, e], p[r, e], sigmoid, True)
-                    np.add.at(part[r], e, 2.5 * w * (d + np.sum(d * w)))
-                else:
-                    np.add.at(G[r], e, 2.5 * d)
-            size = part + p * G + (0 if sigmoid else p * np.sum(p * G, 1, keepdims=True))
-            big = np.abs(np.where(np.isfinite(f64(t)), f64(t), 0)).max(1, keepdims=True)
-            near(f64(got), want, (4 * big + 104) * 2 * U * size + half(dtype) * np.abs(want) * (1 + 1e-4) + TINY, "dlogits")
+            slack = route_backward_slack(f64(t), ids, dw, ds, **kw)
+            near(f64(got), want, slack + half(dtype) * np.abs(want) * (1 + 1e-4) + TINY, "dlogits")
 
 
 def test_route_backward_slots_without_experts_and_in_place(asg):
