@@ -12,10 +12,19 @@ a step.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
-from .linear import _DTYPES, _accumulator, _call, _check, _fail, _first, _nbytes, _on_stream, _product_out, _ptr, _workspace
+from .linear import (_DTYPES, _accumulator, _again, _call, _check, _fail, _first, _nbytes, _product_out, _ptr,
+                     _workspace)
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes(name, *shape):
+    """A workspace's size, which the shape alone decides (the C call takes 0.6 us)."""
+    return getattr(_lib.load(), name)(*shape)
 
 
 def _shapes(x, a, b):
@@ -38,9 +47,8 @@ def _order(offsets, rows, groups, m, dev):
         _check("rows", rows, torch.int32, (m,), dev)
 
 
-@_on_stream
 def adapter_forward(x, a, b, offsets, *, rows=None, scales=None, base=None, y=None, out_dtype=torch.bfloat16,
-                    workspace=None):
+                    workspace=None, stream=None):
     """y[t] = base[t] + scales[g] B_g A_g x[t] for the rows t of each adapter g,
     base[t] for rows without one (ffn_adapter_forward).
 
@@ -48,6 +56,8 @@ def adapter_forward(x, a, b, offsets, *, rows=None, scales=None, base=None, y=No
     [adapters] or None (ones); base [m, n], the shared projection's output, or
     None (zeros). y [m, n] of base's type (out_dtype without a base: bf16 or
     fp32); it may be base, which is then added to in place."""
+    if stream is not None:
+        return _again(adapter_forward, locals())
     dev, m, k, groups, r, n = _shapes(x, a, b)
     _order(offsets, rows, groups, m, dev)
     if scales is not None:
@@ -62,16 +72,14 @@ def adapter_forward(x, a, b, offsets, *, rows=None, scales=None, base=None, y=No
             _check("y", y, out_dtype, (m, n), dev)
     else:
         y = _product_out(y, (m, n), out_dtype, dev)
-    lib = _lib.load()
-    workspace = _workspace(workspace, lib.ffn_adapter_forward_workspace_bytes(m, n, k, r, groups), dev)
-    _call(lib.ffn_adapter_forward, dev, _ptr(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(offsets), _ptr(rows), groups, m, n,
+    workspace = _workspace(workspace, _bytes("ffn_adapter_forward_workspace_bytes", m, n, k, r, groups), dev)
+    _call(_lib.load().ffn_adapter_forward, dev, _ptr(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(offsets), _ptr(rows), groups, m, n,
           k, r, _ptr(base), _ptr(y), _DTYPES[y.dtype], _ptr(workspace), _nbytes(workspace))
     return y
 
 
-@_on_stream
 def adapter_backward(x, a, b, dy, offsets, *, rows=None, scales=None, base=None, need_dx=True, need_da=True, need_db=True,
-                     dx=None, da=None, db=None, accumulate=False, workspace=None):
+                     dx=None, da=None, db=None, accumulate=False, workspace=None, stream=None):
     """Gradients of adapter_forward (ffn_adapter_backward): (dx, da, db); that of
     base is dy itself.
 
@@ -80,6 +88,8 @@ def adapter_backward(x, a, b, dy, offsets, *, rows=None, scales=None, base=None,
     [adapters, r, k] and db [adapters, n, r] fp32, written (zeros for an adapter
     without rows) or added to with accumulate. One that is not needed is not
     computed: None in its place."""
+    if stream is not None:
+        return _again(adapter_backward, locals())
     if not (need_dx or need_da or need_db):
         raise ValueError("need_dx, need_da, need_db: one of the gradients at least")
     for name, need, t in (("dx", need_dx, dx), ("base", need_dx, base), ("da", need_da, da), ("db", need_db, db)):
@@ -103,9 +113,8 @@ def adapter_backward(x, a, b, dy, offsets, *, rows=None, scales=None, base=None,
         da = _accumulator("da", da, accumulate, (groups, r, k), dev)
     if need_db:
         db = _accumulator("db", db, accumulate, (groups, n, r), dev)
-    lib = _lib.load()
-    workspace = _workspace(workspace, lib.ffn_adapter_backward_workspace_bytes(m, n, k, r, groups), dev)
-    _call(lib.ffn_adapter_backward, dev, _ptr(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(dy), _ptr(offsets), _ptr(rows),
+    workspace = _workspace(workspace, _bytes("ffn_adapter_backward_workspace_bytes", m, n, k, r, groups), dev)
+    _call(_lib.load().ffn_adapter_backward, dev, _ptr(x), _ptr(a), _ptr(b), _ptr(scales), _ptr(dy), _ptr(offsets), _ptr(rows),
           groups, m, n, k, r, _ptr(base), _ptr(dx), _ptr(da), _ptr(db), int(bool(accumulate)), _ptr(workspace),
           _nbytes(workspace))
     return dx, da, db

@@ -40,9 +40,9 @@ struct AdapterDesc {
 AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward);
 // first products: h (of x, if d.h) and dh (of dy, if d.dh), what is made of them, and the table of tiles
 hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s);
-// second product: out = base + scale h B^T, or with `back` base + scale dh A
-hipError_t launch_adapter_up(const AdapterDesc& d, bool back, hipStream_t s);
-// gradients of the adapters: da and db, those that are not null
-hipError_t launch_adapter_dw(const AdapterDesc& d, hipStream_t s);
+// forward: out = base + scale h B^T
+hipError_t launch_adapter_up(const AdapterDesc& d, hipStream_t s);
+// backward: out = base + scale dh A, and the gradients da and db; those that are not null
+hipError_t launch_adapter_back(const AdapterDesc& d, hipStream_t s);
 
 }  // namespace ffn

@@ -81,7 +81,7 @@ ffn_status ffn_adapter_forward(const void* x, const void* a, const void* b, cons
   d.hp = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(d.h) + h_bytes(d.p, r));
   const hipError_t e = launch_adapter_down(d, st(stream));
   if (e != hipSuccess) return FFN_E_HIP;
-  return done(launch_adapter_up(d, false, st(stream)));
+  return done(launch_adapter_up(d, st(stream)));
 }
 
 size_t ffn_adapter_backward_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t r, int32_t groups) {
@@ -137,10 +137,9 @@ ffn_status ffn_adapter_backward(const void* x, const void* a, const void* b, con
   if (da) d.dht = reinterpret_cast<uint16_t*>(at + parts_bytes(d.p, r));
   if (dx) d.dhp = reinterpret_cast<uint16_t*>(at + 2 * parts_bytes(d.p, r));
   if (d.p.slices > 1) d.part = reinterpret_cast<float*>(at + 3 * parts_bytes(d.p, r));
-  hipError_t e = launch_adapter_down(d, st(stream));
-  if (e == hipSuccess && dx) e = launch_adapter_up(d, true, st(stream));
-  if (e == hipSuccess && (da || db)) e = launch_adapter_dw(d, st(stream));
-  return done(e);
+  const hipError_t e = launch_adapter_down(d, st(stream));
+  if (e != hipSuccess) return FFN_E_HIP;
+  return done(launch_adapter_back(d, st(stream)));
 }
 
 }  // extern "C"

@@ -588,17 +588,16 @@ struct Up {
   static constexpr int AHEAD = RT == 16 && NF > 1 ? (NF < 4 ? NF : 4) : 1;     // groups whose loads are under way
   static constexpr int W = ALONG ? 128 * PIECES * 16 + 256 : 0;  // LDS of a wave's weights
   static constexpr int H = READY ? PARTS * RT * ((F == 0 ? 2 : NF * 4) + 1) * 16 : 0;
+  static constexpr int BYTES = 4 * W + H + 16;
 };
+// Columns c0 .. of the workgroup's four waves, 128 each, of tile t.
 template <typename T, int RT, int F, bool ALONG>
-__global__ __launch_bounds__(256, F == 0 ? (RT == 16 ? 4 : 3) : F == 1 ? 3 : 2) void k_adapter_up(const AdapterDesc d) {
+__device__ __forceinline__ void up_tile(const AdapterDesc& d, int block, int t, char* s_mem) {
   using U = Up<T, RT, F, ALONG>;
   constexpr int NF = U::NF, PARTS = U::PARTS, PIECES = U::PIECES, MB = U::MB, AHEAD = U::AHEAD;
-  __shared__ __attribute__((aligned(16))) char s_mem[4 * U::W + U::H + 16];
   const int lane = lane_id(), wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
   const int cols = ALONG ? d.n : d.k;
-  const int c0 = (blockIdx.x * 4 + wave) * 128;
-  const int t = blockIdx.y + blockIdx.z * gridDim.y;
-  if (t >= d.p.tiles) return;
+  const int c0 = (block * 4 + wave) * 128;
   const int4 tile = d.tab[t];
   if (tile.x == -2) return;
   if (tile.x == -1) {                            // no adapter: the base alone
@@ -709,7 +708,7 @@ __global__ __launch_bounds__(256, F == 0 ? (RT == 16 ? 4 : 3) : F == 1 ? 3 : 2) 
     }
     __syncthreads();
   } else {
-    const float* hp = (ALONG ? d.h : d.dh) + ((size_t)t * RT + l16) * d.r;
+    const float* hp = (ALONG ? d.h : d.dh) + ((size_t)t * RT + min(l16, rows - 1)) * d.r;     // rows past the last: its own again
     const size_t slab = (size_t)d.p.tiles * RT * d.r;
     const float scale = d.scales ? d.scales[tile.x] : 1.f;
     f32x4_t ha[NF][2];
@@ -798,23 +797,27 @@ __global__ __launch_bounds__(256, F == 0 ? (RT == 16 ? 4 : 3) : F == 1 ? 3 : 2) 
   }
 }
 
-template <typename T, int RT, bool ALONG>
+template <typename T, int RT, int F>
+__global__ __launch_bounds__(256, F == 0 ? (RT == 16 ? 4 : 3) : F == 1 ? 3 : 2) void k_adapter_up(const AdapterDesc d) {
+  __shared__ __attribute__((aligned(16))) char s_mem[Up<T, RT, F, true>::BYTES];
+  const int t = blockIdx.y + blockIdx.z * gridDim.y;
+  if (t < d.p.tiles) up_tile<T, RT, F, true>(d, blockIdx.x, t, s_mem);
+}
+template <typename T, int RT>
 static hipError_t up(const AdapterDesc& d, hipStream_t s) {
-  const int cols = ALONG ? d.n : d.k;
   // a grid's second dimension holds 65535 workgroups: tiles go on in the third
   const int ty = d.p.tiles < 32768 ? d.p.tiles : 32768;
-  const dim3 grid((cols + 511) / 512, ty, (d.p.tiles + ty - 1) / ty), block(256);
-  if (d.r <= 16) ffn_launch((k_adapter_up<T, RT, 0, ALONG>), grid, block, 0, s, d);
-  else if (d.r <= 32) ffn_launch((k_adapter_up<T, RT, 1, ALONG>), grid, block, 0, s, d);
-  else if (d.r <= 64) ffn_launch((k_adapter_up<T, RT, 2, ALONG>), grid, block, 0, s, d);
-  else if (d.r <= 128) ffn_launch((k_adapter_up<T, RT, 4, ALONG>), grid, block, 0, s, d);
-  else ffn_launch((k_adapter_up<T, RT, 8, ALONG>), grid, block, 0, s, d);
+  const dim3 grid((d.n + 511) / 512, ty, (d.p.tiles + ty - 1) / ty), block(256);
+  if (d.r <= 16) ffn_launch((k_adapter_up<T, RT, 0>), grid, block, 0, s, d);
+  else if (d.r <= 32) ffn_launch((k_adapter_up<T, RT, 1>), grid, block, 0, s, d);
+  else if (d.r <= 64) ffn_launch((k_adapter_up<T, RT, 2>), grid, block, 0, s, d);
+  else if (d.r <= 128) ffn_launch((k_adapter_up<T, RT, 4>), grid, block, 0, s, d);
+  else ffn_launch((k_adapter_up<T, RT, 8>), grid, block, 0, s, d);
   return hipGetLastError();
 }
-hipError_t launch_adapter_up(const AdapterDesc& d, bool back, hipStream_t s) {
-  if (back) return d.p.rt == 16 ? up<uint16_t, 16, false>(d, s) : up<uint16_t, 64, false>(d, s);
-  if (d.out_f32) return d.p.rt == 16 ? up<float, 16, true>(d, s) : up<float, 64, true>(d, s);
-  return d.p.rt == 16 ? up<uint16_t, 16, true>(d, s) : up<uint16_t, 64, true>(d, s);
+hipError_t launch_adapter_up(const AdapterDesc& d, hipStream_t s) {
+  if (d.out_f32) return d.p.rt == 16 ? up<float, 16>(d, s) : up<float, 64>(d, s);
+  return d.p.rt == 16 ? up<uint16_t, 16>(d, s) : up<uint16_t, 64>(d, s);
 }
 
 // ---------------------------------------------------------------- gradients of the adapters
@@ -950,13 +953,33 @@ __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int block, 
   }
 }
 
-// blocks_a: workgroups of A's columns, B's behind them
-template <int RT, int RB>
-__global__ __launch_bounds__(kDwWaves * 64) void k_adapter_dw(const AdapterDesc d, int blocks_a) {
-  __shared__ __attribute__((aligned(16))) float s_part[kDwWaves * 8 * 64 * 4];
-  const int slice = blockIdx.z % d.p.slices, j0 = blockIdx.z / d.p.slices * (16 * RB);
-  if ((int)blockIdx.x < blocks_a) dw_tile<RT, RB, true>(d, blockIdx.y, blockIdx.x, j0, slice, s_part);
-  else dw_tile<RT, RB, false>(d, blockIdx.y, blockIdx.x - blocks_a, j0, slice, s_part);
+// The second half of the backward pass, whose two parts read nothing of each other: workgroups of the adapters' gradients
+// (the longer ones), then those of dx. One launch lets the one's memory traffic fill the other's gaps.
+struct BackGrid {
+  int a, b;                      // column blocks of da and db
+  int groups, z;                 // z: rank blocks times slices
+  long long dw;                  // (a + b) groups z: workgroups of da and db
+  int x;                         // column blocks of dx
+};
+template <int RT, int F>
+__global__ __launch_bounds__(kDwWaves * 64, F == 0 ? 3 : 2) void k_adapter_back(const AdapterDesc d, const BackGrid grid) {
+  constexpr int RB = F == 0 ? 1 : F == 1 ? 2 : 4, PART = kDwWaves * 8 * 64 * 16;
+  using U = Up<uint16_t, RT, F, false>;
+  static_assert(kDwWaves * 64 == 256, "one size of workgroup");
+  __shared__ __attribute__((aligned(16))) char s_mem[PART > U::BYTES ? PART : U::BYTES];
+  const long long n = (long long)blockIdx.y * gridDim.x + blockIdx.x;
+  if (n < grid.dw) {
+    const int block = (int)(n % (grid.a + grid.b)), rest = (int)(n / (grid.a + grid.b));
+    const int g = rest % grid.groups, z = rest / grid.groups;
+    const int slice = z % d.p.slices, j0 = z / d.p.slices * (16 * RB);
+    float* s_part = reinterpret_cast<float*>(s_mem);
+    if (block < grid.a) dw_tile<RT, RB, true>(d, g, block, j0, slice, s_part);
+    else dw_tile<RT, RB, false>(d, g, block - grid.a, j0, slice, s_part);
+    return;
+  }
+  const long long at = n - grid.dw;
+  const int t = (int)(at / grid.x);
+  if (t < d.p.tiles) up_tile<uint16_t, RT, F, false>(d, (int)(at - (long long)t * grid.x), t, s_mem);
 }
 // The slices' sums, to da (na values) and db (nb behind them), four values a thread.
 __global__ __launch_bounds__(256) void k_adapter_dw_sum(const AdapterDesc d, size_t na, size_t nb) {
@@ -969,24 +992,34 @@ __global__ __launch_bounds__(256) void k_adapter_dw_sum(const AdapterDesc d, siz
   }
 }
 
-template <int RT, int RB>
-static void dw_ranks(const AdapterDesc& d, hipStream_t s) {
-  const int w = 128 * kDwWaves / d.p.split;      // columns of a workgroup
-  const int ba = d.da ? (d.k + w - 1) / w : 0, bb = d.db ? (d.n + w - 1) / w : 0;
-  const dim3 grid(ba + bb, d.groups, (d.r + 16 * RB - 1) / (16 * RB) * d.p.slices);
-  ffn_launch((k_adapter_dw<RT, RB>), grid, dim3(kDwWaves * 64), 0, s, d, ba);
+template <int RT, int F>
+static void back_ranks(const AdapterDesc& d, hipStream_t s) {
+  constexpr int RB = F == 0 ? 1 : F == 1 ? 2 : 4;
+  const int w = 128 * kDwWaves / d.p.split;      // columns of a workgroup of da and db
+  BackGrid b{};
+  b.a = d.da ? (d.k + w - 1) / w : 0;
+  b.b = d.db ? (d.n + w - 1) / w : 0;
+  b.groups = d.groups;
+  b.z = (d.r + 16 * RB - 1) / (16 * RB) * d.p.slices;
+  b.dw = (long long)(b.a + b.b) * b.groups * b.z;
+  b.x = (d.k + 511) / 512;
+  // a grid holds fewer than 2^32 threads a dimension
+  const long long all = b.dw + (d.out ? (long long)b.x * d.p.tiles : 0), y = (all + (1 << 23) - 1) >> 23;
+  ffn_launch((k_adapter_back<RT, F>), dim3((unsigned)((all + y - 1) / y), (unsigned)y), dim3(256), 0, s, d, b);
 }
 template <int RT>
-static void dw(const AdapterDesc& d, hipStream_t s) {
-  if (d.r <= 16) dw_ranks<RT, 1>(d, s);
-  else if (d.r <= 32) dw_ranks<RT, 2>(d, s);
-  else dw_ranks<RT, 4>(d, s);
+static void back(const AdapterDesc& d, hipStream_t s) {
+  if (d.r <= 16) back_ranks<RT, 0>(d, s);
+  else if (d.r <= 32) back_ranks<RT, 1>(d, s);
+  else if (d.r <= 64) back_ranks<RT, 2>(d, s);
+  else if (d.r <= 128) back_ranks<RT, 4>(d, s);
+  else back_ranks<RT, 8>(d, s);
 }
-hipError_t launch_adapter_dw(const AdapterDesc& d, hipStream_t s) {
-  if (d.p.rt == 16) dw<16>(d, s);
-  else dw<64>(d, s);
+hipError_t launch_adapter_back(const AdapterDesc& d, hipStream_t s) {
+  if (d.p.rt == 16) back<16>(d, s);
+  else back<64>(d, s);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || d.p.slices == 1) return e;
+  if (e != hipSuccess || d.p.slices == 1 || (!d.da && !d.db)) return e;
   const size_t na = d.da ? (size_t)d.groups * d.r * d.k : 0, nb = d.db ? (size_t)d.groups * d.r * d.n : 0;
   const size_t blocks = (na + nb + 1023) / 1024;
   ffn_launch(k_adapter_dw_sum, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, d, na, nb);

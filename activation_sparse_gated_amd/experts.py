@@ -17,7 +17,8 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .linear import _DTYPES, FP8, Fp8Tensor, _blocks, _call, _check, _check_fp8, _fail, _first, _nbytes, _on_stream, _ptr, _workspace
+from .linear import (_DTYPES, FP8, Fp8Tensor, _again, _blocks, _call, _check, _check_fp8, _fail, _first, _nbytes,
+                     _ptr, _workspace)
 
 _TYPES = (torch.bfloat16, torch.float32)
 
@@ -52,9 +53,8 @@ def _pairs(name, t, m, dev):
 
 
 # ---------------------------------------------------------------- router
-@_on_stream
 def route_forward(logits, top_k, *, score="softmax", bias=None, groups=1, top_groups=None, group_best=1,
-                  renormalize=True, scale=1.0, scores=False, weights=None, ids=None):
+                  renormalize=True, scale=1.0, scores=False, weights=None, ids=None, stream=None):
     """The choice of top_k experts for each token and their weights
     (ffn_route_forward): (weights, ids, scores).
 
@@ -66,6 +66,8 @@ def route_forward(logits, top_k, *, score="softmax", bias=None, groups=1, top_gr
     ties to the lower index; -1 (and weight 0) where no expert with a logit above
     -inf is left. scores: fp32 [m, experts], or None unless asked for (True, or
     the tensor that they are written to)."""
+    if stream is not None:
+        return _again(route_forward, locals())
     dev = _first("logits", logits, _TYPES, (2,))
     m, experts = logits.shape
     if top_k < 1:
@@ -84,13 +86,15 @@ def route_forward(logits, top_k, *, score="softmax", bias=None, groups=1, top_gr
     return weights, ids, scores
 
 
-@_on_stream
-def route_backward(logits, ids, dweights, *, dscores=None, score="softmax", renormalize=True, scale=1.0, dlogits=None):
+def route_backward(logits, ids, dweights, *, dscores=None, score="softmax", renormalize=True, scale=1.0, dlogits=None,
+                   stream=None):
     """Gradient of route_forward (ffn_route_backward): dlogits [m, experts] of the
     logits' type, the choice held fixed.
 
     ids [m, top_k] as route_forward gave them; dweights fp32 [m, top_k]; dscores
     fp32 [m, experts] or None. score, renormalize and scale as there."""
+    if stream is not None:
+        return _again(route_backward, locals())
     dev = _first("logits", logits, _TYPES, (2,))
     m, experts = logits.shape
     top_k = _pairs("ids", ids, m, dev)
@@ -104,8 +108,7 @@ def route_backward(logits, ids, dweights, *, dscores=None, score="softmax", reno
 
 
 # ---------------------------------------------------------------- rows to experts and back
-@_on_stream
-def group_rows(ids, groups, *, offsets=None, rows=None, slots=None, workspace=None):
+def group_rows(ids, groups, *, offsets=None, rows=None, slots=None, workspace=None, stream=None):
     """The order of entries by group (ffn_group_rows): (offsets, rows, slots).
 
     ids int32, [m, top_k] experts of route_forward or [m] adapters; what lies
@@ -113,6 +116,8 @@ def group_rows(ids, groups, *, offsets=None, rows=None, slots=None, workspace=No
     [groups + 1], as the products take them; rows int32 [m * top_k], the flat
     index into ids at each place; slots of ids' shape, the place of each entry
     (-1 without a group)."""
+    if stream is not None:
+        return _again(group_rows, locals())
     dev = _first("ids", ids, (torch.int32,), (1, 2))
     n = ids.numel()
     if groups < 1:
@@ -127,14 +132,15 @@ def group_rows(ids, groups, *, offsets=None, rows=None, slots=None, workspace=No
     return offsets, rows, slots
 
 
-@_on_stream
-def gather_forward(x, slots, *, fp8=False, y=None):
+def gather_forward(x, slots, *, fp8=False, y=None, stream=None):
     """y[slots[t, s]] = x[t] (ffn_gather_forward): the tokens' rows in the order of
     group_rows.
 
     x [m, d] bf16 or fp32; slots int32 [m, top_k], different places (-1: none). y
     [m * top_k, d] of x's type, or with fp8 an Fp8Tensor of blocks of 1 x 128;
     rows that no slot names are left as they were."""
+    if stream is not None:
+        return _again(gather_forward, locals())
     dev = _first("x", x, _TYPES, (2,))
     m, d = x.shape
     top_k = _pairs("slots", slots, m, dev)
@@ -154,21 +160,23 @@ def gather_forward(x, slots, *, fp8=False, y=None):
     return y
 
 
-@_on_stream
-def gather_backward(dy, slots, *, dx=None):
+def gather_backward(dy, slots, *, dx=None, stream=None):
     """Gradient of gather_forward: dx[t] = the sum over s of dy[slots[t, s]]
     (ffn_combine_forward without weights), [m, d] of dy's type."""
+    if stream is not None:
+        return _again(gather_backward, locals())
     return _combine(dy, slots, None, None, dx, "dy", "dx")
 
 
-@_on_stream
-def combine_forward(y, slots, weights=None, *, residual=None, out=None):
+def combine_forward(y, slots, weights=None, *, residual=None, out=None, stream=None):
     """out[t] = residual[t] + the sum over s of weights[t, s] y[slots[t, s]]
     (ffn_combine_forward).
 
     y [m * top_k, d] bf16 or fp32; slots int32 [m, top_k] of group_rows (-1: adds
     nothing); weights fp32 [m, top_k] or None (ones); residual [m, d] of y's type
     or None; out may be residual."""
+    if stream is not None:
+        return _again(combine_forward, locals())
     return _combine(y, slots, weights, residual, out, "y", "out")
 
 
@@ -188,8 +196,7 @@ def _combine(y, slots, weights, residual, out, y_name, out_name):
     return out
 
 
-@_on_stream
-def combine_backward(y, slots, weights, dout, *, need_dy=True, need_dweights=True, dy=None, dweights=None):
+def combine_backward(y, slots, weights, dout, *, need_dy=True, need_dweights=True, dy=None, dweights=None, stream=None):
     """Gradients of combine_forward (ffn_combine_backward): (dy, dweights); that of
     the residual is dout itself.
 
@@ -197,6 +204,8 @@ def combine_backward(y, slots, weights, dout, *, need_dy=True, need_dweights=Tru
     dout[t], rows that no slot names left as they were; it may be y. dweights fp32
     [m, top_k], 0 for a slot without a row. One that is not needed is not
     computed: None in its place. Without dweights, y may be None."""
+    if stream is not None:
+        return _again(combine_backward, locals())
     if not (need_dy or need_dweights):
         raise ValueError("need_dy, need_dweights: one of the gradients at least")
     if (not need_dy and dy is not None) or (not need_dweights and dweights is not None):

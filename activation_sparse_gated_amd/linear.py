@@ -108,6 +108,18 @@ def _on_stream(fn):
     return call
 
 
+def _again(fn, given):
+    """fn once more with the arguments of its own locals(), inside their `stream`: what _on_stream does, without a
+    function around every call (0.7 us each)."""
+    stream = given.pop("stream")
+    tensors = (a.q if isinstance(a, Fp8Tensor) else a for a in given.values())
+    device = next((t.device for t in tensors if isinstance(t, torch.Tensor)), None)
+    if device not in (None, stream.device):
+        raise ValueError(f"stream: of {stream.device}, the tensors are on {device}")
+    with torch.cuda.stream(stream):
+        return fn(**given)
+
+
 def _workspace(workspace, nbytes, device):
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
