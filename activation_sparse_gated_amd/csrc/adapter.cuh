@@ -14,6 +14,7 @@ struct AdapterPlan {
   int rt;                        // rows of a tile: 16 or 64
   int ks, kd;                    // slices of the contraction of x A^T and of dy B
   int tiles;                     // tiles at most, those of rows without an adapter among them
+  int few;                       // forward: 0, or both products in one launch, by so many workgroups a tile
   int split, slices;             // of an adapter's rows for its gradients: waves that share a column block, and slices besides
   size_t part;                   // values of a slice's gradients
 };
@@ -29,7 +30,7 @@ struct AdapterDesc {
   float *da, *db;
   int accumulate;
   AdapterPlan p;
-  // workspace
+  // workspace (none with p.few)
   int4* tab;                     // [tiles]: adapter (-1: none, -2: no tile), first place, end
   float *h, *dh;                 // [ks or kd][tiles][rt][r]: x A^T and dy B
   uint16_t *hp, *dhp;            // [tiles][3][rt][r]: s h (tiles of 64 rows) and s dh in bf16 numbers
@@ -38,11 +39,9 @@ struct AdapterDesc {
 };
 
 AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward);
-// first products: h (of x, if d.h) and dh (of dy, if d.dh), what is made of them, and the table of tiles
-hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s);
-// forward: out = base + scale h B^T
-hipError_t launch_adapter_up(const AdapterDesc& d, hipStream_t s);
-// backward: out = base + scale dh A, and the gradients da and db; those that are not null
-hipError_t launch_adapter_back(const AdapterDesc& d, hipStream_t s);
+// out = base + scale (x A^T) B^T
+hipError_t launch_adapter_forward(const AdapterDesc& d, hipStream_t s);
+// out = base + scale dh A, and the gradients da and db; those that are not null. d.dh is needed for out and da, d.h for db
+hipError_t launch_adapter_backward(const AdapterDesc& d, hipStream_t s);
 
 }  // namespace ffn

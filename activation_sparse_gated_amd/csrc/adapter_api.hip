@@ -32,7 +32,7 @@ size_t h_bytes(const AdapterPlan& p, int32_t r) { return up256((size_t)p.ks * p.
 size_t dh_bytes(const AdapterPlan& p, int32_t r) { return up256((size_t)p.kd * p.tiles * p.rt * r * 4); }
 size_t parts_bytes(const AdapterPlan& p, int32_t r) { return up256((size_t)p.tiles * p.rt * r * 6); }
 size_t forward_bytes(const AdapterPlan& p, int32_t r) {
-  return tab_bytes(p) + h_bytes(p, r) + (p.rt == 64 ? parts_bytes(p, r) : 0);
+  return p.few ? 0 : tab_bytes(p) + h_bytes(p, r) + (p.rt == 64 ? parts_bytes(p, r) : 0);
 }
 size_t backward_bytes(const AdapterPlan& p, int32_t r) {
   return tab_bytes(p) + h_bytes(p, r) + dh_bytes(p, r) + 3 * parts_bytes(p, r) + (p.slices > 1 ? p.slices * p.part * 4 : 0);
@@ -57,10 +57,11 @@ ffn_status ffn_adapter_forward(const void* x, const void* a, const void* b, cons
   if (!shape_ok(m, n, k, r, groups) || !dtype_ok(y_dtype)) return FFN_E_INVALID;
   if (m == 0) return FFN_OK;
   if (!need(x) || !need(a) || !need(b) || !opt(scales) || !need(offsets) || !opt(rows) || !opt(base) || !need(y) ||
-      !need(workspace))
+      !opt(workspace))
     return FFN_E_INVALID;
   AdapterDesc d{};
   d.p = adapter_plan(m, n, k, r, groups, false);
+  if (forward_bytes(d.p, r) && !workspace) return FFN_E_INVALID;
   if (workspace_bytes < forward_bytes(d.p, r)) return FFN_E_WORKSPACE;
   d.x = static_cast<const uint16_t*>(x);
   d.a = static_cast<const uint16_t*>(a);
@@ -76,12 +77,12 @@ ffn_status ffn_adapter_forward(const void* x, const void* a, const void* b, cons
   d.base = base;
   d.out = y;
   d.out_f32 = y_dtype == FFN_F32;
-  d.tab = static_cast<int4*>(workspace);
-  d.h = reinterpret_cast<float*>(static_cast<char*>(workspace) + tab_bytes(d.p));
-  d.hp = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(d.h) + h_bytes(d.p, r));
-  const hipError_t e = launch_adapter_down(d, st(stream));
-  if (e != hipSuccess) return FFN_E_HIP;
-  return done(launch_adapter_up(d, st(stream)));
+  if (!d.p.few) {
+    d.tab = static_cast<int4*>(workspace);
+    d.h = reinterpret_cast<float*>(static_cast<char*>(workspace) + tab_bytes(d.p));
+    d.hp = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(d.h) + h_bytes(d.p, r));
+  }
+  return done(launch_adapter_forward(d, st(stream)));
 }
 
 size_t ffn_adapter_backward_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t r, int32_t groups) {
@@ -137,9 +138,7 @@ ffn_status ffn_adapter_backward(const void* x, const void* a, const void* b, con
   if (da) d.dht = reinterpret_cast<uint16_t*>(at + parts_bytes(d.p, r));
   if (dx) d.dhp = reinterpret_cast<uint16_t*>(at + 2 * parts_bytes(d.p, r));
   if (d.p.slices > 1) d.part = reinterpret_cast<float*>(at + 3 * parts_bytes(d.p, r));
-  const hipError_t e = launch_adapter_down(d, st(stream));
-  if (e != hipSuccess) return FFN_E_HIP;
-  return done(launch_adapter_back(d, st(stream)));
+  return done(launch_adapter_backward(d, st(stream)));
 }
 
 }  // extern "C"

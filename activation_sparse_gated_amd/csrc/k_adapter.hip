@@ -111,15 +111,10 @@ __device__ __forceinline__ int row_at(const AdapterDesc& d, int place) {
 // v, or zeros. (Loads are made unconditionally, from a place that is there: a branch around each would end their overlap.)
 __device__ __forceinline__ uint4 keep_if(bool in, const uint4 v) { return uint4{in ? v.x : 0u, in ? v.y : 0u, in ? v.z : 0u, in ? v.w : 0u}; }
 __device__ const uint4 adapter_zero[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return uint4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
-}
-// f - bf16(f); nothing behind an infinity
-__device__ __forceinline__ void remainder8(float (&f)[8], const uint4 hi) {
-  float g[8];
-  unpack8(hi, g);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = fabsf(g[e]) == __builtin_huge_valf() ? 0.f : f[e] - g[e];
+// f less the bf16 number that it became; nothing behind an infinity
+__device__ __forceinline__ float rest_of(float f, uint32_t bf16) {
+  const float g = bf2f(bf16);
+  return fabsf(g) == __builtin_huge_valf() ? 0.f : f - g;
 }
 
 // ---------------------------------------------------------------- first product
@@ -135,8 +130,9 @@ struct DownLds {
   static constexpr int W = 64 * 16 * RB * 2 + 32;                // of a wave's step of B; the last row's read runs on a little
   static constexpr int BYTES = PART > kDownWaves * W ? PART : kDownWaves * W;
 };
-template <int RT, int RB, bool ALONG>
-__device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile, int t, int z, int j0, char* lds) {
+// emit(row, j, sum) is called once for every row of the tile and rank.
+template <int RT, int RB, bool ALONG, typename Emit>
+__device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile, int z, int j0, char* lds, Emit emit) {
   constexpr int MB = RT / 16;
   const int lane = lane_id(), wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
   const uint16_t* u = ALONG ? d.x : d.dy;
@@ -245,7 +241,6 @@ __device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile,
   }
   // the waves' sums, a block of 16 ranks at a time
   float* s_part = reinterpret_cast<float*>(lds);
-  float* out = (ALONG ? d.h : d.dh) + ((size_t)z * d.p.tiles + t) * RT * d.r;
 #pragma unroll
   for (int b = 0; b < RB; ++b) {
     __syncthreads();
@@ -259,8 +254,7 @@ __device__ __forceinline__ void down_tile(const AdapterDesc& d, const int4 tile,
       for (int w = 0; w < kDownWaves; ++w) v += s_part[w * RT * 16 + e];
       const int row = e >> 4, j = j0 + b * 16 + (e & 15);
       if (tile.y + row >= tile.z || row_at(d, tile.y + row) < 0) v = 0.f;
-      if (j >= d.r) continue;
-      out[(size_t)row * d.r + j] = v;
+      if (j < d.r) emit(row, j, v);
     }
   }
 }
@@ -276,8 +270,10 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down(const AdapterD
   const int j0 = (blockIdx.z % chunks) * kDownRanks;
   if (z == 0 && blockIdx.z == 0 && threadIdx.x == 0) d.tab[t] = tile;
   if (tile.x < 0 || z >= (back ? d.p.kd : d.p.ks)) return;
-  if (!back) down_tile<RT, RB, true>(d, tile, t, z, j0, lds);
-  else down_tile<RT, RB, false>(d, tile, t, z, j0, lds);
+  float* out = (back ? d.dh : d.h) + ((size_t)z * d.p.tiles + t) * RT * d.r;
+  auto emit = [&](int row, int j, float v) { out[(size_t)row * d.r + j] = v; };
+  if (!back) down_tile<RT, RB, true>(d, tile, z, j0, lds, emit);
+  else down_tile<RT, RB, false>(d, tile, z, j0, lds, emit);
 }
 
 // The same for tiles of 64 rows: both operands' steps go straight from memory to LDS, 256 bytes of a row by
@@ -527,7 +523,8 @@ __global__ __launch_bounds__(64) void k_adapter_sum(const AdapterDesc d, int wit
   }
 }
 
-hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s) {
+// First products: h (of x, if d.h) and dh (of dy, if d.dh), what is made of them, and the table of tiles.
+static hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s) {
   const int with_h = d.h != nullptr, with_dh = d.dh != nullptr, ranks = d.p.rt == 16 ? kDownRanks : kDown64Ranks;
   const int chunks = (d.r + ranks - 1) / ranks, ks = d.p.ks > d.p.kd ? d.p.ks : d.p.kd;
   const dim3 grid((d.p.tiles + 7) / 8 * 8, ks, (with_h + with_dh) * chunks), block(kDownWaves * 64);
@@ -575,30 +572,29 @@ __device__ __forceinline__ void transpose8(const uint4 (&in)[8], uint4 (&out)[8]
 // and columns exchanged, 16 bytes a row from each of 16 lanes, 8192 x 4096 x 14336 took 160 us.) ALONG: W = B, rows of r
 // elements a column; otherwise W = A^T, rows of the output's columns. F: groups of 32 ranks (0: up to 16, hi and lo in one
 // group).
-// READY: s h is there in bf16 numbers, which the four waves share through LDS (rows of an odd number of 16-byte chunks: no
-// bank conflicts); otherwise each wave makes them of the slices, for its one tile of 16 rows.
-template <typename T, int RT, int F, bool ALONG>
+// s h stands in LDS in bf16 numbers, which the workgroup's WAVES waves share: rows of an odd number of 16-byte chunks, so
+// that there are no bank conflicts.
+__device__ __forceinline__ int h_pitch(int r) { return ((r >> 3) | 1) * 16; }
+template <typename T, int RT, int F, bool ALONG, int WAVES = 4>
 struct Up {
-  static constexpr bool READY = RT == 64 || !ALONG;
   static constexpr int NF = F == 0 ? 1 : F;
   static constexpr int PARTS = sizeof(T) == 4 ? 3 : 2;
   static constexpr int PIECES = F == 0 ? 2 : 4;  // 16-byte chunks of a column's ranks in a group
   static constexpr bool STAY = NF <= 2;          // weights of up to 64 ranks stay in registers for all of the tile's rows
   static constexpr int MB = RT == 64 && !STAY ? 2 : 1;           // 16 rows each, for a group's weights
-  static constexpr int AHEAD = RT == 16 && NF > 1 ? (NF < 4 ? NF : 4) : 1;     // groups whose loads are under way
+  static constexpr int AHEAD = RT == 16 && NF > 1 ? (NF < 3 ? NF : 3) : 1;     // groups whose loads are under way
   static constexpr int W = ALONG ? 128 * PIECES * 16 + 256 : 0;  // LDS of a wave's weights
-  static constexpr int H = READY ? PARTS * RT * ((F == 0 ? 2 : NF * 4) + 1) * 16 : 0;
-  static constexpr int BYTES = 4 * W + H + 16;
+  static constexpr int H = PARTS * RT * ((F == 0 ? 2 : NF * 4) + 1) * 16;      // LDS of s h
+  static constexpr int BYTES = WAVES * W + H;
 };
-// Columns c0 .. of the workgroup's four waves, 128 each, of tile t.
-template <typename T, int RT, int F, bool ALONG>
-__device__ __forceinline__ void up_tile(const AdapterDesc& d, int block, int t, char* s_mem) {
-  using U = Up<T, RT, F, ALONG>;
+// The columns of the workgroup's waves, 128 each, of a tile. fill() brings s h to LDS, while the first loads are under way.
+template <typename T, int RT, int F, bool ALONG, int WAVES, typename Fill>
+__device__ __forceinline__ void up_tile(const AdapterDesc& d, int block, const int4 tile, char* s_mem, Fill fill) {
+  using U = Up<T, RT, F, ALONG, WAVES>;
   constexpr int NF = U::NF, PARTS = U::PARTS, PIECES = U::PIECES, MB = U::MB, AHEAD = U::AHEAD;
   const int lane = lane_id(), wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
   const int cols = ALONG ? d.n : d.k;
-  const int c0 = (block * 4 + wave) * 128;
-  const int4 tile = d.tab[t];
+  const int c0 = (block * WAVES + wave) * 128;
   if (tile.x == -2) return;
   if (tile.x == -1) {                            // no adapter: the base alone
     if (d.base == d.out) return;
@@ -632,15 +628,17 @@ __device__ __forceinline__ void up_tile(const AdapterDesc& d, int block, int t, 
   };
   auto ask = [&](int g) {
     uint4(&to)[ALONG ? 2 * PIECES : 8] = raw[g % AHEAD];
+    int first = g * 32;
+    if constexpr (NF > 2) asm volatile("" : "+v"(first));        // addresses are made here, not all of them up front and spilt
     if constexpr (ALONG) {
 #pragma unroll
       for (int n = 0; n < 2 * PIECES; ++n) {
         int col, piece;
         chunk(n, col, piece);
-        to[n] = ldg16(w + (size_t)min(c0 + col, cols - 1) * d.r + min(g * 32 + piece * 8, d.r - 8));
+        to[n] = ldg16(w + (size_t)min(c0 + col, cols - 1) * d.r + min(first + piece * 8, d.r - 8));
       }
     } else {
-      const int jc = min(g * 32 + jq, d.r - 8);
+      const int jc = min(first + jq, d.r - 8);
 #pragma unroll
       for (int e = 0; e < 8; ++e) to[e] = ldg16(w + (size_t)(jc + e) * cols + min(wc, cols - 8));
     }
@@ -667,16 +665,9 @@ __device__ __forceinline__ void up_tile(const AdapterDesc& d, int block, int t, 
     }
   };
   // ---------------------------------------------------------------- s h
-  const int r8 = d.r >> 3, hpitch = (r8 | 1) * 16;
-  uint4 made[NF][PARTS];                         // not READY: of the tile's 16 rows
   auto part_of = [&](int i0, int g, int n) {     // F = 0: hi for q < 2 and lo for the others in part 0; then the third
-    uint4 v;
-    if constexpr (U::READY) {
-      const int which = F == 0 && n == 0 ? q >> 1 : n;
-      v = *reinterpret_cast<const uint4*>(s_mem + (which * RT + min(i0 + l16, RT - 1)) * hpitch + min(g * 32 + jq, d.r - 8) * 2);
-    } else {
-      v = made[g][n];
-    }
+    const int which = F == 0 && n == 0 ? q >> 1 : n;
+    const uint4 v = *reinterpret_cast<const uint4*>(s_mem + (which * RT + min(i0 + l16, RT - 1)) * h_pitch(d.r) + min(g * 32 + jq, d.r - 8) * 2);
     return as_bf16x8(keep_if(g * 32 + jq < d.r && (F != 0 || n == 0 || q < 2), v));
   };
   // ---------------------------------------------------------------- base
@@ -700,46 +691,7 @@ __device__ __forceinline__ void up_tile(const AdapterDesc& d, int block, int t, 
   for (int g = 0; g < AHEAD; ++g) ask(g);
   fetch(0);
   __builtin_amdgcn_sched_barrier(0);
-  if constexpr (U::READY) {
-    const uint16_t* hrow = (ALONG ? d.hp : d.dhp) + (size_t)t * 3 * RT * d.r;
-    for (int c = threadIdx.x; c < PARTS * RT * r8; c += 256) {
-      const int line = c / r8;
-      *reinterpret_cast<uint4*>(s_mem + line * hpitch + (c - line * r8) * 16) = ldg16(hrow + (size_t)c * 8);
-    }
-    __syncthreads();
-  } else {
-    const float* hp = (ALONG ? d.h : d.dh) + ((size_t)t * RT + min(l16, rows - 1)) * d.r;     // rows past the last: its own again
-    const size_t slab = (size_t)d.p.tiles * RT * d.r;
-    const float scale = d.scales ? d.scales[tile.x] : 1.f;
-    f32x4_t ha[NF][2];
-#pragma unroll
-    for (int g = 0; g < NF; ++g) ha[g][0] = ha[g][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int z = 0; z < d.p.ks; ++z) {
-#pragma unroll
-      for (int g = 0; g < NF; ++g) {
-        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(hp + z * slab + min(g * 32 + jq, d.r - 8));
-        ha[g][0] += p[0];
-        ha[g][1] += p[1];
-      }
-    }
-#pragma unroll
-    for (int g = 0; g < NF; ++g) {
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = ha[g][e >> 2][e & 3] * scale;
-      const uint4 hi = pack8(f);
-      remainder8(f, hi);
-      const uint4 lo = pack8(f);
-      made[g][0] = hi;
-      made[g][1] = lo;
-      if constexpr (F == 0) made[g][0] = q < 2 ? hi : lo;
-      if constexpr (PARTS == 3) {
-        remainder8(f, lo);
-        made[g][2] = pack8(f);
-      }
-    }
-  }
+  fill();
   if (c0 >= cols) return;
   if constexpr (U::STAY) {
     weights(0);
@@ -797,11 +749,93 @@ __device__ __forceinline__ void up_tile(const AdapterDesc& d, int block, int t, 
   }
 }
 
+// s h from memory, [PARTS][RT][r] in bf16 numbers.
+template <int ROWS, int THREADS>
+__device__ __forceinline__ void fill_made(const uint16_t* from, int r, char* s_mem) {
+  const int r8 = r >> 3, pitch = h_pitch(r);
+  for (int c = threadIdx.x; c < ROWS * r8; c += THREADS) {
+    const int line = c / r8;
+    *reinterpret_cast<uint4*>(s_mem + line * pitch + (c - line * r8) * 16) = ldg16(from + (size_t)c * 8);
+  }
+  __syncthreads();
+}
+// s h of a tile of 16 rows from the slices' sums.
+template <int PARTS>
+__device__ __forceinline__ void fill_slices(const AdapterDesc& d, int t, int g, char* s_mem) {
+  const int r4 = d.r >> 2, pitch = h_pitch(d.r);
+  const float scale = d.scales ? d.scales[g] : 1.f;
+  const size_t slab = (size_t)d.p.tiles * 16 * d.r;
+  for (int e = threadIdx.x; e < 16 * r4; e += 256) {
+    const int row = e / r4, j = (e - row * r4) * 4;
+    const float* p = d.h + ((size_t)t * 16 + row) * d.r + j;
+    f32x4_t v = *reinterpret_cast<const f32x4_t*>(p);
+#pragma unroll 4
+    for (int z = 1; z < d.p.ks; ++z) v += *reinterpret_cast<const f32x4_t*>(p + z * slab);
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = v[i] * scale;
+#pragma unroll
+    for (int n = 0; n < PARTS; ++n) {
+      const uint32_t part[2] = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])};
+      *reinterpret_cast<uint2*>(s_mem + (n * 16 + row) * pitch + j * 2) = uint2{part[0], part[1]};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = rest_of(f[i], i & 1 ? part[i >> 1] >> 16 : part[i >> 1] & 0xFFFFu);
+    }
+  }
+  __syncthreads();
+}
+
 template <typename T, int RT, int F>
 __global__ __launch_bounds__(256, F == 0 ? (RT == 16 ? 4 : 3) : F == 1 ? 3 : 2) void k_adapter_up(const AdapterDesc d) {
-  __shared__ __attribute__((aligned(16))) char s_mem[Up<T, RT, F, true>::BYTES];
+  using U = Up<T, RT, F, true>;
+  __shared__ __attribute__((aligned(16))) char s_mem[U::BYTES];
   const int t = blockIdx.y + blockIdx.z * gridDim.y;
-  if (t < d.p.tiles) up_tile<T, RT, F, true>(d, blockIdx.x, t, s_mem);
+  if (t >= d.p.tiles) return;
+  const int4 tile = d.tab[t];
+  up_tile<T, RT, F, true, 4>(d, blockIdx.x, tile, s_mem, [&] {
+    if constexpr (RT == 16) fill_slices<U::PARTS>(d, t, tile.x, s_mem);
+    else fill_made<U::PARTS * RT, 256>(d.hp + (size_t)t * 3 * RT * d.r, d.r, s_mem);
+  });
+}
+
+// Both products of a tile of 16 rows in one launch, for few rows and ranks up to 32, where a launch costs as much as the
+// work: each of d.p.few workgroups makes all of s h for its tile, and takes every d.p.few-th block of 1024 columns, the
+// first one's weights and base on their way meanwhile. 4096 x 14336, rank 16: one row 8.7 us a call instead of 12.8, 16 rows
+// of 16 adapters 11.0 instead of 12.9.
+template <typename T, int F>
+__global__ __launch_bounds__(kDownWaves * 64, 2) void k_adapter_few(const AdapterDesc d) {
+  using U = Up<T, 16, F, true, kDownWaves>;
+  constexpr int RB = F == 0 ? 1 : 2, PART = DownLds<16, RB>::PART;
+  static_assert(F <= 1, "ranks of one pass");
+  __shared__ __attribute__((aligned(16))) char s_mem[U::H + (kDownWaves * U::W > PART ? kDownWaves * U::W : PART)];
+  const int4 tile = adapter_tile<16>(d, blockIdx.x, gridDim.x);
+  if (tile.x == -2) return;
+  auto up = [&](int block, auto fill) { up_tile<T, 16, F, true, kDownWaves>(d, block, tile, s_mem, fill); };
+  auto down = [&] {
+    const float scale = d.scales ? d.scales[tile.x] : 1.f;
+    const int pitch = h_pitch(d.r);
+    down_tile<16, RB, true>(d, tile, 0, 0, s_mem + U::H, [&](int row, int j, float v) {
+      v *= scale;
+#pragma unroll
+      for (int n = 0; n < U::PARTS; ++n) {
+        const uint32_t part = pack_bf16(v, 0.f) & 0xFFFFu;
+        *reinterpret_cast<uint16_t*>(s_mem + (n * 16 + row) * pitch + j * 2) = (uint16_t)part;
+        v = rest_of(v, part);
+      }
+    });
+    __syncthreads();
+  };
+  const int n = (d.n + kDownWaves * 128 - 1) / (kDownWaves * 128), first = blockIdx.y, step = gridDim.y;
+  up(first, down);
+  for (int block = first + step; block < n; block += step) up(block, [] {});
+}
+
+template <typename T>
+static hipError_t few(const AdapterDesc& d, hipStream_t s) {
+  const dim3 grid((d.p.tiles + 7) / 8 * 8, d.p.few), block(kDownWaves * 64);
+  if (d.r <= 16) ffn_launch((k_adapter_few<T, 0>), grid, block, 0, s, d);
+  else ffn_launch((k_adapter_few<T, 1>), grid, block, 0, s, d);
+  return hipGetLastError();
 }
 template <typename T, int RT>
 static hipError_t up(const AdapterDesc& d, hipStream_t s) {
@@ -815,7 +849,10 @@ static hipError_t up(const AdapterDesc& d, hipStream_t s) {
   else ffn_launch((k_adapter_up<T, RT, 8>), grid, block, 0, s, d);
   return hipGetLastError();
 }
-hipError_t launch_adapter_up(const AdapterDesc& d, hipStream_t s) {
+hipError_t launch_adapter_forward(const AdapterDesc& d, hipStream_t s) {
+  if (d.p.few) return d.out_f32 ? few<float>(d, s) : few<uint16_t>(d, s);
+  const hipError_t e = launch_adapter_down(d, s);
+  if (e != hipSuccess) return e;
   if (d.out_f32) return d.p.rt == 16 ? up<float, 16>(d, s) : up<float, 64>(d, s);
   return d.p.rt == 16 ? up<uint16_t, 16>(d, s) : up<uint16_t, 64>(d, s);
 }
@@ -979,7 +1016,10 @@ __global__ __launch_bounds__(kDwWaves * 64, F == 0 ? 3 : 2) void k_adapter_back(
   }
   const long long at = n - grid.dw;
   const int t = (int)(at / grid.x);
-  if (t < d.p.tiles) up_tile<uint16_t, RT, F, false>(d, (int)(at - (long long)t * grid.x), t, s_mem);
+  if (t >= d.p.tiles) return;
+  up_tile<uint16_t, RT, F, false, 4>(d, (int)(at - (long long)t * grid.x), d.tab[t], s_mem, [&] {
+    fill_made<U::PARTS * RT, 256>(d.dhp + (size_t)t * 3 * RT * d.r, d.r, s_mem);
+  });
 }
 // The slices' sums, to da (na values) and db (nb behind them), four values a thread.
 __global__ __launch_bounds__(256) void k_adapter_dw_sum(const AdapterDesc d, size_t na, size_t nb) {
@@ -1015,10 +1055,12 @@ static void back(const AdapterDesc& d, hipStream_t s) {
   else if (d.r <= 128) back_ranks<RT, 4>(d, s);
   else back_ranks<RT, 8>(d, s);
 }
-hipError_t launch_adapter_back(const AdapterDesc& d, hipStream_t s) {
+hipError_t launch_adapter_backward(const AdapterDesc& d, hipStream_t s) {
+  hipError_t e = launch_adapter_down(d, s);
+  if (e != hipSuccess) return e;
   if (d.p.rt == 16) back<16>(d, s);
   else back<64>(d, s);
-  const hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess || d.p.slices == 1 || (!d.da && !d.db)) return e;
   const size_t na = d.da ? (size_t)d.groups * d.r * d.k : 0, nb = d.db ? (size_t)d.groups * d.r * d.n : 0;
   const size_t blocks = (na + nb + 1023) / 1024;
@@ -1035,7 +1077,7 @@ AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) 
   const long long tiles = (long long)m / p.rt + groups + 2;
   p.tiles = (int)(tiles < m ? tiles : m);
   // slices of the first products: enough workgroups for the chip
-  const int live = (m + p.rt - 1) / p.rt;
+  const int live = p.rt == 64 ? (m + 63) / 64 : m / 16 + groups < m ? m / 16 + groups : m;
   auto slices = [&](int width) {
     const int steps = width / (p.rt == 64 ? kStep : 64), least = p.rt == 64 ? 4 : kDownWaves;
     int ks = 1;
@@ -1046,6 +1088,21 @@ AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) 
   };
   p.ks = slices(k);
   p.kd = backward ? slices(n) : 1;
+  // Both products in one launch, with about a workgroup a CU, if there are columns for as many; where that costs less than
+  // a launch: a workgroup reads its tile's operands of the first product (160 KB at most: 64 rows of 4 adapters, rank 16,
+  // 4096 x 4096 take 12.8 us either way), and a tile's workgroups all read the same (30 MB at most together: 48 rows of 32
+  // adapters, 4096 x 14336, 13.6 us instead of 12.4).
+  p.few = 0;
+  if (!backward && p.rt == 16 && r <= 32) {
+    const int blocks = (n + kDownWaves * 128 - 1) / (kDownWaves * 128);
+    const int most = live < 256 ? 256 / live : 1, turns = (blocks + most - 1) / most;
+    const int few = (blocks + turns - 1) / turns, rows = m / groups < 16 ? (m + groups - 1) / groups : 16;
+    const long long read = 2LL * (r + rows) * k;
+    if (read <= 160 << 10 && read * live * (few - 1) <= 30000000) {
+      p.few = few;
+      p.ks = 1;
+    }
+  }
   // waves of the adapters' gradients: two for each SIMD, if there are steps of 32 rows for as many
   const int steps = (m / groups + 31) / 32;
   const long long waves = ((long long)(n + 127) / 128 + (k + 127) / 128) * groups * ((r + 63) / 64);

@@ -42,7 +42,7 @@ extern "C" {
 
 int32_t ffn_adapter_abi_version(void);
 
-/* Bytes of workspace ffn_adapter_forward needs (0 if invalid, or without rows). */
+/* Bytes of workspace ffn_adapter_forward needs (0: none, as for few rows, or invalid). */
 size_t ffn_adapter_forward_workspace_bytes(int32_t m, int32_t n, int32_t k, int32_t r, int32_t groups);
 
 /* y[t] = base[t] + scales[g] B_g (A_g x[t]) for the rows t of each adapter g,

@@ -126,6 +126,26 @@ def check_backward(asg, s, base, accumulate=False):
     return dx, da, db
 
 
+# few rows with long contractions, which take two launches, and many tiles of few rows in one
+FEW = [(1, 136, 16392, 16, 1), (48, 264, 5128, 24, 33), (130, 136, 8200, 8, 7), (33, 520, 4104, 64, 70), (1300, 72, 2056, 40, 200),
+       (90, 1032, 4104, 32, 3), (5000, 264, 136, 16, 1000), (16, 10248, 136, 8, 1), (300, 2056, 328, 32, 40)]
+
+
+@pytest.mark.parametrize("kind", ["rows", "ordered"])
+@pytest.mark.parametrize("shape", FEW, ids=lambda s: "x".join(map(str, s)))
+def test_forward_of_few_rows(asg, shape, kind):
+    say("adapter forward, few rows", shape, kind)
+    m, n, k, r, groups = shape
+    s, g = make(m, n, k, r, groups, kind, 7)
+    for out in ("bf16", "f32"):
+        base = dev(g.normal(0, 1, (m, n)), out)
+        y = check_forward(asg, s, base, out)
+        check_forward(asg, dict(s, scales=None), None, out)
+        again = base.clone()
+        z = asg.adapter_forward(s["x"], s["a"], s["b"], dev(s["offsets"]), base=again, y=again, **call(s))
+        assert z is again and torch_().equal(z, y)
+
+
 @pytest.mark.parametrize("kind", ["rows", "ordered"])
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
 def test_backward(asg, shape, kind):
@@ -257,4 +277,6 @@ def test_refusals(asg):
     with pytest.raises(asg.FFNError):
         asg.adapter_forward(x, torch.zeros(2, 12, 64, **bf), torch.zeros(2, 72, 12, **bf), off)
     with pytest.raises(asg.FFNError):
-        asg.adapter_forward(x, a, b, off, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        asg.adapter_forward(torch.zeros(900, 64, **bf), a, b, off, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(asg.FFNError):
+        asg.adapter_backward(x, a, b, dy, off, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
