@@ -193,6 +193,27 @@ def test_route_close_values_are_told_apart(asg, m, experts):
             check_route(asg, l, "f32", 8, dict(kw, groups=8, top_groups=2, group_best=best), zero)
 
 
+@pytest.mark.parametrize("m", [1, 1000, 1040])
+@pytest.mark.parametrize("experts", [64, 256])
+def test_route_groups_by_the_second_of_two_close_values(asg, m, experts):
+    # two experts next to each other, equal in fp32, the second one larger in fp64: the best of their group, ahead of a value
+    # between the two in another group
+    say("route groups close", m, experts)
+    g = rng(14, m, experts)
+    step, size = 2.0 ** -20, experts // 8
+    l = np.clip(g.normal(-2, 1, (m, experts)), None, 4).astype(np.float32)
+    for t in range(m):
+        one, two = g.permutation(8)[:2] * size + 2 * g.integers(0, size // 2, 2)
+        l[t, one], l[t, one + 1], l[t, two] = 9, 9 + 2 * step, 9 + step
+        if t % 2:
+            l[t, two + 1] = 9 + step / 2 if t % 4 == 1 else 9 - 4 * step
+    zero = np.zeros(experts, np.float32)
+    for kw in (dict(sigmoid=True), dict()):
+        for top_groups in (1, 2):
+            check_route(asg, l, "f32", 4, dict(kw, groups=8, top_groups=top_groups, group_best=1), zero)
+        check_route(asg, l, "f32", 4, dict(kw, groups=8, top_groups=1, group_best=1), None)
+
+
 def test_route_far_logits(asg):
     # saturated and vanishing scores: the choice is the logits', the renormalised weights keep their ratio
     say("route far")
@@ -287,7 +308,7 @@ def test_route_backward_slots_without_experts_and_in_place(asg):
 
 # ---------------------------------------------------------------- order by group
 @pytest.mark.parametrize("groups", [1, 2, 7, 8, 63, 64, 255, 256, 1000, 1024])
-@pytest.mark.parametrize("n", [1, 5, 64, 200, 256, 257, 1000, 4096, 4097, 9999, 16384, 16385, 40000, 70001])
+@pytest.mark.parametrize("n", [1, 5, 64, 200, 256, 257, 1000, 4096, 4097, 8192, 8193, 9999, 16384, 16385, 40000, 70001])
 def test_group_rows(asg, n, groups):
     say("group", n, groups)
     g = rng(10, n, groups)
