@@ -1071,19 +1071,28 @@ hipError_t launch_adapter_backward(const AdapterDesc& d, hipStream_t s) {
 // ---------------------------------------------------------------- plan
 AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) {
   AdapterPlan p;
-  // tiles of 64 rows where adapters have that many to share their weights' reads, of 16 where rows are few
-  p.rt = m >= 512 && m / 16 >= groups ? 64 : 16;
+  // Tiles of 64 rows where adapters have rows to share their weights' reads, and where there is work enough for more
+  // launches. Forward, rank 64, 4096 x 4096, 8 adapters, tiles of 16 and of 64: 1024 rows 20.7 and 21.1 us, 2048 28.4 and
+  // 24.4, 4096 50.8 and 40.4; rank 16: 4096 rows 29.0 and 33.0; 1024 x 1024, rank 64: 4096 rows 19.5 and 20.6, 8192 of 256
+  // adapters 44.8 and 36.0; 16 rows an adapter: 29.9 and 36.0. Backward, rank 64, 32 rows an adapter: 256 rows, 4096 x 4096,
+  // 30.5 and 25.8; 512, 1024 x 1024, 21.8 and 23.2.
+  const bool long_way = backward ? (long long)m * (n + k) >= 1 << 21 : m >= 8192 || (long long)m * r * k >= 1LL << 29;
+  p.rt = long_way && m / 32 >= groups ? 64 : 16;
   // every adapter's last tile may be short, and so may the two runs of rows without one
   const long long tiles = (long long)m / p.rt + groups + 2;
   p.tiles = (int)(tiles < m ? tiles : m);
-  // slices of the first products: enough workgroups for the chip
+  // Slices of the first products, where there are too few tiles for the chip. Tiles of 16 rows: 48 rows of 32 adapters,
+  // 4096 x 14336, rank 16, in 1, 2, 4, 8 slices 15.0, 13.0, 12.5, 12.7 us; 16 of 16, 4096 x 4096, rank 64: 24.8, 18.1, 15.1,
+  // 14.7. Tiles of 64, forward, 4096 x 4096, rank 64: 2048 rows 31.9, 26.9, 24.2, 24.8; 4096 rows 47.7, 41.3, 39.0, 43.1; 8192
+  // rows of uneven adapters, 4096 x 14336, whole 127, in two 134. Backward (of dy B), 4095 x 2048 x 8192, rank 16: 58.1, 51.2,
+  // 50.0, 50.3.
   const int live = p.rt == 64 ? (m + 63) / 64 : m / 16 + groups < m ? m / 16 + groups : m;
+  const int wanted = p.rt == 64 && (backward || live >= 128) ? 128 : 256;
   auto slices = [&](int width) {
     const int steps = width / (p.rt == 64 ? kStep : 64), least = p.rt == 64 ? 4 : kDownWaves;
     int ks = 1;
     // (backward, slices of both products besides that are about as long as each other)
-    while (ks < 8 && steps / (ks * 2) >= least &&
-           (live * ks < (p.rt == 64 ? 128 : 256) || (backward && p.rt == 64 && steps / ks > 32))) ks *= 2;
+    while (ks < 8 && steps / (ks * 2) >= least && (live * ks < wanted || (backward && p.rt == 64 && steps / ks > 32))) ks *= 2;
     return ks;
   };
   p.ks = slices(k);

@@ -70,7 +70,7 @@ def test_group_refusals(lib, kw, want):
 
 def test_group_workspace(lib):
     f = lib.ffn_group_rows_workspace_bytes
-    assert f(16384, 8) == 0 < f(16385, 8) <= f(2 ** 24, 1024) and f(2 ** 24 + 1, 8) == 0 == f(20000, 1025) == f(-1, 8)
+    assert f(8192, 8) == 0 < f(8193, 8) <= f(2 ** 24, 1024) and f(2 ** 24 + 1, 8) == 0 == f(20000, 1025) == f(-1, 8)
 
 
 def gather(lib, x=P, dtype=1, m=4, d=64, slots=P, k=2, y=P, q=None, s=None):
@@ -115,7 +115,7 @@ def adapter(lib, x=P, a=P, b=P, s=None, off=P, rows=None, g=2, m=4, n=64, k=64, 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(x=None), INVALID), (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(off=None), INVALID), (dict(y=None), INVALID),
-    (dict(ws=None, m=5000), INVALID), (dict(ws=P + 8), INVALID), (dict(nb=16, m=5000), WORKSPACE), (dict(s=P + 4), INVALID),
+    (dict(ws=None, r=40), INVALID), (dict(ws=P + 8), INVALID), (dict(nb=16, r=40), WORKSPACE), (dict(s=P + 4), INVALID),
     (dict(rows=P + 8), INVALID), (dict(base=P + 2), INVALID), (dict(g=0), INVALID), (dict(g=1025), INVALID), (dict(m=-1), INVALID),
     (dict(m=2 ** 26 + 1), INVALID), (dict(n=12), INVALID), (dict(k=4), INVALID), (dict(r=12), INVALID), (dict(r=0), INVALID),
     (dict(r=264), INVALID), (dict(n=2 ** 22 + 8), INVALID), (dict(yt=2), INVALID)])
@@ -140,7 +140,7 @@ def test_adapter_backward_refusals(lib, kw, want):
 
 def test_adapter_workspace(lib):
     for f in (lib.ffn_adapter_forward_workspace_bytes, lib.ffn_adapter_backward_workspace_bytes):
-        assert f(5000, 64, 64, 16, 2) > 0 and f(0, 64, 64, 16, 2) == 0 == f(5000, 60, 64, 16, 2) == f(5000, 64, 64, 16, 1025)
+        assert f(5, 64, 64, 40, 2) > 0 and f(0, 64, 64, 40, 2) == 0 == f(5, 60, 64, 40, 2) == f(5, 64, 64, 40, 1025)
     assert lib.ffn_adapter_forward_workspace_bytes(5, 64, 64, 16, 2) == 0 < lib.ffn_adapter_backward_workspace_bytes(5, 64, 64, 16, 2)
 
 

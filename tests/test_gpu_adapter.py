@@ -129,12 +129,17 @@ def check_backward(asg, s, base, accumulate=False):
 # few rows with long contractions, which take two launches, and many tiles of few rows in one
 FEW = [(1, 136, 16392, 16, 1), (48, 264, 5128, 24, 33), (130, 136, 8200, 8, 7), (33, 520, 4104, 64, 70), (1300, 72, 2056, 40, 200),
        (90, 1032, 4104, 32, 3), (5000, 264, 136, 16, 1000), (16, 10248, 136, 8, 1), (300, 2056, 328, 32, 40)]
+# many rows of few adapters (tiles of 64), every number of ranks, whole and in slices
+MANY = [(8200, 136, 264, 16, 9), (8300, 200, 136, 64, 250), (8192, 200, 200, 200, 6), (2100, 264, 8200, 64, 3),
+        (2056, 136, 4104, 128, 20), (9000, 200, 136, 40, 1), (8400, 520, 1032, 8, 200), (8201, 264, 392, 256, 2),
+        (8333, 136, 328, 72, 3), (16500, 72, 136, 32, 4), (8450, 264, 136, 128, 100), (4100, 136, 8200, 16, 7),
+        (2050, 72, 16392, 24, 64)]
 
 
 @pytest.mark.parametrize("kind", ["rows", "ordered"])
-@pytest.mark.parametrize("shape", FEW, ids=lambda s: "x".join(map(str, s)))
-def test_forward_of_few_rows(asg, shape, kind):
-    say("adapter forward, few rows", shape, kind)
+@pytest.mark.parametrize("shape", FEW + MANY, ids=lambda s: "x".join(map(str, s)))
+def test_forward_of_few_and_many_rows(asg, shape, kind):
+    say("adapter forward, few and many rows", shape, kind)
     m, n, k, r, groups = shape
     s, g = make(m, n, k, r, groups, kind, 7)
     for out in ("bf16", "f32"):
@@ -164,6 +169,16 @@ def test_backward(asg, shape, kind):
             assert one is None if v != need else torch.equal(one, all_)
     again = base.clone()
     assert torch.equal(asg.adapter_backward(*inputs, off, base=again, dx=again, need_da=False, need_db=False, **kw)[0], dx)
+
+
+@pytest.mark.parametrize("kind", ["rows", "ordered"])
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "x".join(map(str, s)))
+def test_backward_of_many_rows(asg, shape, kind):
+    say("adapter backward, many rows", shape, kind)
+    m, n, k, r, groups = shape
+    s, g = make(m, n, k, r, groups, kind, 8)
+    check_backward(asg, s, dev(g.normal(0, 1, (m, k)), "bf16"))
+    check_backward(asg, dict(s, scales=None), None, accumulate=True)
 
 
 def test_offsets_and_rows_out_of_range(asg):
@@ -277,6 +292,6 @@ def test_refusals(asg):
     with pytest.raises(asg.FFNError):
         asg.adapter_forward(x, torch.zeros(2, 12, 64, **bf), torch.zeros(2, 72, 12, **bf), off)
     with pytest.raises(asg.FFNError):
-        asg.adapter_forward(torch.zeros(900, 64, **bf), a, b, off, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        asg.adapter_forward(x, torch.zeros(2, 40, 64, **bf), torch.zeros(2, 72, 40, **bf), off, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(asg.FFNError):
         asg.adapter_backward(x, a, b, dy, off, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
