@@ -15,6 +15,12 @@
 // output's rounding takes), for fp32 outputs as three (2^-24); with ranks up to 16
 // the first two share one instruction, hi in the contraction's first half and
 // lo in its second.
+//
+// Bound by HBM: 2 r operations for each element of x, y, A and B. Many rows:
+// 8192 x 4096 x 14336, rank 64, 29.8 us for the first product and 100.7 for the
+// second (525 MB, 5.2 TB/s). Few rows: by the latency of the chain of loads and
+// by the launches, one row 8.7 us in one launch, 48 rows of 32 adapters 5.9 and
+// 7.1 in two.
 #include <type_traits>
 
 #include "adapter.cuh"
@@ -120,9 +126,11 @@ __device__ __forceinline__ float rest_of(float f, uint32_t bf16) {
 // ---------------------------------------------------------------- first product
 // h[place][j] = sum over i of u[row][i] W[j][i] for one tile, one slice of the contraction and up to 16 RB ranks from j0
 // on. The waves take the slice's steps of 64 elements in turn, each with the loads of its next one under way; their sums
-// are added in order. ALONG: the weights' rows run along the contraction (A). Otherwise across it (B, rows of r
-// elements): a step's 64 rows go through the wave's own part of LDS, which the transposing read turns: in each 16 lanes,
-// lane 4 v + u points at row 8 q + 4 h + v, elements 4 u .. + 3, and lane j receives element j % 4 of lane 4 v + j / 4.
+// are added in order. (48 rows of 32 adapters, 4096 wide, rank 16, 8 slices: 5.9 us. With three to six steps' loads under
+// way instead of one: no faster, 14.9 instead of 14.3 us in k_adapter_few.) ALONG: the weights' rows run along the
+// contraction (A). Otherwise across it (B, rows of r elements): a step's 64 rows go through the wave's own part of LDS,
+// which the transposing read turns: in each 16 lanes, lane 4 v + u points at row 8 q + 4 h + v, elements 4 u .. + 3, and
+// lane j receives element j % 4 of lane 4 v + j / 4.
 constexpr int kDownRanks = 64, kDown64Ranks = 128;               // of a workgroup, with tiles of 16 and of 64 rows
 template <int RT, int RB>
 struct DownLds {
@@ -276,11 +284,13 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down(const AdapterD
   else down_tile<RT, RB, false>(d, tile, z, j0, lds, emit);
 }
 
-// The same for tiles of 64 rows: both operands' steps go straight from memory to LDS, 256 bytes of a row by
-// neighbouring lanes, STAGES - 1 steps ahead of the products (a lane of the version above takes 16 bytes of a row of its
-// own, and the weights come in anew for every 16 or 32 rows: 8192 x 4096, 64 ranks, 55 us). Wave (i, h) has rows 16 i ..
-// and half h of each step, for all ranks. Tiles start at different steps, or all of them would read the same few
-// channels of memory at a time. Rows of 256 bytes in LDS, chunk c at c ^ (row & 15): no bank conflicts.
+// The same for tiles of 64 rows: both operands' steps go straight from memory to LDS, 256 bytes of a row by neighbouring
+// lanes, STAGES - 1 steps ahead of the products (a lane of the version above takes 16 bytes of a row of its own, and the
+// weights come in anew for every 16 or 32 rows: 8192 x 4096, 64 ranks, 55 us). Wave (i, h) has rows 16 i .. and half h of
+// each step, for all ranks. 8192 x 4096, 64 ranks: 29.8 us, of which the products take nothing (without them 29.1) and the
+// weights 5.5; a plain read of the same 67 MB takes 15 to 16. Steps of 64 elements in 3 to 8 stages and two or four slices:
+// 28.3 to 32.1, and 5.2 to 5.5 for the slices' sum. Tiles start at different steps, or all of them would read the same few
+// channels of memory at a time. Rows of 256 bytes in LDS, chunk c at c ^ (row & 15): reads of rows meet no bank twice.
 constexpr int kStep = 128, kStepBytes = 2 * kStep; // elements and bytes of a row in a step
 __device__ __forceinline__ void to_lds16(const void* p, const char* l) {
   const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)l;
@@ -459,9 +469,9 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down64(const Adapte
   else down64_tile<RB, false>(d, tile, t, z, j0, lds);
 }
 
-// Behind it, for each of h and dh: the slices' sums times the adapter's scale, as two bf16 numbers (three for fp32
-// outputs) in rows of ranks for the second product, and as three with the tile's rows along for the adapters' gradients.
-// Four rows of four ranks a thread.
+// Behind it (4.7 us for 4095 rows, rank 16, two launches' worth of latency), for each of h and dh: the slices' sums times
+// the adapter's scale, as two bf16 numbers (three for fp32 outputs) in rows of ranks for the second product, and as three
+// with the tile's rows along for the adapters' gradients. Four rows of four ranks a thread.
 template <int KS>
 __device__ __forceinline__ void sum_rows(const AdapterDesc& d, const float* h, size_t slab, float (&f)[4][4], float scale) {
   f32x4_t v[4][KS];
@@ -567,13 +577,13 @@ __device__ __forceinline__ void transpose8(const uint4 (&in)[8], uint4 (&out)[8]
   }
 }
 
-// out = base + s h W^T for a tile: a wave has 128 columns, accumulator e of lane l column 8 (l % 16) + e of row 4 (l / 16) + v
-// in its value v, so that a lane reads and writes eight neighbours and 16 lanes 256 bytes of a row. (With the lanes' rows
-// and columns exchanged, 16 bytes a row from each of 16 lanes, 8192 x 4096 x 14336 took 160 us.) ALONG: W = B, rows of r
-// elements a column; otherwise W = A^T, rows of the output's columns. F: groups of 32 ranks (0: up to 16, hi and lo in one
-// group).
-// s h stands in LDS in bf16 numbers, which the workgroup's WAVES waves share: rows of an odd number of 16-byte chunks, so
-// that there are no bank conflicts.
+// out = base + s h W^T for a tile: a wave has 128 columns, accumulator e of lane l column 8 (l % 16) + e of row 4 (l / 16)
+// + v in its value v, so that a lane reads and writes eight neighbours and 16 lanes 256 bytes of a row. (With the lanes'
+// rows and columns exchanged, 16 bytes a row from each of 16 lanes, 8192 x 4096 x 14336, rank 64, took 160 us; so 100.7:
+// 235 MB of the base, as many of the output and 55 of s h and the weights, 5.2 TB/s. Stores past the caches: no gain.)
+// ALONG: W = B, rows of r elements a column; otherwise W = A^T, rows of the output's columns. F: groups of 32 ranks (0: up
+// to 16, hi and lo in one group). s h stands in LDS in bf16 numbers, which the workgroup's WAVES waves share, in rows of an
+// odd number of 16-byte chunks, so that the lanes' rows lie in different banks.
 __device__ __forceinline__ int h_pitch(int r) { return ((r >> 3) | 1) * 16; }
 template <typename T, int RT, int F, bool ALONG, int WAVES = 4>
 struct Up {
@@ -863,7 +873,8 @@ hipError_t launch_adapter_forward(const AdapterDesc& d, hipStream_t s) {
 // the next ones under way; s h enters as three bf16 numbers. A workgroup's four waves are `split` waves for each of its 4 /
 // split column blocks, which take the steps of 32 rows in turn and whose sums are added in order (waves of different
 // columns share the reads of s h, 1.5 times as many bytes as x with 64 ranks). Where that leaves the chip empty, the rows
-// are cut into slices besides, whose sums k_adapter_dw_sum adds.
+// are cut into slices besides, whose sums k_adapter_dw_sum adds. One adapter, 4096 rows, 1024 x 1024, rank 16: with 1, 2, 4
+// waves a block 133, 76, 47 us the whole pass; with 4 and 1, 2, 4, 8, 16 slices 46.8, 34.0, 27.5, 25.5, 26.8.
 constexpr int kDwWaves = 4;
 template <int RT, int RB, bool OF_A>
 __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int block, int j0, int slice, float* s_part) {
@@ -991,7 +1002,8 @@ __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int block, 
 }
 
 // The second half of the backward pass, whose two parts read nothing of each other: workgroups of the adapters' gradients
-// (the longer ones), then those of dx. One launch lets the one's memory traffic fill the other's gaps.
+// (the longer ones), then those of dx. One launch lets the one's memory traffic fill the other's gaps: 4095 x 2048 x 8192,
+// rank 16, 26.4 us for 132 MB from memory (5.0 TB/s) instead of 32.
 struct BackGrid {
   int a, b;                      // column blocks of da and db
   int groups, z;                 // z: rank blocks times slices
@@ -1082,10 +1094,10 @@ AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) 
   const long long tiles = (long long)m / p.rt + groups + 2;
   p.tiles = (int)(tiles < m ? tiles : m);
   // Slices of the first products, where there are too few tiles for the chip. Tiles of 16 rows: 48 rows of 32 adapters,
-  // 4096 x 14336, rank 16, in 1, 2, 4, 8 slices 15.0, 13.0, 12.5, 12.7 us; 16 of 16, 4096 x 4096, rank 64: 24.8, 18.1, 15.1,
-  // 14.7. Tiles of 64, forward, 4096 x 4096, rank 64: 2048 rows 31.9, 26.9, 24.2, 24.8; 4096 rows 47.7, 41.3, 39.0, 43.1; 8192
-  // rows of uneven adapters, 4096 x 14336, whole 127, in two 134. Backward (of dy B), 4095 x 2048 x 8192, rank 16: 58.1, 51.2,
-  // 50.0, 50.3.
+  // 4096 x 14336, rank 16, in 1, 2, 4, 8 slices 15.0, 13.0, 12.5, 12.7 us; 16 of 16, 4096 x 4096, rank 64: 24.8, 18.1,
+  // 15.1, 14.7. Tiles of 64, forward, 4096 x 4096, rank 64: 2048 rows 31.9, 26.9, 24.2, 24.8; 4096 rows 47.7, 41.3, 39.0,
+  // 43.1; 8192 rows of uneven adapters, 4096 x 14336, whole 127, in two 134. Backward (of dy B), 4095 x 2048 x 8192, rank
+  // 16: 58.1, 51.2, 50.0, 50.3.
   const int live = p.rt == 64 ? (m + 63) / 64 : m / 16 + groups < m ? m / 16 + groups : m;
   const int wanted = p.rt == 64 && (backward || live >= 128) ? 128 : 256;
   auto slices = [&](int width) {

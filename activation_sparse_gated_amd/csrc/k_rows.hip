@@ -9,7 +9,11 @@
 //
 // The rest is bound by HBM: every row is read and written once, 16 bytes (fp32:
 // 32) a lane, a token's rows by the same lanes, so that x (gather) and dout
-// (gradient) are read once for all of a token's slots.
+// (gradient) are read once for all of a token's slots. 4096 rows of 4096 to two
+// slots each in 8 bits 14.3 us, 4.8 TB/s; the sum of 8 slots each 56.5 us, 5.35
+// TB/s; its gradients, 4095 x 2048, two slots, 14.1 us, 6.0 TB/s, part of it from
+// the memory-side cache. The order of 8192 entries takes 7.0 us, of 16 entries
+// 2.3: one workgroup's chain of ballots and LDS accesses.
 #include "experts.cuh"
 #include "lin_util.cuh"
 
@@ -151,7 +155,7 @@ static hipError_t group_rows(const GroupDesc& d, hipStream_t s) {
   return hipGetLastError();
 }
 hipError_t launch_group_rows(const GroupDesc& d, hipStream_t s) {
-  // bits of a group's number, `groups` (none) among them
+  // bits of a group's number, `groups` (none) among them (8192 entries of 8 groups: 7.1 us; by 11 bits 10.8)
   if (d.groups < 16) return group_rows<4>(d, s);
   if (d.groups < 64) return group_rows<6>(d, s);
   if (d.groups < 512) return group_rows<9>(d, s);
@@ -203,6 +207,9 @@ static hipError_t go_gather(const RowsDesc& d, hipStream_t s) {
   else ffn_launch((k_gather<T, TPR, false>), grid, dim3(256), 0, s, d);
   return hipGetLastError();
 }
+// 4096 rows with 16, 64 and 256 threads each, us: gather of 128 columns 2.8, 3.1, 4.1, of 512 5.3, 4.1, 4.8, of 1024 9.4,
+// 6.5, 6.3; combination's gradients of 128 columns 3.0, 3.5, 5.2, of 512 6.3, 5.8, 6.9, of 1024 9.4, 8.6, 9.3. (One row of
+// 1024 is done sooner by 256.)
 template <typename T>
 static hipError_t gather(const RowsDesc& d, hipStream_t s) {
   if (d.d <= 128) return go_gather<T, 16>(d, s);
@@ -340,6 +347,7 @@ static hipError_t by_slots(const RowsDesc& d, bool fwd, hipStream_t s) {
   if (d.top_k <= 8) return go_combine<T, TPR, 8>(d, fwd, s);
   return go_combine<T, TPR, 16>(d, fwd, s);
 }
+// As gather.
 template <typename T>
 static hipError_t combine(const RowsDesc& d, bool fwd, hipStream_t s) {
   if (d.d <= 128) return by_slots<T, 16>(d, fwd, s);

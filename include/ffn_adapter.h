@@ -8,7 +8,8 @@
  * caller, 16-byte aligned, row-major dense; calls are asynchronous on `stream`,
  * check their arguments before launching anything, write nothing on an error,
  * allocate nothing, keep no state and may be captured into a graph. A call
- * without rows does nothing but what is said below, and takes null pointers.
+ * without rows does nothing but what is said below, and takes null pointers. An
+ * output shares memory with an input only where that is said.
  *
  * Rows. `offsets` (device, int32 [groups + 1]) and `rows` (device, NULL or int32
  * [m]) say which rows an adapter has: places offsets[g] .. offsets[g + 1] - 1

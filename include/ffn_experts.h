@@ -9,7 +9,8 @@
  * caller, 16-byte aligned, row-major dense; calls are asynchronous on `stream`,
  * check their arguments before launching anything, write nothing on an error,
  * allocate nothing, keep no state and may be captured into a graph. A call
- * without rows does nothing but what is said below, and takes null pointers.
+ * without rows does nothing but what is said below, and takes null pointers. An
+ * output shares memory with an input only where that is said.
  * `dtype` is ffn_dtype (FFN_F32 or FFN_BF16); sums are held in fp32 or more and
  * made in a fixed order, so results are the same from run to run. m * top_k is
  * at most 2^31 - 2^16.
@@ -51,7 +52,8 @@ int32_t ffn_experts_abi_version(void);
  *           scale * s / (the sum of the token's chosen s); without the bias
  *   scores  NULL or [m x experts] fp32: s (for losses on all of them)
  * Equal values go to the lower index (of the group, and of the expert). Where
- * scores decide they are told apart in fp64, so that the choice is that of the
+ * scores decide they are told apart in fp64 (nothing but its rounding, 2^-53 of a
+ * score or of a group's sum, can confuse them), so that the choice is that of the
  * exact scores; without a bias experts stand in the order of their logits, and
  * so do groups with group_best = 1.
  * An expert whose logit is -inf is never chosen, and a group with no other is
