@@ -208,8 +208,7 @@ static hipError_t go_gather(const RowsDesc& d, hipStream_t s) {
   return hipGetLastError();
 }
 // 4096 rows with 16, 64 and 256 threads each, us: gather of 128 columns 2.8, 3.1, 4.1, of 512 5.3, 4.1, 4.8, of 1024 9.4,
-// 6.5, 6.3; combination's gradients of 128 columns 3.0, 3.5, 5.2, of 512 6.3, 5.8, 6.9, of 1024 9.4, 8.6, 9.3. (One row of
-// 1024 is done sooner by 256.)
+// 6.5, 6.3; combination's gradients of 128 columns 3.0, 3.5, 5.2, of 512 6.3, 5.8, 6.9, of 1024 9.4, 8.6, 9.3.
 template <typename T>
 static hipError_t gather(const RowsDesc& d, hipStream_t s) {
   if (d.d <= 128) return go_gather<T, 16>(d, s);
