@@ -311,11 +311,13 @@ __global__ __launch_bounds__(256) void k_router_fwd(const RouterDesc d) {
   constexpr int TPW = 64 / LPT;
   constexpr bool EXACT16 = sizeof(T) == 2 && !SCORED;            // the integers hold value and expert whole
   __shared__ double s_key[4 * TPW * LPT * EPL];
+  __shared__ __attribute__((aligned(16))) float s_logit[4 * TPW * LPT * EPL];    // for the chosen ones: sooner there than from memory
   const int lane = lane_id(), sub = lane % LPT, wave = threadIdx.x >> 6, slot = lane / LPT;
   const long long token = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * (4 * TPW) + wave * TPW + slot;
   const bool here = token < d.m;
   const size_t t = here ? (size_t)token : (size_t)d.m - 1;      // the last token again: lanes stay together
   double* lds = s_key + (wave * TPW + slot) * LPT * EPL;
+  float* logits = s_logit + (wave * TPW + slot) * LPT * EPL;
   float l[EPL];
   float mx = -kInf;
   const size_t row = t * d.experts + sub * EPL;
@@ -343,9 +345,24 @@ __global__ __launch_bounds__(256) void k_router_fwd(const RouterDesc d) {
   }
   float bias[EPL];
   if constexpr (SCORED) {
+    if (EPL % 4 == 0 && d.bias && d.experts == LPT * EPL) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) bias[j] = d.bias && sub * EPL + j < d.experts ? d.bias[sub * EPL + j] : 0.f;
+      for (int j = 0; j < EPL; j += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(d.bias + sub * EPL + j);
+        bias[j] = v.x;
+        bias[(j + 1) % EPL] = v.y;
+        bias[(j + 2) % EPL] = v.z;
+        bias[(j + 3) % EPL] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) bias[j] = d.bias && sub * EPL + j < d.experts ? d.bias[sub * EPL + j] : 0.f;
+    }
   }
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) logits[sub * EPL + j] = l[j];
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int j = 0; j < EPL; ++j) mx = fmaxf(mx, l[j] != l[j] ? kInf : l[j]);    // a NaN as +inf: either makes every score of a softmax NaN
   mx = token_max<LPT>(mx);
@@ -472,7 +489,7 @@ __global__ __launch_bounds__(256) void k_router_fwd(const RouterDesc d) {
       // the exact values, a candidate a lane, and how many come before each
       double x = -(double)kInf;
       if (id >= 0) {
-        const float li = logit_at<T>(d.logits, t * d.experts + id);
+        const float li = logits[id];
         x = li;
         if constexpr (SCORED) {
           if (d.bias && d.sigmoid) x = 1.0 / (1.0 + exp(-(double)li)) + (double)d.bias[id];
@@ -535,7 +552,7 @@ __global__ __launch_bounds__(256) void k_router_fwd(const RouterDesc d) {
     }
   }
   const bool live = id >= 0 && sub < d.top_k;   // candidates beyond the slots fall away
-  const float w = chosen_weight<LPT>(d, live, live ? logit_at<T>(d.logits, t * d.experts + id) : 0.f, shift, inv);
+  const float w = chosen_weight<LPT>(d, live, live ? logits[id] : 0.f, shift, inv);
   if (here && sub < d.top_k) {
     d.ids[t * d.top_k + sub] = id;
     d.weights[t * d.top_k + sub] = live ? w * d.scale : 0.f;
