@@ -7,9 +7,9 @@
 // first of those who have it leaving.
 //
 // Bound by the length of that chain of dependent steps, not by its bytes: 8 of
-// 256 experts with a bias and groups, fp32, take 5.4 us for one token and 13.4
-// for 8192 (0.65 TB/s; the card copies at 5.2). The gradient, 4095 tokens of 64
-// experts: 3.7 us.
+// 256 experts with a bias and groups, fp32, take 5.3 us for one token and 10.6
+// for 8192 (0.85 TB/s; the card copies at 5.2). The gradient, 4095 tokens of 64
+// experts: 3.6 us.
 #include "experts.cuh"
 #include "lin_util.cuh"
 
@@ -305,7 +305,7 @@ __device__ __forceinline__ int token_max_i(int v) {
 // its list. Where two values lie closer than those bits and the scores' errors allow to tell, the wave orders its
 // candidates again by their exact values, each in a lane of its own; where that does not settle it (groups, many equal
 // values), it goes the long way: every score in fp64, one turn over all of them a slot. (The long way alone: 19.9 us for
-// 8192 tokens of 256 experts, 13.2 for one; so: 13.4 and 5.4.)
+// 8192 tokens of 256 experts, 13.2 for one; so: 10.6 and 5.3.)
 template <typename T, int LPT, int EPL, bool SCORED>
 __global__ __launch_bounds__(256) void k_router_fwd(const RouterDesc d) {
   constexpr int TPW = 64 / LPT;

@@ -5,22 +5,23 @@
 // order, without atomics: waves take runs of consecutive entries, a wave ranks
 // its 64 entries of a turn by ballots over the bits of their group, and counts
 // of the earlier turns, waves and blocks come in front. Up to 8192 entries are
-// one workgroup's work; more are counted by blocks of 4096 first.
+// one launch's work, of one workgroup or, with fewer than 64 groups, of one for
+// every 1024 entries; more are counted by blocks of 4096 first.
 //
 // The rest is bound by HBM: every row is read and written once, 16 bytes (fp32:
 // 32) a lane, a token's rows by the same lanes, so that x (gather) and dout
 // (gradient) are read once for all of a token's slots. 4096 rows of 4096 to two
 // slots each in 8 bits 14.3 us, 4.8 TB/s; the sum of 8 slots each 56.5 us, 5.35
 // TB/s; its gradients, 4095 x 2048, two slots, 14.1 us, 6.0 TB/s, part of it from
-// the memory-side cache. The order of 8192 entries takes 7.0 us, of 16 entries
-// 2.3: one workgroup's chain of ballots and LDS accesses.
+// the memory-side cache. The order of 8192 entries of 8 groups takes 6.0 us, of
+// 16 entries 2.3: a chain of loads, ballots and LDS accesses.
 #include "experts.cuh"
 #include "lin_util.cuh"
 
 namespace ffn {
 
 // ---------------------------------------------------------------- order by group
-constexpr int kOneBlock = 8192;                  // entries that one workgroup orders by itself (8192 of 8 groups: 7.9 us instead of 8.7 in blocks; 16384: 12.9, 8.9)
+constexpr int kOneBlock = 8192;                  // entries ordered in one launch (256 groups, 8192: 11.1 us, in blocks 11.3; 16384: 19.4, 11.7)
 constexpr int kBlock = 4096;                     // entries of a block, where there are more
 
 // The place of each of this lane's entries (entry i * 64 + lane of the wave's run) among those of its group in the run,
@@ -137,6 +138,60 @@ __global__ __launch_bounds__(NT) void k_group_rows(const GroupDesc d, int blocks
   }
 }
 
+// The same for fewer than 64 groups in one launch of several workgroups: each has 1024 entries to place and counts all the
+// others', up to 1024 CHUNKS, besides. A wave's lane g counts group g, from the same ballots. 4096 and 8192 entries of 8
+// groups 4.2 and 5.6 us, in one workgroup 5.3 and 7.9; 16384: 8.9, as in blocks.
+template <int CHUNKS, int BITS>
+__global__ __launch_bounds__(1024) void k_group_few(const GroupDesc d) {
+  constexpr int W = 16;
+  static_assert(CHUNKS * 64 < 1 << 11, "a wave's counts in bits");
+  // a wave's entries of a group: in the blocks before this one (from bit 0), in it (11), everywhere (20)
+  __shared__ uint32_t s_count[W][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, G = d.groups, own = blockIdx.x;
+  int key[CHUNKS], rank = 0, mine = 0;
+  uint32_t count = 0;
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) key[c] = d.ids[min(c * 1024 + (int)threadIdx.x, d.n - 1)];
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    const bool in = c * 1024 + (int)threadIdx.x < d.n;
+    const int k = key[c] >= 0 && key[c] < G ? key[c] : G;
+    uint64_t of_lane = ballot64(in), of_key = of_lane;           // entries of group `lane`, and of this entry's group
+    auto both = [](int v, int b) {               // bit b of v in every bit
+      const uint32_t m = (uint32_t)((int)((uint32_t)v << (31 - b)) >> 31);
+      return (uint64_t)m << 32 | m;
+    };
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) {
+      const uint64_t set = ballot64((k >> b & 1) != 0);
+      of_lane &= ~(set ^ both(lane, b));
+      if (c == own) of_key &= ~(set ^ both(k, b));
+    }
+    const uint32_t n = lane >> BITS ? 0u : (uint32_t)__popcll(of_lane);
+    count += (n << 20) + (c < own ? n : c == own ? n << 11 : 0u);
+    if (c == own) {
+      rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(of_key >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)of_key, 0u));
+      mine = k;
+    }
+  }
+  s_count[wave][lane] = count;
+  __syncthreads();
+  // every wave sums for itself: lane g the start of group g, and where this wave's entries of it go
+  int all = 0, earlier = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const uint32_t v = s_count[w][lane];
+    all += (int)(v >> 20);
+    earlier += (int)((v & 2047u) + (w < wave ? v >> 11 & 511u : 0u));
+  }
+  const int start = wave_incl_scan(all) - all;
+  if (own == 0 && wave == 0 && lane <= G) d.offsets[lane] = start;
+  const int place = __shfl(start + earlier, mine, 64) + rank, at = own * 1024 + threadIdx.x;
+  if (at >= d.n) return;
+  if (d.rows) d.rows[place] = at;
+  if (d.slots) d.slots[at] = mine == G ? -1 : place;
+}
+
 int group_rows_blocks(int n) { return n <= kOneBlock ? 1 : (n + kBlock - 1) / kBlock; }
 
 template <int BITS>
@@ -147,6 +202,11 @@ static hipError_t group_rows(const GroupDesc& d, hipStream_t s) {
     ffn_launch((k_group_rows<1024, 4, BITS, false>), dim3(blocks), dim3(1024), 0, s, d, blocks);
   } else if (d.n <= 256) {
     ffn_launch((k_group_rows<256, 1, BITS, false>), dim3(1), dim3(256), 0, s, d, 1);
+  } else if constexpr (BITS <= 6) {
+    const dim3 grid((d.n + 1023) / 1024);
+    if (d.n <= 2048) ffn_launch((k_group_few<2, BITS>), grid, dim3(1024), 0, s, d);
+    else if (d.n <= 4096) ffn_launch((k_group_few<4, BITS>), grid, dim3(1024), 0, s, d);
+    else ffn_launch((k_group_few<8, BITS>), grid, dim3(1024), 0, s, d);
   } else if (d.n <= 4096) {
     ffn_launch((k_group_rows<1024, 4, BITS, false>), dim3(1), dim3(1024), 0, s, d, 1);
   } else {
@@ -155,7 +215,7 @@ static hipError_t group_rows(const GroupDesc& d, hipStream_t s) {
   return hipGetLastError();
 }
 hipError_t launch_group_rows(const GroupDesc& d, hipStream_t s) {
-  // bits of a group's number, `groups` (none) among them (8192 entries of 8 groups: 7.1 us; by 11 bits 10.8)
+  // bits of a group's number, `groups` (none) among them (8192 entries of 8 groups in one workgroup: 7.1 us; by 11 bits 10.8)
   if (d.groups < 16) return group_rows<4>(d, s);
   if (d.groups < 64) return group_rows<6>(d, s);
   if (d.groups < 512) return group_rows<9>(d, s);
