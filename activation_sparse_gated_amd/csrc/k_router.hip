@@ -664,9 +664,9 @@ static hipError_t go(const RouterDesc& d, bool fwd, hipStream_t s) {
   else ffn_launch((k_router_fwd<T, LPT, EPL, false>), grid, dim3(256), 0, s, d);
   return hipGetLastError();
 }
-// Up to this many tokens a wave takes one token of more than 64 experts, in up to four registers a lane, the shorter way
-// through; with more of them four tokens, which leaves fewer waves to a SIMD. One token, 1024, 4096 of 256 experts: 5.9, 7.0,
-// 10.5 us one a wave, 7.7, 9.4, 9.7 four a wave; of 128 experts 5.9, 6.3, 9.6 and 6.1, 6.8, 7.7.
+// Up to this many tokens a wave takes one token of more than 128 experts, four registers a lane: the shorter way through;
+// with more of them four tokens, which leaves fewer waves to a SIMD. One token, 512, 1024, 4096 of 256 experts: 5.9, 6.1, 6.9,
+// 9.9 us one a wave, 6.3, 7.6, 7.9, 8.0 four a wave; of 128 experts 5.7, 5.9, 6.3, 9.4 and 5.4, 6.1, 6.5, 6.9.
 constexpr int kWideTokens = 1024;
 // Otherwise a token has 16 lanes (8 for as few experts), and its experts so many registers of each.
 template <typename T>
@@ -675,8 +675,8 @@ static hipError_t by_experts(const RouterDesc& d, bool fwd, hipStream_t s) {
   if (d.experts <= 16) return go<T, 16, 1>(d, fwd, s);
   if (d.experts <= 32) return go<T, 16, 2>(d, fwd, s);
   if (d.experts <= 64) return go<T, 16, 4>(d, fwd, s);
-  if (d.m <= kWideTokens && fwd) return d.experts <= 128 ? go<T, 64, 2>(d, fwd, s) : go<T, 64, 4>(d, fwd, s);
   if (d.experts <= 128) return go<T, 16, 8>(d, fwd, s);
+  if (d.m <= kWideTokens && fwd) return go<T, 64, 4>(d, fwd, s);
   return go<T, 16, 16>(d, fwd, s);
 }
 hipError_t launch_router_fwd(const RouterDesc& d, hipStream_t s) {
