@@ -33,7 +33,7 @@ struct AdapterDesc {
   // workspace (none with p.few)
   int4* tab;                     // [tiles]: adapter (-1: none, -2: no tile), first place, end
   float *h, *dh;                 // [ks or kd][tiles][rt][r]: x A^T and dy B
-  uint16_t *hp, *dhp;            // [tiles][3][rt][r]: s h (tiles of 64 rows) and s dh in bf16 numbers
+  uint16_t *hp, *dhp;            // null, or [tiles][3][rt][r]: s h (forward, tiles of 64 rows) and s dh in bf16 numbers
   uint16_t *ht, *dht;            // null, or [tiles][3][r][rt]: the same with the rows along
   float* part;                   // [slices][part]: partial gradients, if slices > 1
 };

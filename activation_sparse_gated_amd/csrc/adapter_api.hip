@@ -80,7 +80,7 @@ ffn_status ffn_adapter_forward(const void* x, const void* a, const void* b, cons
   if (!d.p.few) {
     d.tab = static_cast<int4*>(workspace);
     d.h = reinterpret_cast<float*>(static_cast<char*>(workspace) + tab_bytes(d.p));
-    d.hp = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(d.h) + h_bytes(d.p, r));
+    if (d.p.rt == 64) d.hp = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(d.h) + h_bytes(d.p, r));
   }
   return done(launch_adapter_forward(d, st(stream)));
 }

@@ -278,8 +278,27 @@ __global__ __launch_bounds__(kDownWaves * 64) void k_adapter_down(const AdapterD
   const int j0 = (blockIdx.z % chunks) * kDownRanks;
   if (z == 0 && blockIdx.z == 0 && threadIdx.x == 0) d.tab[t] = tile;
   if (tile.x < 0 || z >= (back ? d.p.kd : d.p.ks)) return;
+  // backward and whole: what k_adapter_sum would make of it
+  uint16_t* rows = back ? d.dhp : d.hp;
+  uint16_t* turned = back ? d.dht : d.ht;
+  const bool whole = (rows || turned) && (back ? d.p.kd : d.p.ks) == 1;
+  const float scale = whole && d.scales ? d.scales[tile.x] : 1.f;
+  const size_t at = (size_t)t * 3 * RT * d.r;
   float* out = (back ? d.dh : d.h) + ((size_t)z * d.p.tiles + t) * RT * d.r;
-  auto emit = [&](int row, int j, float v) { out[(size_t)row * d.r + j] = v; };
+  auto emit = [&](int row, int j, float v) {
+    if (!whole) {
+      out[(size_t)row * d.r + j] = v;
+      return;
+    }
+    v *= scale;
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      const uint32_t part = pack_bf16(v, 0.f) & 0xFFFFu;
+      if (rows && n < 2) rows[at + ((size_t)n * RT + row) * d.r + j] = (uint16_t)part;
+      if (turned) turned[at + ((size_t)n * d.r + j) * RT + row] = (uint16_t)part;
+      v = rest_of(v, part);
+    }
+  };
   if (!back) down_tile<RT, RB, true>(d, tile, z, j0, lds, emit);
   else down_tile<RT, RB, false>(d, tile, z, j0, lds, emit);
 }
@@ -492,7 +511,7 @@ __global__ __launch_bounds__(64) void k_adapter_sum(const AdapterDesc d, int wit
   const int t = blockIdx.x, which = !with_h || blockIdx.z, r4 = d.r >> 2;
   const int e = blockIdx.y * 64 + threadIdx.x, r0 = e / r4 * 4, j = (e - e / r4 * r4) * 4;
   const int g = d.tab[t].x;
-  if (g < 0 || r0 >= RT || (RT == 64 && (which ? d.p.kd : d.p.ks) == 1)) return;
+  if (g < 0 || r0 >= RT || (which ? d.p.kd : d.p.ks) == 1) return;
   const size_t at = (size_t)t * RT * d.r;
   const float* h = (which ? d.dh : d.h) + at + (size_t)r0 * d.r + j;
   uint16_t* rows = which ? d.dhp : d.hp;
@@ -501,7 +520,6 @@ __global__ __launch_bounds__(64) void k_adapter_sum(const AdapterDesc d, int wit
   const float scale = d.scales ? d.scales[g] : 1.f;
   float f[4][4];
   switch (which ? d.p.kd : d.p.ks) {
-    case 1: sum_rows<1>(d, h, slab, f, scale); break;
     case 2: sum_rows<2>(d, h, slab, f, scale); break;
     case 4: sum_rows<4>(d, h, slab, f, scale); break;
     default: sum_rows<8>(d, h, slab, f, scale);
@@ -551,8 +569,8 @@ static hipError_t launch_adapter_down(const AdapterDesc& d, hipStream_t s) {
   const hipError_t e = hipGetLastError();
   // forward with tiles of 16 rows, the second product adds the slices as it reads them: a launch less
   if (e != hipSuccess || (d.p.rt == 16 && !with_dh && !d.ht)) return e;
-  // and with tiles of 64 rows a product that is not sliced is finished by its own kernel
-  if (d.p.rt == 64 && (!with_h || d.p.ks == 1) && (!with_dh || d.p.kd == 1)) return e;
+  // and otherwise a product that is not sliced is finished by its own kernel
+  if ((!with_h || d.p.ks == 1) && (!with_dh || d.p.kd == 1)) return e;
   if (d.p.rt == 16) ffn_launch(k_adapter_sum<16>, dim3(d.p.tiles, (d.r + 63) / 64, with_h + with_dh), dim3(64), 0, s, d, with_h);
   else ffn_launch(k_adapter_sum<64>, dim3(d.p.tiles, (d.r * 4 + 63) / 64, with_h + with_dh), dim3(64), 0, s, d, with_h);
   return hipGetLastError();
@@ -1107,8 +1125,12 @@ AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) 
     while (ks < 8 && steps / (ks * 2) >= least && (live * ks < wanted || (backward && p.rt == 64 && steps / ks > 32))) ks *= 2;
     return ks;
   };
-  p.ks = slices(k);
-  p.kd = backward ? slices(n) : 1;
+  // Backward with tiles of 16 rows, whole where that is short or tiles are many, which saves the sum's launch: 2048 x 2048, 31
+  // rows, rank 16, 12.4 us in slices, 12.2 whole (with the host's time 16.1, 13.5), rank 64 19.7, 24.1; 300 rows of 100
+  // adapters 27.0, 20.7 and 65.6, 52.8.
+  const bool whole = backward && p.rt == 16 && (live >= 96 || (long long)(n > k ? n : k) * (r < 64 ? r : 64) < 65536);
+  p.ks = whole ? 1 : slices(k);
+  p.kd = backward && !whole ? slices(n) : 1;
   // Both products in one launch, with about a workgroup a CU, if there are columns for as many; where that costs less than
   // a launch: a workgroup reads its tile's operands of the first product (160 KB at most: 64 rows of 4 adapters, rank 16,
   // 4096 x 4096 take 12.8 us either way), and a tile's workgroups all read the same (30 MB at most together: 48 rows of 32
