@@ -254,9 +254,9 @@ __device__ __forceinline__ int pick(const RouterDesc& d, Key (&key)[EPL], int su
   return id;
 }
 
-// fp32 as integers of the same order, and back.
+// fp32 as integers of the same order, and back. (-0 as 0, which it is equal to: their bits are not.)
 __device__ __forceinline__ int ordered(float v) {
-  const int b = __float_as_int(v);
+  const int b = __float_as_int(v + 0.f);
   return b ^ (b >> 31 & 0x7FFFFFFF);
 }
 __device__ __forceinline__ float unordered(int o) { return __int_as_float(o ^ (o >> 31 & 0x7FFFFFFF)); }
