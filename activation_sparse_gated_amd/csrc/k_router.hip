@@ -130,6 +130,15 @@ __device__ __forceinline__ int beaten(Key v, int group, int sub, int shift) {
   }
 }
 
+// A group's value, by the two largest of its experts (-inf: none). Two biases near the lowest number sum to less than it: that
+// is held at it, since -inf marks a group without experts (equal fp32 values are settled in fp64, where no sum gets there).
+__device__ __forceinline__ float group_value(const RouterDesc& d, float a, float b) {
+  return d.group_best == 2 && b != -kInf ? fmaxf(a + b, -__FLT_MAX__) : a;
+}
+__device__ __forceinline__ double group_value(const RouterDesc& d, double a, double b) {
+  return d.group_best == 2 && b != -(double)kInf ? a + b : a;
+}
+
 // The lanes of a group, if every group is a run of 2^n whole lanes; 0 otherwise.
 template <int LPT, int EPL>
 __device__ __forceinline__ int group_lanes(const RouterDesc& d) {
@@ -149,7 +158,7 @@ __device__ __forceinline__ bool run_stays(const RouterDesc& d, Key a, Key b, int
     if (lanes > 8) merge2<8>(a, b);
     if (lanes > 16) merge2<16>(a, b);
   }
-  const Key v = d.group_best == 2 && b != none ? a + b : a;
+  const Key v = group_value(d, a, b);
   int rank = 0;                                  // groups that beat this one
   if constexpr (LPT == 64) {
     for (int g = 0; g < d.groups; ++g) {
@@ -198,7 +207,7 @@ __device__ __forceinline__ uint32_t keep_groups(const RouterDesc& d, const Key (
         a = maximum(a, v);
       }
     }
-    value[i] = d.group_best == 2 && b != none ? a + b : a;
+    value[i] = group_value(d, a, b);
   }
   __builtin_amdgcn_wave_barrier();
   uint32_t keep = 0;

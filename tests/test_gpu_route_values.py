@@ -50,3 +50,36 @@ def test_zeros_of_both_signs_are_equal(asg, shape, m, dtype):
             for best in (1, 2):
                 kw = dict(sigmoid=sigmoid, groups=groups, top_groups=top_groups, group_best=best)
                 check_route(asg, l, dtype, top_k, kw, None)
+
+
+# ---------------------------------------------------------------- biases at the ends of fp32
+LOW = float(np.finfo(np.float32).min)
+# experts, top_k, groups, groups that stay: groups through LDS, of whole lanes of 16 and of 64
+ENDS = [(8, 6, 4, 3), (64, 16, 8, 6), (60, 16, 12, 11), (256, 16, 16, 15), (250, 16, 25, 24)]
+
+
+@pytest.mark.parametrize("m", [5, 1040])
+@pytest.mark.parametrize("shape", ENDS, ids=lambda s: "x".join(map(str, s)))
+def test_groups_of_the_lowest_biases_are_groups(asg, shape, m):
+    # the sum of two such biases lies below every fp32 number, which is not to have no experts
+    experts, top_k, groups, top_groups = shape
+    say("route lowest biases", shape, m)
+    size, g = experts // groups, rng(16, m, *shape)
+    l = g.normal(0, 2, (m, experts))
+    l[1, :size] = -np.inf                               # a group that has none
+    bias = (0.1 * g.normal(0, 1, experts)).astype(np.float32)
+    ends = []
+    for n, value in ((2, LOW), (groups, LOW), (top_groups, LOW), (2, -LOW), (groups, -LOW)):
+        b = bias.copy()
+        b[experts - n * size:] = value                  # the last n groups
+        ends.append(b)
+    b = bias.copy()
+    b[-size], b[-2 * size:-size] = LOW, LOW             # one of a group's two, and both of another's
+    b[-3 * size:-2 * size] = LOW / 2                    # whose sum is the lowest number itself
+    ends.append(b)
+    ends.append(-b)
+    for b in ends:
+        for sigmoid in (False, True):
+            for best in (1, 2):
+                check_route(asg, l, "f32", top_k, dict(sigmoid=sigmoid, groups=groups, top_groups=top_groups, group_best=best), b)
+            check_route(asg, l, "f32", top_k, dict(sigmoid=sigmoid), b)
