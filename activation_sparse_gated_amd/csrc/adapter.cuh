@@ -39,6 +39,21 @@ struct AdapterDesc {
 };
 
 AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward);
+
+// The workgroups of the second half of the backward pass: those of the adapters' gradients, then those of dx. The grid may
+// hold some more, which have nothing to do.
+struct BackGrid {
+  int a, b;                      // column blocks of da and db
+  int groups, z;                 // z: rank blocks times slices
+  int x;                         // column blocks of dx (0: not asked for)
+  unsigned gx, gy;               // the grid
+  long long dw, all;             // (a + b) groups z workgroups of da and db; with those of dx
+};
+BackGrid adapter_back_grid(const AdapterPlan& p, int n, int k, int r, int groups, bool dx, bool da, bool db);
+enum BackPart : int { BACK_GRADIENTS = 0, BACK_DX = 1, BACK_NOTHING = 2 };
+__host__ __device__ __attribute__((used)) inline int adapter_back_part(const BackGrid& g, long long workgroup) {
+  return workgroup < g.dw ? BACK_GRADIENTS : workgroup < g.all ? BACK_DX : BACK_NOTHING;
+}
 // out = base + scale (x A^T) B^T
 hipError_t launch_adapter_forward(const AdapterDesc& d, hipStream_t s);
 // out = base + scale dh A, and the gradients da and db; those that are not null. d.dh is needed for out and da, d.h for db

@@ -1019,23 +1019,21 @@ __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int block, 
   }
 }
 
+// Blocks of 16 ranks that a workgroup of the gradients takes.
+constexpr int back_ranks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 // The second half of the backward pass, whose two parts read nothing of each other: workgroups of the adapters' gradients
 // (the longer ones), then those of dx. One launch lets the one's memory traffic fill the other's gaps: 4095 x 2048 x 8192,
 // rank 16, 26.4 us for 132 MB from memory (5.0 TB/s); the whole pass 53 us instead of 59.
-struct BackGrid {
-  int a, b;                      // column blocks of da and db
-  int groups, z;                 // z: rank blocks times slices
-  long long dw;                  // (a + b) groups z: workgroups of da and db
-  int x;                         // column blocks of dx
-};
 template <int RT, int F>
 __global__ __launch_bounds__(kDwWaves * 64, F == 0 ? 3 : 2) void k_adapter_back(const AdapterDesc d, const BackGrid grid) {
-  constexpr int RB = F == 0 ? 1 : F == 1 ? 2 : 4, PART = kDwWaves * 8 * 64 * 16;
+  constexpr int RB = back_ranks(F == 0 ? 16 : 32 * F), PART = kDwWaves * 8 * 64 * 16;
   using U = Up<uint16_t, RT, F, false>;
   static_assert(kDwWaves * 64 == 256, "one size of workgroup");
   __shared__ __attribute__((aligned(16))) char s_mem[PART > U::BYTES ? PART : U::BYTES];
   const long long n = (long long)blockIdx.y * gridDim.x + blockIdx.x;
-  if (n < grid.dw) {
+  const int what = adapter_back_part(grid, n);
+  if (what == BACK_NOTHING) return;
+  if (what == BACK_GRADIENTS) {
     const int block = (int)(n % (grid.a + grid.b)), rest = (int)(n / (grid.a + grid.b));
     const int g = rest % grid.groups, z = rest / grid.groups;
     const int slice = z % d.p.slices, j0 = z / d.p.slices * (16 * RB);
@@ -1046,7 +1044,6 @@ __global__ __launch_bounds__(kDwWaves * 64, F == 0 ? 3 : 2) void k_adapter_back(
   }
   const long long at = n - grid.dw;
   const int t = (int)(at / grid.x);
-  if (t >= d.p.tiles) return;
   up_tile<uint16_t, RT, F, false, 4>(d, (int)(at - (long long)t * grid.x), d.tab[t], s_mem, [&] {
     fill_made<U::PARTS * RT, 256>(d.dhp + (size_t)t * 3 * RT * d.r, d.r, s_mem);
   });
@@ -1062,28 +1059,33 @@ __global__ __launch_bounds__(256) void k_adapter_dw_sum(const AdapterDesc d, siz
   }
 }
 
-template <int RT, int F>
-static void back_ranks(const AdapterDesc& d, hipStream_t s) {
-  constexpr int RB = F == 0 ? 1 : F == 1 ? 2 : 4;
-  const int w = 128 * kDwWaves / d.p.split;      // columns of a workgroup of da and db
-  BackGrid b{};
-  b.a = d.da ? (d.k + w - 1) / w : 0;
-  b.b = d.db ? (d.n + w - 1) / w : 0;
-  b.groups = d.groups;
-  b.z = (d.r + 16 * RB - 1) / (16 * RB) * d.p.slices;
-  b.dw = (long long)(b.a + b.b) * b.groups * b.z;
-  b.x = (d.k + 511) / 512;
+BackGrid adapter_back_grid(const AdapterPlan& p, int n, int k, int r, int groups, bool dx, bool da, bool db) {
+  const int w = 128 * kDwWaves / p.split, ranks = 16 * back_ranks(r);          // columns and ranks of a workgroup of da and db
+  BackGrid b;
+  b.a = da ? (k + w - 1) / w : 0;
+  b.b = db ? (n + w - 1) / w : 0;
+  b.groups = groups;
+  b.z = (r + ranks - 1) / ranks * p.slices;
+  b.x = dx ? (k + 511) / 512 : 0;
+  b.dw = (long long)(b.a + b.b) * groups * b.z;
+  b.all = b.dw + (long long)b.x * p.tiles;
   // a grid holds fewer than 2^32 threads a dimension
-  const long long all = b.dw + (d.out ? (long long)b.x * d.p.tiles : 0), y = (all + (1 << 23) - 1) >> 23;
-  ffn_launch((k_adapter_back<RT, F>), dim3((unsigned)((all + y - 1) / y), (unsigned)y), dim3(256), 0, s, d, b);
+  b.gy = (unsigned)((b.all + (1 << 23) - 1) >> 23);
+  b.gx = (unsigned)((b.all + b.gy - 1) / b.gy);
+  return b;
+}
+template <int RT, int F>
+static void back_launch(const AdapterDesc& d, hipStream_t s) {
+  const BackGrid b = adapter_back_grid(d.p, d.n, d.k, d.r, d.groups, d.out, d.da, d.db);
+  ffn_launch((k_adapter_back<RT, F>), dim3(b.gx, b.gy), dim3(kDwWaves * 64), 0, s, d, b);
 }
 template <int RT>
 static void back(const AdapterDesc& d, hipStream_t s) {
-  if (d.r <= 16) back_ranks<RT, 0>(d, s);
-  else if (d.r <= 32) back_ranks<RT, 1>(d, s);
-  else if (d.r <= 64) back_ranks<RT, 2>(d, s);
-  else if (d.r <= 128) back_ranks<RT, 4>(d, s);
-  else back_ranks<RT, 8>(d, s);
+  if (d.r <= 16) back_launch<RT, 0>(d, s);
+  else if (d.r <= 32) back_launch<RT, 1>(d, s);
+  else if (d.r <= 64) back_launch<RT, 2>(d, s);
+  else if (d.r <= 128) back_launch<RT, 4>(d, s);
+  else back_launch<RT, 8>(d, s);
 }
 hipError_t launch_adapter_backward(const AdapterDesc& d, hipStream_t s) {
   hipError_t e = launch_adapter_down(d, s);
