@@ -17,8 +17,8 @@ import functools
 import torch
 
 from . import _lib
-from .linear import (_DTYPES, _accumulator, _again, _call, _check, _fail, _first, _nbytes, _product_out, _ptr,
-                     _workspace)
+from .linear import (_DTYPES, _accumulator, _again, _call, _check, _fail, _first, _nbytes, _no_size,
+                     _product_out, _ptr, _workspace)
 
 
 @functools.lru_cache(maxsize=256)
@@ -38,6 +38,8 @@ def _shapes(x, a, b):
     n = b.shape[1]
     _check("a", a, torch.bfloat16, (groups, r, k), dev)
     _check("b", b, torch.bfloat16, (groups, n, r), dev)
+    if (m | k | groups | r | n) >> 31:
+        _no_size("x, a, b", m, k, groups, r, n)
     return dev, m, k, groups, r, n
 
 

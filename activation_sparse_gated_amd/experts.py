@@ -18,7 +18,7 @@ import torch
 
 from . import _lib
 from .linear import (_DTYPES, FP8, Fp8Tensor, _again, _blocks, _call, _check, _check_fp8, _fail, _first, _nbytes,
-                     _ptr, _workspace)
+                     _no_size, _ptr, _workspace)
 
 _TYPES = (torch.bfloat16, torch.float32)
 
@@ -49,7 +49,10 @@ def _pairs(name, t, m, dev):
     if getattr(t, "ndim", 0) != 2:
         _fail(name, t, "int32 tensor of 2 dimensions")
     _check(name, t, torch.int32, t.shape if m is None else (m, t.shape[1]), dev)
-    return t.shape[1]
+    top_k = t.shape[1]
+    if top_k >> 31:
+        _no_size(name, top_k)
+    return top_k
 
 
 # ---------------------------------------------------------------- router
@@ -72,6 +75,10 @@ def route_forward(logits, top_k, *, score="softmax", bias=None, groups=1, top_gr
     m, experts = logits.shape
     if top_k < 1:
         raise ValueError(f"top_k: 1 at least, got {top_k}")
+    if top_groups is None:
+        top_groups = groups
+    if (top_k | groups | top_groups | group_best) >> 31:
+        _no_size("top_k, groups, top_groups, group_best", top_k, groups, top_groups, group_best)
     if bias is not None:
         _check("bias", bias, torch.float32, (experts,), dev)
     weights = _out("weights", weights, torch.float32, (m, top_k), dev)
@@ -81,7 +88,7 @@ def route_forward(logits, top_k, *, score="softmax", bias=None, groups=1, top_gr
     else:
         scores = _out("scores", None if scores is True else scores, torch.float32, (m, experts), dev)
     _call(_lib.load().ffn_route_forward, dev, logits.data_ptr(), _DTYPES[logits.dtype], m, experts, top_k,
-          _score(score), _ptr(bias), groups, groups if top_groups is None else top_groups, group_best,
+          _score(score), _ptr(bias), groups, top_groups, group_best,
           int(bool(renormalize)), float(scale), weights.data_ptr(), ids.data_ptr(), _ptr(scores))
     return weights, ids, scores
 
@@ -122,6 +129,8 @@ def group_rows(ids, groups, *, offsets=None, rows=None, slots=None, workspace=No
     n = ids.numel()
     if groups < 1:
         raise ValueError(f"groups: 1 at least, got {groups}")
+    if (n | groups) >> 31:
+        _no_size("ids, groups", n, groups)
     offsets = _out("offsets", offsets, torch.int32, (groups + 1,), dev)
     rows = _out_like("rows", rows, ids, (n,))
     slots = _out_like("slots", slots, ids, ids.shape)

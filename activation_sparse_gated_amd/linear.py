@@ -68,7 +68,14 @@ def _first(name, t, dtypes, ndims):
     """The tensor that the others are measured by."""
     if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() in ndims and t.is_cuda and t.is_contiguous()):
         _fail(name, t, f"GPU tensor of {' or '.join(map(str, ndims))} dimensions, {' or '.join(map(str, dtypes))}")
+    if t.numel() >> 31 and any(n >> 31 for n in t.shape):
+        _no_size(name, *t.shape)
     return t.device
+
+
+# The C calls take sizes as int32, and ctypes cuts a larger one off without a word: `>> 31` is 0 for what fits.
+def _no_size(name, *sizes):
+    raise ValueError(f"{name}: sizes are 0 .. 2^31 - 1, got {', '.join(map(str, sizes))}")
 
 
 def _ptr(t):
