@@ -23,7 +23,10 @@
  * Sums are held in fp32 and made in a fixed order; x A^T and dy B are kept in
  * fp32 between the two products and enter the second as the sum of two bf16
  * numbers (three where the output is fp32), which hold them to 2^-16 (2^-24) of
- * their size.
+ * their size. An infinity or a NaN makes what it enters infinite or NaN (which of
+ * the two, the parts decide: an infinite weight times a part that is 0 is NaN), and
+ * nothing else; what rows without an adapter and adapters without rows hold does
+ * not matter.
  */
 #ifndef FFN_ADAPTER_H
 #define FFN_ADAPTER_H
