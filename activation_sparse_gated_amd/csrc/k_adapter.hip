@@ -828,8 +828,8 @@ __global__ __launch_bounds__(256, F == 0 ? (RT == 16 ? 4 : 3) : F == 1 ? 3 : 2) 
 
 // Both products of a tile of 16 rows in one launch, for few rows and ranks up to 32, where a launch costs as much as the
 // work: each of d.p.few workgroups makes all of s h for its tile, and takes every d.p.few-th block of 1024 columns, the
-// first one's weights and base on their way meanwhile. 4096 x 14336, rank 16: one row 8.7 us a call instead of 12.8, 16 rows
-// of 16 adapters 11.0 instead of 12.9.
+// first one's weights and base on their way meanwhile. 4096 x 14336, rank 16, one row: 8.7 us a call instead of 12.7 in two
+// launches (in a captured graph 9.1 and 8.2); 16 rows of 16 adapters 9.2 and 12.3 (9.7 either way).
 template <typename T, int F>
 __global__ __launch_bounds__(kDownWaves * 64, 2) void k_adapter_few(const AdapterDesc d) {
   using U = Up<T, 16, F, true, kDownWaves>;
@@ -1023,7 +1023,8 @@ __device__ __forceinline__ void dw_tile(const AdapterDesc& d, int g, int block, 
 constexpr int back_ranks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 // The second half of the backward pass, whose two parts read nothing of each other: workgroups of the adapters' gradients
 // (the longer ones), then those of dx. One launch lets the one's memory traffic fill the other's gaps: 4095 x 2048 x 8192,
-// rank 16, 26.4 us for 132 MB from memory (5.0 TB/s); the whole pass 53 us instead of 59.
+// rank 16, 26.4 us for 132 MB from memory (5.0 TB/s); the whole pass 53 us instead of 59. Both read their operand for the
+// second time, of which dy, for dB, is the larger: that needs h, not dh, so it could be summed where dy is read first.
 template <int RT, int F>
 __global__ __launch_bounds__(kDwWaves * 64, F == 0 ? 3 : 2) void k_adapter_back(const AdapterDesc d, const BackGrid grid) {
   constexpr int RB = back_ranks(F == 0 ? 16 : 32 * F), PART = kDwWaves * 8 * 64 * 16;
@@ -1134,9 +1135,12 @@ AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) 
   p.ks = whole ? 1 : slices(k);
   p.kd = backward && !whole ? slices(n) : 1;
   // Both products in one launch, with about a workgroup a CU, if there are columns for as many; where that costs less than
-  // a launch: a workgroup reads its tile's operands of the first product (160 KB at most: 64 rows of 4 adapters, rank 16,
-  // 4096 x 4096 take 12.8 us either way), and a tile's workgroups all read the same (30 MB at most together: 48 rows of 32
-  // adapters, 4096 x 14336, 13.6 us instead of 12.4).
+  // a launch: a workgroup reads its tile's operands of the first product (160 KB at most: 16 rows of 16 adapters, rank 32,
+  // 4096 x 14336, 14.7 us a call instead of 12.3), and a tile's workgroups all read the same (30 MB at most together). Rank
+  // 16, one launch and two, us a call: 24 rows of 24 adapters 11.4 and 12.2, 32 of 32 11.6 and 12.2, 48 of 24 12.1 and 12.2,
+  // 48 of 30 (29 MB) 12.3 and 12.3, 48 of 32 (31 MB) 12.3 and 12.2, 64 of 64 (fewer workgroups a tile) 15.0 and 16.1: from
+  // there on neither is ahead. Without the host's time, in a captured graph: 12.1 and 11.4, 12.4 and 12.2, 12.8 and 11.5,
+  // 13.0 and 12.6, 12.9 and 12.2, 15.8 and 16.9.
   p.few = 0;
   if (!backward && p.rt == 16 && r <= 32) {
     const int blocks = (n + kDownWaves * 128 - 1) / (kDownWaves * 128);
@@ -1148,7 +1152,10 @@ AdapterPlan adapter_plan(int m, int n, int k, int r, int groups, bool backward) 
       p.ks = 1;
     }
   }
-  // waves of the adapters' gradients: two for each SIMD, if there are steps of 32 rows for as many
+  // Waves of the adapters' gradients: two for each SIMD, if there are steps of 32 rows for as many. Planned by the average
+  // adapter; where one has nearly all rows, its waves walk them one after the other: 8192 rows of 8 adapters, 4096 x 14336,
+  // rank 16, the whole pass even 146 us, all but 7 in one 257, and 169 with that one adapter alone; 4096 rows of 100
+  // adapters, 1024 x 1024, 28.6, 80.5 and 26.8.
   const int steps = (m / groups + 31) / 32;
   const long long waves = ((long long)(n + 127) / 128 + (k + 127) / 128) * groups * ((r + 63) / 64);
   p.split = 1;

@@ -192,6 +192,9 @@ __global__ __launch_bounds__(1024) void k_group_few(const GroupDesc d) {
   if (d.slots) d.slots[at] = mine == G ? -1 : place;
 }
 
+// Every block adds up the counts of all of them, which takes less than a launch between up to some hundred thousand entries
+// and grows with their square: 8, 256, 1024 groups of 2^16 entries 10.5, 13.7, 15.7 us, 2^18 17.5, 21.6, 24.5, 2^20 46, 57,
+// 63, 2^22 238, 333, 383, 2^24 (4096 blocks) 3.1, 4.8, 9.8 ms.
 int group_rows_blocks(int n) { return n <= kOneBlock ? 1 : (n + kBlock - 1) / kBlock; }
 
 template <int BITS>
