@@ -63,12 +63,13 @@ def note(msg: str) -> None:
 
 def src_hash() -> str:
     """Hash of every kernel source of the workloads here (all but those of the
-    separate operators of ffn_linear.h): stored counter readings apply only to
-    the kernels they were taken on."""
+    separate operators of ffn_linear.h, ffn_experts.h and ffn_adapter.h): stored
+    counter readings apply only to the kernels they were taken on."""
     d = os.path.join(ROOT, "activation_sparse_gated_amd", "csrc")
     h = hashlib.sha256()
     for name in sorted(os.listdir(d)):
-        if name.startswith(("k_linear", "k_rmsnorm", "k_quant", "lin_util", "linear")):
+        if name.startswith(("k_linear", "k_rmsnorm", "k_quant", "lin_util", "linear", "k_router", "k_rows", "experts",
+                            "k_adapter", "adapter")):
             continue
         with open(os.path.join(d, name), "rb") as fh:
             h.update(name.encode() + b"\0" + fh.read())
